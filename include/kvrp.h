@@ -77,6 +77,7 @@ typedef enum kvrp_status {
 
 #define KVRP_DEV_BAD_PAGE 0x1u
 #define KVRP_DEV_TIMEOUT 0x2u
+#define KVRP_DEV_BAD_LENGTH 0x4u   /* kvrp_seqs: a sequence's rows or length out of range */
 
 /* One destination pool (one tensor). */
 typedef struct kvrp_dst {
@@ -420,6 +421,133 @@ kvrp_status kv_attend_relocated(
     void* workspace, size_t workspace_bytes, uint32_t* d_status, kvrp_stream_t stream);
 
 /*
+ * Serving rows behind reused chunks.  After the chunks of a window were
+ * relocated into the paged cache (Kamera, section 3), the model goes on over
+ * that cache: new rows (a question, then one token at a time) are normed,
+ * rotated and appended, and attend over everything before them.  kv_append
+ * writes the bf16 pools of the relocation calls (one layer); kv_append_q8,
+ * kv_pack_q8 and kv_attend_q8 keep the cache in 8 bits, half the bytes that a
+ * decode step has to read.
+ *
+ * The 8-bit cache of one tensor (K or V) of one layer:
+ *   data    e4m3 (float8 e4m3fn) [num_pages][16][n_kv_heads * head_dim]: the
+ *           layout of the bf16 pools, one byte a value.
+ *   scale   fp32 [num_pages][n_kv_heads]: one for each block, the 16 tokens x
+ *           head_dim values of a (page, head).  A block stands for value * scale.
+ * The calls here write scale = 2^max(-126, ceil(log2(amax / 448))), amax over
+ * the block's finite values (a power of two: see kv_append_q8 on blocks that
+ * grow); kv_attend_q8 reads any finite scale > 0.  Values that are not finite
+ * are stored as NaN.
+ *
+ * kvrp_seqs -- a ragged batch of sequences over one paged cache.  The arrays
+ * are on the device, so a captured graph can be replayed while they change;
+ * the same kvrp_seqs serves the append and the attention of a step.
+ *   row_start     int32 [n_seqs + 1], non-decreasing from >= 0 to <= n_rows:
+ *                 sequence s owns the rows [row_start[s], row_start[s + 1]) of
+ *                 q, k, v, out.  NULL: one row per sequence (n_rows == n_seqs).
+ *   seq_lens      int32 [n_seqs]: tokens of the cache, the new rows included;
+ *                 row i of sequence s is the token at position
+ *                 seq_lens[s] - (rows of s) + i.  0 marks an idle place of the
+ *                 batch: its rows are not appended, and attention gives zeros.
+ *   block_tables  int32 [n_seqs][table_stride]: physical page of each 16
+ *                 tokens; entries past ceil(seq_lens[s] / 16) are not read.
+ *   max_rows      host bound on the rows of one sequence (0: n_rows); it only
+ *                 chooses the kernel, see kv_attend_q8.
+ * What only the device can see is OR-ed into *d_status: KVRP_DEV_BAD_LENGTH
+ * (rows out of order or range, a negative length, fewer tokens than rows, more
+ * tokens than the table has pages for): the sequence is skipped, its rows of
+ * the outputs stay as they were; KVRP_DEV_BAD_PAGE (a table entry outside
+ * [0, num_pages)): see each call.
+ */
+typedef struct kvrp_seqs {
+  const int32_t* row_start;
+  const int32_t* seq_lens;
+  const int32_t* block_tables;
+  int32_t n_seqs;
+  int32_t n_rows;
+  int32_t table_stride;
+  int32_t num_pages;
+  int32_t max_rows;
+} kvrp_seqs;
+
+/*
+ * kv_append -- the new rows of one layer into the paged bf16 cache, in one
+ * launch: per head an RMS norm of q and k (optional), the position rotation,
+ * q returned, k and v written into their slots.
+ *     q', k' = R(position) (w * x / sqrt(mean(x^2) + norm_eps)),  v' = v
+ * in fp32, rounded once to bf16.  R is rotate-half RoPE or, with mrope_section,
+ * M-RoPE; the angle position * theta^(-2i/head_dim) is formed mod 2 pi in
+ * 64-bit fixed point (error below 2^-30 turns over the int32 range of positions).
+ *   q, k, v      device bf16, row r at base + r * stride elements, heads
+ *                contiguous [n_heads][head_dim] inside a row (so a fused
+ *                projection [q | k | v] passes three pointers and one stride).
+ *                Strides 0: dense rows.  q may be NULL with q_out NULL.
+ *   q_norm, k_norm   device bf16 [head_dim] weights, both or neither.
+ *   positions    device int32 [n_rows], or [3][n_rows] (t, h, w) with
+ *                mrope_section; NULL: the cache positions (all three sections).
+ *   mrope_section  host array of 3 frequency-pair counts summing to
+ *                head_dim / 2, or NULL (plain RoPE).
+ *   q_out        device bf16 [n_rows][n_q_heads][head_dim], dense.  May be q
+ *                itself when q is dense.
+ *   k_pool, v_pool   bf16 pools [num_pages][16][n_kv_heads * head_dim] of the layer.
+ * A row whose page is bad (KVRP_DEV_BAD_PAGE) is left out of the pools; its q
+ * row is written.  n_q_heads a multiple of n_kv_heads, at most 16 x; head_dim
+ * 64 or 128.  Two sequences must not append into one page.  Pointers and row
+ * strides as everywhere: 16 bytes, multiples of 8 elements.  Asynchronous on
+ * `stream`; may be captured into a graph.
+ */
+kvrp_status kv_append(
+    const void* q, const void* k, const void* v,
+    int64_t q_stride, int64_t k_stride, int64_t v_stride, const kvrp_seqs* seqs,
+    int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+    const void* q_norm, const void* k_norm, float norm_eps,
+    double rope_theta, const int32_t* positions, const int32_t* mrope_section,
+    void* q_out, void* k_pool, void* v_pool,
+    uint32_t* d_status, kvrp_stream_t stream);
+
+/*
+ * kv_append_q8 -- kv_append into the 8-bit cache: k', v' are rounded once, from
+ * fp32 to e4m3 under their block's scale.  A block whose first slot is among
+ * the new rows starts afresh.  One that holds earlier tokens keeps the larger
+ * of its scale and the new rows'; where it grows, its earlier values are
+ * rounded again to the new scale (a shift by a power of two: exact but for
+ * values that fall among e4m3's subnormals).  Slots past the new rows keep
+ * their bytes.  Calling again with the same rows gives the same cache.
+ */
+kvrp_status kv_append_q8(
+    const void* q, const void* k, const void* v,
+    int64_t q_stride, int64_t k_stride, int64_t v_stride, const kvrp_seqs* seqs,
+    int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+    const void* q_norm, const void* k_norm, float norm_eps,
+    double rope_theta, const int32_t* positions, const int32_t* mrope_section,
+    void* q_out, void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+    uint32_t* d_status, kvrp_stream_t stream);
+
+/*
+ * kv_pack_q8 -- bf16 tokens of all layers (a chunk that a relocation call just
+ * wrote, or canonical rows) into the 8-bit cache, K and V in one launch.
+ * Logical page i (tokens 16 i ..) goes to page block_table[i]; slots of the
+ * last page past n_tokens become zero and do not count for its scale.
+ *   k_src, v_src   bf16; layer l at base + l * src_layer_stride elements (0:
+ *                  dense), as rows [n_tokens][D], or with src_table as pools
+ *                  [src_pages][16][D] read through it (D = n_kv_heads * head_dim).
+ *   k_pool, v_pool e4m3 pools, layer l at base + l * pool_layer_stride elements
+ *                  (0: num_pages * 16 * D; a multiple of 16).
+ *   k_scale, v_scale   layer l at base + l * scale_layer_stride (0: num_pages *
+ *                  n_kv_heads).
+ *   block_table    device int32 [ceil(n_tokens / 16)]; NULL: page i.
+ * A bad entry of either table sets KVRP_DEV_BAD_PAGE and skips the page.
+ */
+kvrp_status kv_pack_q8(
+    const void* k_src, const void* v_src, int64_t src_layer_stride,
+    const int32_t* src_table, int32_t src_pages,
+    int32_t n_layers, int32_t n_tokens, int32_t n_kv_heads, int32_t head_dim,
+    void* k_pool, void* v_pool, int64_t pool_layer_stride,
+    float* k_scale, float* v_scale, int64_t scale_layer_stride,
+    const int32_t* block_table, int32_t num_pages,
+    uint32_t* d_status, kvrp_stream_t stream);
+
+/*
  * kvrp_test_set_wait_limit -- for tests of the failure path only.  Sets the
  * limit, in SM clock cycles, of the relocation kernel's pipeline waits in the
  * plans built from now on by any thread (0 restores the default of about one
@@ -451,12 +579,12 @@ const char* kvrp_status_string(kvrp_status status);
 /* Text of the last error seen by this host thread (static per thread). */
 const char* kvrp_last_error(void);
 
-/* Kernel launches that this host thread's last relocation call (kv_relocate_*)
- * or attention call (kv_attend_relocated) enqueued.  Relocation: the relocation
+/* Kernel launches that this host thread's last relocation call (kv_relocate_*),
+ * attention call (kv_attend_*), append or pack enqueued.  Relocation: the relocation
  * kernel, plus for a batch the small copy launches that carry its launch plan to
  * the device (31 KB of plan each).  Attention: the block and combine kernels (2;
- * the combine alone when no chunk has tokens).  0 when the call returned an
- * error or had nothing to move. */
+ * the combine alone when no chunk has tokens).  Append and pack: 1.  0 when the
+ * call returned an error or had nothing to move. */
 int32_t kvrp_last_launch_count(void);
 
 /* Library version, major * 10000 + minor * 100 + patch. */

@@ -17,12 +17,14 @@ KVRP_ERR_CUDA = 4
 KVRP_ERR_WORKSPACE = 5
 KVRP_DEV_BAD_PAGE = 0x1
 KVRP_DEV_TIMEOUT = 0x2
+KVRP_DEV_BAD_LENGTH = 0x4
 
 EXPORTED_SYMBOLS = (
     "kv_relocate_patch", "kv_relocate_patch_mrope", "kv_relocate_patch_mla", "kv_relocate_batch",
     "kv_relocate_batch_workspace_size", "kv_relocate_batch_noalloc", "kv_relocate_batch_mrope",
     "kv_relocate_batch_mla", "kvrp_test_set_wait_limit", "kvrp_test_attend_split", "kv_patch_form_workspace_size",
     "kv_patch_form", "kv_patch_form_orbit", "kv_attend_relocated_workspace_size", "kv_attend_relocated",
+    "kv_append", "kv_append_q8", "kv_pack_q8",
     "kvrp_status_string",
     "kvrp_last_error", "kvrp_last_launch_count", "kvrp_version",
 )
@@ -58,6 +60,12 @@ class kvrp_mla_chunk(C.Structure):
     _fields_ = [("src", C.c_void_p), ("src_layer_stride", C.c_int64), ("n_tokens", C.c_int32),
                 ("rank", C.c_int32), ("delta", C.c_int64), ("u", C.c_void_p), ("v", C.c_void_p),
                 ("u_layer_stride", C.c_int64), ("v_layer_stride", C.c_int64), ("dst", kvrp_dst)]
+
+
+class kvrp_seqs(C.Structure):
+    _fields_ = [("row_start", C.c_void_p), ("seq_lens", C.c_void_p), ("block_tables", C.c_void_p),
+                ("n_seqs", C.c_int32), ("n_rows", C.c_int32), ("table_stride", C.c_int32),
+                ("num_pages", C.c_int32), ("max_rows", C.c_int32)]
 
 
 def _load_library():
@@ -124,6 +132,19 @@ def _load_library():
     L.kv_attend_relocated.argtypes = [
         C.c_void_p, C.POINTER(kvrp_attn_chunk), C.c_int32, C.POINTER(C.c_int32), C.c_int32, C.c_int32, C.c_int32,
         C.c_int32, C.c_double, C.c_float, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]
+    append_args = [
+        C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.POINTER(kvrp_seqs), C.c_int32, C.c_int32,
+        C.c_int32, C.c_void_p, C.c_void_p, C.c_float, C.c_double, C.c_void_p, C.POINTER(C.c_int32), C.c_void_p,
+        C.c_void_p, C.c_void_p]
+    L.kv_append.restype = st
+    L.kv_append.argtypes = append_args + [C.c_void_p, C.c_void_p]
+    L.kv_append_q8.restype = st
+    L.kv_append_q8.argtypes = append_args + [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]
+    L.kv_pack_q8.restype = st
+    L.kv_pack_q8.argtypes = [
+        C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
+        C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int32, C.c_void_p,
+        C.c_void_p]
     L.kvrp_status_string.restype = C.c_char_p
     L.kvrp_status_string.argtypes = [C.c_int]
     L.kvrp_last_error.restype = C.c_char_p
@@ -169,17 +190,31 @@ def kvrp_version() -> int:
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
-    return int(x.data_ptr())
+    return x.data_ptr()
+
+
+def _find_current_stream():
+    """torch's current stream as an address.  The raw getter costs 0.2 us a call where
+    building a Stream object costs 3 us, as much as the rest of a call's marshalling."""
+    import torch
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None or not torch.cuda.is_available():
+        return lambda: int(torch.cuda.current_stream().cuda_stream)
+    torch.cuda.current_stream()   # initialises CUDA as the public call does
+    return lambda: raw(device())
+
+
+def _current_stream() -> int:
+    global _current_stream
+    _current_stream = _find_current_stream()
+    return _current_stream()
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -473,3 +508,72 @@ def kv_attend_relocated(q, chunks, seq_chunks, *, n_q_heads: int, n_kv_heads: in
     _check(lib().kv_attend_relocated(
         _ptr(q), arr, n, sc, len(seq_chunks) - 1, int(n_q_heads), int(n_kv_heads), int(head_dim), float(rope_theta),
         float(softmax_scale), _ptr(out), _ptr(workspace), int(workspace_bytes), _ptr(d_status), _stream(stream)))
+
+
+class Seqs:
+    """A ragged batch over one paged cache (fields as in struct kvrp_seqs): device
+    int32 tensors seq_lens [n_seqs], block_tables [n_seqs][table_stride] and, unless
+    every sequence has one row, row_start [n_seqs + 1].  Build it once and pass it to
+    every append and attention call of the steps that use these arrays: the arrays'
+    contents may change in between, their sizes may not."""
+
+    def __init__(self, seq_lens, block_tables, num_pages: int, n_rows: Optional[int] = None, row_start=None,
+                 max_rows: int = 0):
+        n_seqs, table_stride = int(block_tables.shape[0]), int(block_tables.shape[1])
+        for name, t, n in (("seq_lens", seq_lens, n_seqs), ("block_tables", block_tables, n_seqs * table_stride),
+                           ("row_start", row_start, n_seqs + 1)):
+            if t is not None and (t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous() or t.numel() != n):
+                raise ValueError(f"{name}: a contiguous int32 tensor of {n} entries is needed")
+        if n_rows is None:
+            if row_start is not None:
+                raise ValueError("n_rows is needed with row_start")
+            n_rows = n_seqs
+        self.arrays = (seq_lens, block_tables, row_start)   # keeps the device memory alive
+        self.c = kvrp_seqs(_ptr(row_start), _ptr(seq_lens), _ptr(block_tables), n_seqs, int(n_rows), table_stride,
+                           int(num_pages), int(max_rows))
+        self.ref = C.byref(self.c)
+
+
+_SECTIONS = {}
+
+
+def _sections(mrope_section):
+    if mrope_section is None:
+        return None
+    key = tuple(int(v) for v in mrope_section)
+    if len(key) != 3:
+        raise ValueError("mrope_section: three counts")
+    if key not in _SECTIONS:
+        _SECTIONS[key] = (C.c_int32 * 3)(*key)
+    return _SECTIONS[key]
+
+
+def kv_append(q, k, v, seqs: Seqs, *, n_q_heads: int, n_kv_heads: int, head_dim: int, rope_theta: float, k_pool, v_pool,
+              q_out=None, positions=None, mrope_section=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6,
+              q_stride: int = 0, k_stride: int = 0, v_stride: int = 0, d_status=None, stream=None) -> None:
+    """New rows into the paged bf16 cache: per-head RMS norm (optional), rotation, append; q returned in q_out."""
+    _check(lib().kv_append(
+        _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride, seqs.ref, n_q_heads, n_kv_heads, head_dim, _ptr(q_norm),
+        _ptr(k_norm), norm_eps, rope_theta, _ptr(positions), _sections(mrope_section), _ptr(q_out), _ptr(k_pool),
+        _ptr(v_pool), _ptr(d_status), _stream(stream)))
+
+
+def kv_append_q8(q, k, v, seqs: Seqs, *, n_q_heads: int, n_kv_heads: int, head_dim: int, rope_theta: float, k_pool, v_pool,
+                 k_scale, v_scale, q_out=None, positions=None, mrope_section=None, q_norm=None, k_norm=None,
+                 norm_eps: float = 1e-6, q_stride: int = 0, k_stride: int = 0, v_stride: int = 0, d_status=None,
+                 stream=None) -> None:
+    """kv_append into the 8-bit cache (e4m3 pools, one fp32 scale for each page and head)."""
+    _check(lib().kv_append_q8(
+        _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride, seqs.ref, n_q_heads, n_kv_heads, head_dim, _ptr(q_norm),
+        _ptr(k_norm), norm_eps, rope_theta, _ptr(positions), _sections(mrope_section), _ptr(q_out), _ptr(k_pool),
+        _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(d_status), _stream(stream)))
+
+
+def kv_pack_q8(k_src, v_src, *, n_layers: int, n_tokens: int, n_kv_heads: int, head_dim: int, k_pool, v_pool, k_scale,
+               v_scale, num_pages: int, block_table=None, src_table=None, src_pages: int = 0, src_layer_stride: int = 0,
+               pool_layer_stride: int = 0, scale_layer_stride: int = 0, d_status=None, stream=None) -> None:
+    """bf16 tokens of all layers (rows, or pools read through src_table) into the 8-bit cache."""
+    _check(lib().kv_pack_q8(
+        _ptr(k_src), _ptr(v_src), src_layer_stride, _ptr(src_table), src_pages, n_layers, n_tokens, n_kv_heads, head_dim,
+        _ptr(k_pool), _ptr(v_pool), pool_layer_stride, _ptr(k_scale), _ptr(v_scale), scale_layer_stride, _ptr(block_table),
+        num_pages, _ptr(d_status), _stream(stream)))
