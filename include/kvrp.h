@@ -548,6 +548,40 @@ kvrp_status kv_pack_q8(
     uint32_t* d_status, kvrp_stream_t stream);
 
 /*
+ * kv_attend_q8 -- attention of the new rows over the 8-bit cache of one layer:
+ *     out[r][j] = softmax(softmax_scale * q[r][j] . K) V
+ * over the tokens 0 .. position of row r (causal: the rows of a sequence are
+ * its last tokens, appended before this call), query head j reading KV head
+ * j / (n_q_heads / n_kv_heads).  One row a sequence is a decode step, a few are
+ * a draft's verification, many a prompt behind reused chunks.
+ *   q            device bf16, row r at q + r * q_stride elements (0: dense),
+ *                [n_q_heads][head_dim] inside a row, rotated (kv_append_q8's q_out).
+ *   k_pool, v_pool, k_scale, v_scale   the cache; only read.
+ *   out          device bf16 [n_rows][n_q_heads][head_dim], dense.
+ *   lse          optional device fp32 [n_rows][n_q_heads]: the natural log of the
+ *                sum of exp(score), with which partial results over disjoint
+ *                token sets are merged.
+ *   workspace    device scratch of kv_attend_q8_workspace_size(...) bytes; its
+ *                contents need not survive between calls; calls that can overlap
+ *                need one each.  max_rows is kvrp_seqs.max_rows (1 without row_start).
+ * An idle sequence (length 0) gets zeros and a log-sum-exp of -inf.  A sequence
+ * with a bad length, or more rows than max_rows, is flagged and its rows are left as
+ * they were.  A bad table entry sets KVRP_DEV_BAD_PAGE and reads as a page of
+ * zeros.  Slots past a sequence's length are never used, whatever they hold.
+ * The output does not depend on how the work is split over the GPU beyond fp32
+ * rounding, and the same call gives the same bits.  Asynchronous on `stream`; may
+ * be captured into a graph and replayed as lengths and tables change.
+ */
+size_t kv_attend_q8_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_rows);
+
+kvrp_status kv_attend_q8(
+    const void* q, int64_t q_stride, const kvrp_seqs* seqs,
+    int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, float softmax_scale,
+    const void* k_pool, const void* v_pool, const float* k_scale, const float* v_scale,
+    void* out, float* lse, void* workspace, size_t workspace_bytes,
+    uint32_t* d_status, kvrp_stream_t stream);
+
+/*
  * kvrp_test_set_wait_limit -- for tests of the failure path only.  Sets the
  * limit, in SM clock cycles, of the relocation kernel's pipeline waits in the
  * plans built from now on by any thread (0 restores the default of about one

@@ -17,6 +17,7 @@ CUDA kernel.  Names mirror the C ABI in include/kvrp.h:
     kv_append                new rows into the paged bf16 cache: q/k norms, rotation, append
     kv_append_q8             the same into the 8-bit cache (e4m3, a scale for each page and head)
     kv_pack_q8               bf16 pages (a relocated chunk) into the 8-bit cache
+    kv_attend_q8             causal attention of the new rows over the 8-bit cache
 
 Tensors may be passed as torch CUDA tensors (their data_ptr is used) or as raw
 device addresses (int).  Streams default to torch's current stream.  A status
@@ -37,5 +38,5 @@ from ._abi import (  # noqa: F401
     kv_patch_form, kv_patch_form_orbit, kv_patch_form_workspace_size,
     kv_attend_relocated, kv_attend_relocated_workspace_size, AttnChunk, attn_chunk_array, KVRP_ATTN_MAX_CHUNKS,
     KVRP_ROPE_NONE, KVRP_ROPE_HEADS, KVRP_ROPE_MLA_TAIL,
-    Seqs, kv_append, kv_append_q8, kv_pack_q8,
+    Seqs, kv_append, kv_append_q8, kv_pack_q8, kv_attend_q8, kv_attend_q8_workspace_size,
 )

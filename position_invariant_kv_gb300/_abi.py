@@ -24,7 +24,7 @@ EXPORTED_SYMBOLS = (
     "kv_relocate_batch_workspace_size", "kv_relocate_batch_noalloc", "kv_relocate_batch_mrope",
     "kv_relocate_batch_mla", "kvrp_test_set_wait_limit", "kvrp_test_attend_split", "kv_patch_form_workspace_size",
     "kv_patch_form", "kv_patch_form_orbit", "kv_attend_relocated_workspace_size", "kv_attend_relocated",
-    "kv_append", "kv_append_q8", "kv_pack_q8",
+    "kv_append", "kv_append_q8", "kv_pack_q8", "kv_attend_q8_workspace_size", "kv_attend_q8",
     "kvrp_status_string",
     "kvrp_last_error", "kvrp_last_launch_count", "kvrp_version",
 )
@@ -145,6 +145,12 @@ def _load_library():
         C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
         C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int32, C.c_void_p,
         C.c_void_p]
+    L.kv_attend_q8_workspace_size.restype = C.c_size_t
+    L.kv_attend_q8_workspace_size.argtypes = [C.c_int32] * 4
+    L.kv_attend_q8.restype = st
+    L.kv_attend_q8.argtypes = [
+        C.c_void_p, C.c_int64, C.POINTER(kvrp_seqs), C.c_int32, C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_void_p,
+        C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]
     L.kvrp_status_string.restype = C.c_char_p
     L.kvrp_status_string.argtypes = [C.c_int]
     L.kvrp_last_error.restype = C.c_char_p
@@ -577,3 +583,20 @@ def kv_pack_q8(k_src, v_src, *, n_layers: int, n_tokens: int, n_kv_heads: int, h
         _ptr(k_src), _ptr(v_src), src_layer_stride, _ptr(src_table), src_pages, n_layers, n_tokens, n_kv_heads, head_dim,
         _ptr(k_pool), _ptr(v_pool), pool_layer_stride, _ptr(k_scale), _ptr(v_scale), scale_layer_stride, _ptr(block_table),
         num_pages, _ptr(d_status), _stream(stream)))
+
+
+def kv_attend_q8_workspace_size(n_q_heads: int, n_kv_heads: int, head_dim: int, max_rows: int = 1) -> int:
+    """Scratch bytes of kv_attend_q8 (depends on the current device's SM count)."""
+    return int(lib().kv_attend_q8_workspace_size(int(n_q_heads), int(n_kv_heads), int(head_dim), int(max_rows)))
+
+
+def kv_attend_q8(q, seqs: Seqs, *, n_q_heads: int, n_kv_heads: int, head_dim: int, softmax_scale: float, k_pool, v_pool,
+                 k_scale, v_scale, out, workspace, lse=None, q_stride: int = 0, workspace_bytes: Optional[int] = None,
+                 d_status=None, stream=None) -> None:
+    """Causal attention of the new rows over the 8-bit cache (one row a sequence, or many)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().kv_attend_q8(
+        _ptr(q), q_stride, seqs.ref, n_q_heads, n_kv_heads, head_dim, softmax_scale, _ptr(k_pool), _ptr(v_pool),
+        _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes, _ptr(d_status),
+        _stream(stream)))

@@ -36,7 +36,9 @@ namespace kvrp {
 namespace append {
 
 using namespace kvrp::ptx;
+using q8::flag;
 using q8::kPage;
+using q8::sequence;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
@@ -58,27 +60,10 @@ struct Params {
   uint64_t turn[64];      // theta^(-2i/d) / (2 pi), in units of 2^-64 turns
 };
 
-__device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) {
-  if (status) atomicOr(status, bit);
-}
-
 // One run: rows [row0, row0 + n) are the tokens at positions pos0 .. of sequence seq.
 struct Run {
   int seq, row0, n, pos0;
 };
-
-// The rows and length of sequence s; false (and rows 0) where they are out of range.
-// A sequence of length 0 is an idle place of the batch: no rows, and nothing wrong.
-__device__ __forceinline__ bool sequence(const kvrp_seqs& q, int s, int& row0, int& rows, int& len) {
-  row0 = q.row_start ? q.row_start[s] : s;
-  const int end = q.row_start ? q.row_start[s + 1] : s + 1;
-  len = q.seq_lens[s];
-  rows = end - row0;
-  const bool ok = row0 >= 0 && end >= row0 && end <= q.n_rows && len >= rows &&
-                  (int64_t)len <= (int64_t)q.table_stride * kPage;
-  if (!ok || len == 0) rows = 0;
-  return ok || len == 0;
-}
 
 // Run number `want` of the batch.  With one row per sequence that is sequence `want`;
 // else the CTA scans the sequences' run counts, 256 at a time.

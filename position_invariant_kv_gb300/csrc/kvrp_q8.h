@@ -9,6 +9,7 @@
 // moved to a larger scale by a shift, which is exact down to e4m3's subnormals instead
 // of one more rounding of every value.  A value that is not finite is stored as NaN.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -18,6 +19,24 @@ namespace kvrp {
 namespace q8 {
 
 constexpr int kPage = 16;   // tokens per page (and per block)
+
+#ifdef __CUDACC__
+
+__device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) {
+  if (status) atomicOr(status, bit);
+}
+// The rows and length of sequence s; false (and rows 0) where they are out of range.
+// A sequence of length 0 is an idle place of the batch: no rows, and nothing wrong.
+__device__ __forceinline__ bool sequence(const kvrp_seqs& q, int s, int& row0, int& rows, int& len) {
+  row0 = q.row_start ? q.row_start[s] : s;
+  const int end = q.row_start ? q.row_start[s + 1] : s + 1;
+  len = q.seq_lens[s];
+  rows = end - row0;
+  const bool ok = row0 >= 0 && end >= row0 && end <= q.n_rows && len >= rows &&
+                  (int64_t)len <= (int64_t)q.table_stride * kPage;
+  if (!ok || len == 0) rows = 0;
+  return ok || len == 0;
+}
 
 // The scale of a block whose largest finite magnitude is amax: the exponent of the
 // least power of two s with amax <= 448 s = 1.75 * 2^8 s, read off amax's own bits.
@@ -44,7 +63,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
   return r;
 }
 
+#endif  // __CUDACC__
+
 }  // namespace q8
+
+// Tensor map of an 8-bit pool [num_pages][16][row_bytes] whose box is one head of one page:
+// head_dim bytes (128- or 64-byte swizzle) of its 16 slots.  Coordinates (head * head_dim, 0, page).
+kvrp_status encode_q8_pool(CUtensorMap* map, const void* pool, int num_pages, int row_bytes, int head_dim);
 
 // Host checks that the entry points over a ragged batch (kvrp_seqs) share.
 kvrp_status check_seqs(const char* fn, const kvrp_seqs* s);

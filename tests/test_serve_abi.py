@@ -106,6 +106,38 @@ def test_pack_refusals(kvrp):
         assert st() == kvrp.KVRP_ERR_CUDA
 
 
+def test_attend_q8_refusals(kvrp):
+    inv, ali, uns = kvrp.KVRP_ERR_INVALID_ARG, kvrp.KVRP_ERR_ALIGNMENT, kvrp.KVRP_ERR_UNSUPPORTED
+
+    def st(seqs=None, **over):
+        args = dict(q=0x10000, n_q_heads=8, n_kv_heads=2, head_dim=128, softmax_scale=0.1, k_pool=0x20000, v_pool=0x30000,
+                    k_scale=0x40000, v_scale=0x50000, out=0x60000, lse=0x70000, workspace=0x100000, workspace_bytes=1 << 40,
+                    stream=0)
+        args.update(over)
+        q = args.pop("q")
+        with pytest.raises(kvrp.KvrpError) as e:
+            kvrp.kv_attend_q8(q, seqs or _Seqs(kvrp, max_rows=2), **args)
+        assert kvrp.kvrp_last_launch_count() == 0
+        return e.value.status
+
+    for over, code in BAD_SEQS:
+        assert st(seqs=_Seqs(kvrp, **over)) == getattr(kvrp, "KVRP_ERR_" + code), over
+    assert st(q=None) == inv and st(out=None) == inv and st(k_scale=None) == inv and st(v_pool=None) == inv
+    assert st(softmax_scale=0.0) == inv and st(softmax_scale=-1.0) == inv and st(softmax_scale=float("nan")) == inv
+    assert st(head_dim=256) == uns and st(n_q_heads=7) == uns and st(n_q_heads=34) == uns
+    assert st(q_stride=1016) == inv and st(q_stride=1028) == ali
+    assert st(q=0x10008) == ali and st(k_pool=0x20008) == ali and st(out=0x60004) == ali and st(lse=0x70002) == ali
+    assert st(v_scale=0x50001) == ali
+    assert st(workspace=None) == kvrp.KVRP_ERR_WORKSPACE and st(workspace_bytes=1024) == kvrp.KVRP_ERR_WORKSPACE
+    assert kvrp.kv_attend_q8_workspace_size(8, 3, 128, 1) == 0 and kvrp.kv_attend_q8_workspace_size(8, 2, 96, 1) == 0
+    assert kvrp.kv_attend_q8_workspace_size(8, 2, 128, 0) == 0
+    need = kvrp.kv_attend_q8_workspace_size(8, 2, 128, 2)
+    assert need > 0
+    import torch
+    if not torch.cuda.is_available():
+        assert st(workspace_bytes=need) == kvrp.KVRP_ERR_CUDA
+
+
 def test_seqs_object_checks(kvrp):
     import torch
     lens, table = torch.zeros(3, dtype=torch.int32), torch.zeros((3, 4), dtype=torch.int32)
