@@ -45,35 +45,11 @@
 #include "kvrp_plan.h"
 #include "kvrp_ptx.h"
 #include "kvrp_q8.h"
+#include "kvrp_attend_q8.h"
 
 namespace kvrp {
 namespace attend_q8 {
 
-using namespace kvrp::ptx;
-using q8::flag;
-using q8::kPage;
-using q8::sequence;
-
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kShift = 7.f;       // weights of the accumulator are exp2(. + 7)
-constexpr float kLazy = 8.f;        // how far a score may pass the running maximum
-constexpr int kMaxCtasPerSm = 2;
-constexpr int kMaxCols = 16;        // rows x group of the decode kernel
-
-struct Params {
-  const uint16_t* q;
-  int64_t q_stride;
-  uint16_t* out;
-  float* lse;
-  const float *k_scale, *v_scale;
-  kvrp_seqs seqs;
-  uint32_t* status;
-  float* partial;       // [n_cta][2][cols][D + 4]: O, then max, accumulator max, sum
-  int4* meta;           // [n_cta]: x, y = sequence and head whose first part this CTA holds (x < 0: none),
-                        //          z = 0 no part of a unit begun before, 1 a middle part, 2 the last part
-  int Hq, Hkv, g, n_cta, cols, max_rows;
-  float scale;          // softmax_scale * log2(e)
-};
 
 // ---- shares ---------------------------------------------------------------------------
 struct Seq {
@@ -170,37 +146,6 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// Bounded wait that ignores the abort flag: lets this CTA's own copies land before it exits.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint32_t* status) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kTimeoutCycles) {
-      if (status) atomicOr(status, KVRP_DEV_TIMEOUT);
-      return;
-    }
-  }
-}
-
-__device__ __forceinline__ void write_idle(const Params& p, int D) {
-  // idle places of the batch (length 0): zeros, and no tokens' log-sum-exp
-  for (int s = blockIdx.x; s < p.seqs.n_seqs; s += gridDim.x) {
-    int row0, rows, len;
-    if (!sequence(p.seqs, s, row0, rows, len) || len != 0) continue;
-    const int end = p.seqs.row_start ? p.seqs.row_start[s + 1] : s + 1;
-    if (row0 < 0 || end > p.seqs.n_rows) {
-      if (threadIdx.x == 0) flag(p.status, KVRP_DEV_BAD_LENGTH);
-      continue;
-    }
-    for (int64_t i = (int64_t)row0 * p.Hq * D + threadIdx.x * 8; i < (int64_t)end * p.Hq * D; i += blockDim.x * 8)
-      *reinterpret_cast<uint4*>(p.out + i) = make_uint4(0, 0, 0, 0);
-    if (p.lse)
-      for (int64_t i = (int64_t)row0 * p.Hq + threadIdx.x; i < (int64_t)end * p.Hq; i += blockDim.x) p.lse[i] = -INFINITY;
-  }
-}
-
 // ---- decode ----------------------------------------------------------------------------
 constexpr int kWarps = 8;
 template <int D, int NT>
@@ -657,14 +602,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
   if (p.lse && f == 0) p.lse[row] = (m + lg2(l)) * kLn2;
 }
 
-int cta_bound() {
+int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       n <= 0) {
     cudaGetLastError();
     n = 160;   // no device: a size for the checks of a host without one
   }
-  return kMaxCtasPerSm * n;
+  return n;
 }
 
 size_t meta_bytes(int n_cta) { return ((size_t)n_cta * sizeof(int4) + 255) / 256 * 256; }
@@ -681,7 +626,9 @@ extern "C" {
 
 size_t kv_attend_q8_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_rows) {
   if (check_heads("kv_attend_q8_workspace_size", n_q_heads, n_kv_heads, head_dim) != KVRP_OK || max_rows <= 0) return 0;
-  return attend_q8::workspace_bytes(attend_q8::cta_bound(), attend_q8::kMaxCols, head_dim);
+  const bool few = (int64_t)max_rows * (n_q_heads / n_kv_heads) <= attend_q8::kMaxCols;
+  return few ? attend_q8::workspace_bytes(attend_q8::kMaxCtasPerSm * attend_q8::sm_count(), attend_q8::kMaxCols, head_dim)
+             : attend_q8::workspace_bytes(attend_q8::sm_count(), attend_q8::kPromptRows, head_dim);
 }
 
 kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs, int32_t n_q_heads, int32_t n_kv_heads,
@@ -708,8 +655,9 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   const int max_rows = !seqs->row_start ? 1 : seqs->max_rows ? seqs->max_rows : seqs->n_rows;
   const size_t need = kv_attend_q8_workspace_size(n_q_heads, n_kv_heads, head_dim, max_rows);
   if (!workspace || workspace_bytes < need) return fail(KVRP_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
-  const int g = n_q_heads / n_kv_heads, cols = max_rows * g;
-  if (cols > attend_q8::kMaxCols) return fail(KVRP_ERR_UNSUPPORTED, "%s: rows x group above %d", fn, attend_q8::kMaxCols);
+  const int g = n_q_heads / n_kv_heads;
+  const bool few = (int64_t)max_rows * g <= attend_q8::kMaxCols;
+  const int cols = few ? max_rows * g : attend_q8::kPromptRows;
   int sms = 0, smem_optin = 0;
   st = current_device_sms(&sms, &smem_optin);
   if (st != KVRP_OK) return st;
@@ -727,8 +675,8 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   p.Hq = n_q_heads;
   p.Hkv = n_kv_heads;
   p.g = g;
-  p.n_cta = attend_q8::kMaxCtasPerSm * sms;
-  p.cols = attend_q8::kMaxCols;
+  p.n_cta = few ? attend_q8::kMaxCtasPerSm * sms : sms;
+  p.cols = few ? attend_q8::kMaxCols : attend_q8::kPromptRows;
   p.max_rows = max_rows;
   p.scale = softmax_scale * 1.4426950408889634f;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
@@ -739,6 +687,12 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   if (st == KVRP_OK) st = encode_q8_pool(&vmap, v_pool, seqs->num_pages, n_kv_heads * head_dim, head_dim);
   if (st != KVRP_OK) return st;
 
+  if (!few) {
+    const cudaError_t e = attend_q8::launch_prompt(kmap, vmap, p, head_dim, stream);
+    if (e != cudaSuccess) return fail(KVRP_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    g_last_launches = 2;
+    return KVRP_OK;
+  }
   const bool two = cols > 8;
   auto kernel = head_dim == 64 ? (two ? attend_q8::decode_kernel<64, 2> : attend_q8::decode_kernel<64, 1>)
                                : (two ? attend_q8::decode_kernel<128, 2> : attend_q8::decode_kernel<128, 1>);

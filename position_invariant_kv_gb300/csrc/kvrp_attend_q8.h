@@ -1,0 +1,83 @@
+// What the two attention kernels over the 8-bit cache share: few rows a sequence
+// (kvrp_attend_q8.cu) and many (kvrp_attend_q8_prompt.cu).
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kvrp.h"
+#include "kvrp_ptx.h"
+#include "kvrp_q8.h"
+
+namespace kvrp {
+namespace attend_q8 {
+
+using namespace kvrp::ptx;
+using q8::flag;
+using q8::kPage;
+using q8::sequence;
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kShift = 7.f;       // weights of the accumulator are exp2(. + 7)
+constexpr float kLazy = 8.f;        // how far a score may pass the running maximum
+constexpr int kMaxCtasPerSm = 2;
+constexpr int kMaxCols = 16;        // rows x group of the decode kernel
+
+struct Params {
+  const uint16_t* q;
+  int64_t q_stride;
+  uint16_t* out;
+  float* lse;
+  const float *k_scale, *v_scale;
+  kvrp_seqs seqs;
+  uint32_t* status;
+  float* partial;       // [n_cta][2][cols][D + 4]: O, then max, accumulator max, sum
+  int4* meta;           // [n_cta]: x, y = sequence and head whose first part this CTA holds (x < 0: none),
+                        //          z = 0 no part of a unit begun before, 1 a middle part, 2 the last part
+  int Hq, Hkv, g, n_cta, cols, max_rows;
+  float scale;          // softmax_scale * log2(e)
+};
+
+// The kernel for many rows: its columns (rows a partial result holds) and its launch,
+// p.n_cta blocks.
+constexpr int kPromptRows = 256;
+cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap, const Params& p, int head_dim, cudaStream_t stream);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Bounded wait that ignores the abort flag: lets this CTA's own copies land before it exits.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint32_t* status) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kTimeoutCycles) {
+      if (status) atomicOr(status, KVRP_DEV_TIMEOUT);
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ void write_idle(const Params& p, int D) {
+  // idle places of the batch (length 0): zeros, and no tokens' log-sum-exp
+  for (int s = blockIdx.x; s < p.seqs.n_seqs; s += gridDim.x) {
+    int row0, rows, len;
+    if (!sequence(p.seqs, s, row0, rows, len) || len != 0) continue;
+    const int end = p.seqs.row_start ? p.seqs.row_start[s + 1] : s + 1;
+    if (row0 < 0 || end > p.seqs.n_rows) {
+      if (threadIdx.x == 0) flag(p.status, KVRP_DEV_BAD_LENGTH);
+      continue;
+    }
+    for (int64_t i = (int64_t)row0 * p.Hq * D + threadIdx.x * 8; i < (int64_t)end * p.Hq * D; i += blockDim.x * 8)
+      *reinterpret_cast<uint4*>(p.out + i) = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (int64_t i = (int64_t)row0 * p.Hq + threadIdx.x; i < (int64_t)end * p.Hq; i += blockDim.x) p.lse[i] = -INFINITY;
+  }
+}
+
+#endif  // __CUDACC__
+
+}  // namespace attend_q8
+}  // namespace kvrp

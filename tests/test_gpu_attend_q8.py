@@ -138,6 +138,71 @@ def test_few_rows(name):
     assert torch.equal(first[0], c.out) and torch.equal(first[1], c.lse)     # the same bits again
 
 
+PROMPT = {
+    "one_tile": dict(ctx=[0], rows=[30], hq=4, hkv=2, d=128, max_rows=30),
+    "one_tile_d64": dict(ctx=[5], rows=[20], hq=2, hkv=2, d=64),
+    "two_q_tiles": dict(ctx=[100], rows=[40], hq=7, hkv=1, d=128),
+    "ragged": dict(ctx=[0, 130, 17, 500, 3], rows=[37, 1, 0, 64, 129], hq=14, hkv=2, d=128),
+    "ragged_d64": dict(ctx=[3, 1000, 0], rows=[150, 2, 17], hq=8, hkv=4, d=64),
+    "group_1": dict(ctx=[250], rows=[300], hq=2, hkv=2, d=64),
+    "group_16": dict(ctx=[60, 0], rows=[21, 2], hq=32, hkv=2, d=128),
+    "long_context": dict(ctx=[6000], rows=[18], hq=7, hkv=1, d=128),
+    "any_scale": dict(ctx=[300], rows=[30], hq=4, hkv=2, d=128, pow2=False),
+    "value_scales": dict(ctx=[400], rows=[30], hq=4, hkv=2, d=128, v_spread=6),
+    "idle": dict(ctx=[40, 10, 0], rows=[20, 5, 30], hq=4, hkv=4, d=64, idle=(1,)),
+    "unspoken_bound": dict(ctx=[9, 8], rows=[19, 14], hq=4, hkv=4, d=128, max_rows=0),
+}
+
+
+@pytest.mark.parametrize("name", PROMPT)
+def test_many_rows(name):
+    c = Case(**PROMPT[name])
+    if c.max_rows == 0:
+        c.ws = torch.empty(c.kvrp.kv_attend_q8_workspace_size(c.hq, c.hkv, c.d, sum(c.rows)), dtype=torch.uint8, device="cuda")
+    c.run()
+    assert c.kvrp.kvrp_last_launch_count() == 2
+    c.check()
+    assert int(c.status) == 0
+    first = c.out.clone(), c.lse.clone()
+    c.out.fill_(3.0)
+    c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(first[0], c.out) and torch.equal(first[1], c.lse)
+
+
+def test_a_prompt_is_its_rows_one_by_one():
+    """The kernel for many rows against the one for few, on the same cache."""
+    c = Case(ctx=[90], rows=[25], hq=8, hkv=2, d=128)
+    c.run()
+    one = torch.empty_like(c.out)
+    for i in range(25):
+        seqs = c.kvrp.Seqs(seq_lens=i32([91 + i]), block_tables=i32(c.table), num_pages=c.pages)
+        c.run(seqs=seqs, q=c.dq[i:], out=one[i:], lse=None)
+    torch.cuda.synchronize()
+    _, _, mag = attend_rows(bf16_bits_to_f64(c.q), *c.sequence(0), 2, c.sm)
+    a, b = f64(c.out), f64(one)
+    assert np.all(np.abs(a - b) <= 2 * (2.0 ** -8 * np.abs(a) + 2.0 ** -10 * mag))
+
+
+def test_prompt_bad_lengths_and_bad_pages():
+    c = Case(ctx=[60, 30, 90], rows=[20, 20, 40], hq=4, hkv=2, d=64)
+    for lens in ([80, 19, 130], [80, 16 * c.table.shape[1] + 1, 130]):
+        c.out.fill_(5.0)
+        c.status.zero_()
+        c.run(seqs=c.kvrp.Seqs(seq_lens=i32(lens), block_tables=i32(c.table), num_pages=c.pages, n_rows=80,
+                               row_start=i32(c.starts), max_rows=40))
+        c.check(seqs=[0, 2])
+        assert int(c.status) == 4 and bool((c.out[20:40] == 5.0).all())
+    for bad in (-1, c.pages):
+        table = c.table.copy()
+        table[1, 0] = bad
+        c.status.zero_()
+        c.run(seqs=c.kvrp.Seqs(seq_lens=i32(c.lens), block_tables=i32(table), num_pages=c.pages, n_rows=80,
+                               row_start=i32(c.starts), max_rows=40))
+        c.check(seqs=[0, 2])
+        assert int(c.status) == 1
+
+
 def test_zero_values_and_zero_queries():
     """A page of zero values beside others (its scale is the floor), and a query of zeros."""
     c = Case(ctx=[100], rows=[1], hq=4, hkv=1, d=128, one_each=True)
