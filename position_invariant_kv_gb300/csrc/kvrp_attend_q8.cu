@@ -52,89 +52,113 @@ namespace attend_q8 {
 
 
 // ---- shares ---------------------------------------------------------------------------
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+
 struct Seq {
-  int row0, rows, len, pages;
+  int row0, rows, len, pages;   // pages 0: no work
 };
-// Sequence s as the decode kernel sees it; pages 0 where it has no work.
-__device__ __forceinline__ Seq seq_at(const Params& p, int s, int max_rows, bool tell = false) {
+// a / n and a b / n, by the 32-bit divider where they fit
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  return (uint64_t)(a | b) < (1ull << 31) ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ Seq seq_at(const Params& p, int s, bool* idle = nullptr, bool tell = false) {
   Seq r;
-  const bool ok = sequence(p.seqs, s, r.row0, r.rows, r.len) && r.rows <= max_rows;
+  const bool ok = sequence(p.seqs, s, r.row0, r.rows, r.len) && r.rows <= p.max_rows;
   r.pages = ok && r.rows > 0 ? (r.len + kPage - 1) / kPage : 0;
   if (tell && !ok) flag(p.status, KVRP_DEV_BAD_LENGTH);
+  if (idle && r.len == 0) *idle = true;
   return r;
 }
 
-// A position in the list of (sequence, head, page), and the pages left of the share.
+// A segment: pages [page, end) of (sequence, head group), and the pages left of the share
+// from `page` on.
 struct Cursor {
-  int s, h, page, end;    // the segment's next page and its end
-  int64_t left;           // pages of the share from `page` on
+  int s, grp, page, end;
+  int64_t left;
+};
+struct Plan {
+  Cursor at;
+  Seq seq;
+  int64_t total, b;   // pages in all, the share's end
+  int n_cta;
+  bool idle;          // some place of the batch is idle
+};
+struct PlanSmem {
+  int64_t sum[kWarps];
+  int64_t before;
+  Seq seq;
+  int found;
 };
 
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sh) {
+// This CTA's share of the list of (sequence, head group, page).  A share is at least kLeast
+// pages a stream, so that a small batch is not cut into parts that cost more to join than to read.
+constexpr int kLeast = 2;
+__device__ __forceinline__ bool find_share(const Params& p, Plan* out, PlanSmem& sh) {
+  const int n = p.seqs.n_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool idle = false;
+  int64_t later = 0;   // pages of the sequences past the first kThreads
+  for (int s = kThreads + tid; s < n; s += kThreads) later += seq_at(p, s, &idle, blockIdx.x == 0).pages;
+  if (n > kThreads) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int64_t all = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) all += sh[w];
-  return all;
-}
-
-// This CTA's share of the pages.  A share is at least one page a warp, so that a small
-// batch is not cut into parts that cost more to merge than to read.
-template <int kWarps>
-__device__ __forceinline__ bool find_share(const Params& p, int max_rows, Cursor* out, int64_t* sh, int* found) {
-  const int n = p.seqs.n_seqs, threads = 32 * kWarps;
-  const int tid = threadIdx.x;
-  int64_t mine = 0;
-  for (int s = tid; s < n; s += threads) mine += (int64_t)seq_at(p, s, max_rows, blockIdx.x == 0).pages * p.Hkv;
-  const int64_t total = block_sum(mine, sh);
-  const int n_cta = (int)min((int64_t)p.n_cta, (total + kWarps - 1) / kWarps);
-  if ((int)blockIdx.x >= n_cta) return false;
-  const int64_t a = total * blockIdx.x / n_cta, b = total * (blockIdx.x + 1) / n_cta;
-  // the sequence that holds page a: prefix sums, `threads` sequences at a time
-  int64_t before = 0;
-  for (int s0 = 0; s0 < n; s0 += threads) {
+    for (int o = 16; o > 0; o >>= 1) later += __shfl_xor_sync(0xffffffffu, later, o);
+    if (lane == 0) sh.sum[warp] = later;
+    __syncthreads();
+    later = 0;
+    for (int w = 0; w < kWarps; ++w) later += sh.sum[w];
+    __syncthreads();
+  }
+  int64_t before = 0, a = 0;
+  for (int s0 = 0; s0 < n; s0 += kThreads) {   // prefix sums, kThreads sequences at a time
     const int s = s0 + tid;
-    const int64_t c = s < n ? (int64_t)seq_at(p, s, max_rows).pages * p.Hkv : 0;
-    int64_t sum = c;
+    Seq q = {0, 0, 0, 0};
+    if (s < n) q = s0 == 0 ? seq_at(p, s, &idle, blockIdx.x == 0) : seq_at(p, s);
+    int64_t sum = q.pages;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t t = __shfl_up_sync(0xffffffffu, sum, o);
-      if ((tid & 31) >= o) sum += t;
+      if (lane >= o) sum += t;
     }
-    __syncthreads();
-    if ((tid & 31) == 31) sh[tid >> 5] = sum;
-    if (tid == 0) *found = -1;
-    __syncthreads();
-    int64_t at = before + sum - c;
+    if (lane == 31) sh.sum[warp] = sum;
+    if (tid == 0) sh.found = -1;
+    out->idle = __syncthreads_or(idle);
+    int64_t lo = before + sum - q.pages;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w < (tid >> 5)) at += sh[w];
-      before += sh[w];
+      if (w < warp) lo += sh.sum[w];
+      before += sh.sum[w];
     }
-    if (a >= at && a < at + c) {
-      *found = s;
-      sh[kWarps] = a - at;
+    if (s0 == 0) {
+      out->total = (before + later) * p.n_grp;
+      out->n_cta = (int)min((int64_t)p.n_cta, div64(out->total + kLeast * p.streams - 1, kLeast * p.streams));
+      if ((int)blockIdx.x >= out->n_cta) return false;
+      a = div64(out->total * blockIdx.x, out->n_cta);
+      out->b = div64(out->total * (blockIdx.x + 1), out->n_cta);
+    }
+    if (a >= lo * p.n_grp && a < (lo + q.pages) * p.n_grp) {
+      sh.found = s;
+      sh.before = lo * p.n_grp;
+      sh.seq = q;
     }
     __syncthreads();
-    if (*found >= 0) break;
+    if (sh.found >= 0) break;
+    __syncthreads();
   }
-  const Seq q = seq_at(p, *found, max_rows);
-  out->s = *found;
-  out->h = (int)(sh[kWarps] / q.pages);
-  out->page = (int)(sh[kWarps] % q.pages);
-  out->left = b - a;
-  out->end = (int)min((int64_t)q.pages, out->page + out->left);
+  out->seq = sh.seq;
+  out->at.s = sh.found;
+  const int64_t at = a - sh.before;
+  out->at.grp = (int)div64(at, out->seq.pages);
+  out->at.page = (int)(at - (int64_t)out->at.grp * out->seq.pages);
+  out->at.left = out->b - a;
+  out->at.end = (int)min((int64_t)out->seq.pages, out->at.page + out->at.left);
   return true;
 }
-// The next segment of the share; false at its end.
-__device__ __forceinline__ bool next_segment(const Params& p, int max_rows, Cursor& c, int first, Seq& q) {
+// The next segment of the share after one that began at page `first`; false at the share's end.
+__device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, int first, Seq& q) {
   c.left -= c.end - first;
   if (c.left <= 0) return false;
-  if (++c.h == p.Hkv) {
-    c.h = 0;
-    do q = seq_at(p, ++c.s, max_rows);
+  if (++c.grp == p.n_grp) {
+    c.grp = 0;
+    do q = seq_at(p, ++c.s);
     while (q.pages == 0);
   }
   c.page = 0;
@@ -142,120 +166,164 @@ __device__ __forceinline__ bool next_segment(const Params& p, int max_rows, Curs
   return true;
 }
 
+// Asynchronous copies to shared memory (zeros past the first `bytes`), and their groups.
+__device__ __forceinline__ void copy4(uint32_t to, const float* from, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>   // until at most N of this thread's groups are in flight
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Where a box keeps 16-byte chunk `chunk` of row `row` (the row's D bytes, 16 rows): swizzled so that
+// both the fragment loads of K (8 rows a chunk at a time) and of V (4 rows, every other one) and the
+// copies themselves touch all banks.
+template <int D>
+__device__ __forceinline__ uint32_t box_offset(int row, int chunk) {
+  if (D == 128) return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
+  return (uint32_t)((row >> 1) * 128 + (((row ^ (row >> 1)) & 1) << 6) + ((chunk ^ ((row >> 1) & 2)) << 4));
+}
+
+// Assignments that the compiler keeps inside their branch.
+__device__ __forceinline__ void make_minus_inf(float& x) { asm volatile("mov.b32 %0, 0xff800000;" : "=f"(x)); }
+__device__ __forceinline__ void make_zero(uint32_t& x) { asm volatile("mov.b32 %0, 0;" : "=r"(x)); }
+
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+
 // ---- decode ----------------------------------------------------------------------------
-constexpr int kWarps = 8;
+constexpr int kMergeSlots = 2;   // warps that hand over their results at a time
 template <int D, int NT>
 struct Decode {
+  static constexpr int kPages = 128 / D;                      // pages of a step
   static constexpr int kBox = kPage * D;                      // bytes of one head's K (or V) of a page
-  // 8 to 12 KB a warp, 128 to 192 KB in flight on an SM; two CTAs fit beside their merge buffers
-  static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 6 : 5);
-  static constexpr int kRing = kWarps * kStages * 2 * kBox;
+  static constexpr int kStage = 2 * kPages * kBox;            // 4 KB
+  // Two CTAs an SM, 12 KB in flight a warp.  16 columns of head_dim 128 need 200 registers a thread:
+  // one CTA, 24 KB a warp.
+  static constexpr int kCtas = D == 128 && NT == 2 ? 1 : 2;
+  static constexpr int kStages = kCtas == 1 ? 6 : 3;
+  static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kMerge = 32 * (D / 16 * NT * 4 + NT * 6);   // words of one warp's accumulator and statistics
-  static constexpr int kSmem = 1024 + kRing + kWarps / 2 * kMerge * 4;
+  static constexpr int kSmem = kRing + kMergeSlots * kMerge * 4;
 };
 
 template <int D, int NT>   // head_dim; tiles of 8 (row, head) columns
-__global__ void __launch_bounds__(32 * kWarps, 2)
-    decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                  const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kernel(const __grid_constant__ Params p) {
+  using C = Decode<D, NT>;
   constexpr int KT = D / 16;                 // 16-deep steps over the features; 16-feature tiles of O^T
-  constexpr int kBox = Decode<D, NT>::kBox, kStages = Decode<D, NT>::kStages, kMerge = Decode<D, NT>::kMerge;
+  constexpr int PG = C::kPages, kBox = C::kBox, kStages = C::kStages, kMerge = C::kMerge;
   constexpr int FPL = D / 8;                 // features of O a lane holds for a column
-  extern __shared__ uint8_t raw_smem[];
-  __shared__ __align__(8) uint64_t bars[kWarps * kStages];
-  __shared__ float2 scales[kWarps * kStages];
-  __shared__ int64_t sh[kWarps + 1];
-  __shared__ int found, abort_flag;
+  extern __shared__ __align__(128) uint8_t raw_smem[];
+  __shared__ float2 scales[kWarps * kStages * PG];
+  __shared__ PlanSmem plan_smem;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
-  const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
-  const uint32_t ring = smem + (uint32_t)warp * kStages * 2 * kBox;
-  float* merge = reinterpret_cast<float*>(raw_smem + (smem - smem_u32(raw_smem)) + Decode<D, NT>::kRing);
-  const uint32_t bar0 = smem_u32(bars) + 8u * warp * kStages;
-  float2* my_scales = scales + warp * kStages;
-  if (tid == 0) {
-    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(bars) + 8u * i, 1);
-    abort_flag = 0;
-    mbar_init_fence();
-  }
-  volatile int* abort_p = &abort_flag;
-  if (tid == 32) {
-    prefetch_tensormap(&kmap);
-    prefetch_tensormap(&vmap);
-  }
+  const uint32_t ring = smem_u32(raw_smem) + (uint32_t)warp * kStages * C::kStage;
+  float* merge = reinterpret_cast<float*>(raw_smem + C::kRing);
+  float2* my_scales = scales + warp * kStages * PG;
   pdl_wait();
   pdl_launch_dependents();
-  const int max_rows = p.max_rows;
-  Cursor ic;
-  if (!find_share<kWarps>(p, max_rows, &ic, sh, &found)) {
-    if (tid == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    write_idle(p, D);
+  Plan plan;
+  if (!find_share(p, &plan, plan_smem)) {
+    if (tid == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (plan.idle) write_idle(p, D);
     return;
   }
-  __syncthreads();   // the barriers are initialised
-  Cursor cc = ic;    // the segment being computed
-  Seq cq = seq_at(p, cc.s, max_rows), iq = cq;
+  // this warp's head of the group, and its stream: pages stream, stream + streams, ... of a segment
+  const int hd = warp & (p.hg - 1), stream = warp / p.hg;
 
-  // ---- the issuing side: which page goes into the ring next --------------------------
-  int issue_first = ic.page;   // the segment's first page
-  int b_page = 0, b_at = 32;   // a batch of table entries and scales, one a lane
-  float b_ks = 0.f, b_vs = 0.f;
-  int n_issued = 0;
+  // ---- the issuing side: which pages go into the ring next ------------------------------
+  // Steps that this stream has in pages [first, end).
+  auto steps_of = [&](int first, int end) {
+    const int blocks = (end - first + PG - 1) / PG;
+    return blocks > stream ? (blocks - stream - 1) / p.streams + 1 : 0;
+  };
+  Cursor ic = plan.at;
+  Seq iq = plan.seq;
+  int i_first = ic.page;                             // the segment's first page
+  int i_left = steps_of(ic.page, ic.end), i_q = 0;   // steps to issue in it, pages of the stream begun in it
+  int b_page = -1, b_at = 32;                        // a batch of table entries, one a lane
+  int i_st = 0;
   bool more = true;
-  auto refill = [&]() {
-    const int pg = ic.page + lane * kWarps;
-    b_page = p.seqs.num_pages;   // past the pool: the box reads zeros
-    b_ks = b_vs = 0.f;
-    if (pg < ic.end) {
-      const int e = p.seqs.block_tables[(int64_t)ic.s * p.seqs.table_stride + pg];
-      if (e >= 0 && e < p.seqs.num_pages) {
-        b_page = e;
-        b_ks = p.k_scale[(int64_t)e * p.Hkv + ic.h];
-        b_vs = p.v_scale[(int64_t)e * p.Hkv + ic.h];
-      } else {
-        flag(p.status, KVRP_DEV_BAD_PAGE);
-      }
-    }
-    b_at = 0;
-  };
-  auto settle = [&]() {   // move to the first segment that has a page for this warp
-    while (more && ic.page >= ic.end) {
-      more = next_segment(p, max_rows, ic, issue_first, iq);
-      issue_first = 0;
-      ic.page = warp;
+  auto settle = [&]() {   // to the next segment that has a step for this stream
+    while (i_left == 0 && (more = next_segment(p, ic, i_first, iq))) {
+      i_first = i_q = 0;
+      i_left = steps_of(0, ic.end);
       b_at = 32;
+      // its queries, which the computing side reads some steps from now: a 128-byte line a lane
+      const int lines = D / 64 * p.g, line = lane;   // of one row's heads
+      for (int x = line; x < iq.rows * lines; x += 32)
+        prefetch_l1(p.q + (iq.row0 + x / lines) * p.q_stride + (int64_t)((ic.grp * p.hg + hd) * p.g) * D + (x % lines) * 64);
     }
   };
-  ic.page += warp;
-  settle();
+  if (i_left == 0) settle();
+  // A lane's 16 bytes of a box: row `brow` (and every kRows-th after it), chunk lane % (D / 16).
+  constexpr int kRows = 512 / D;
+  const int row_bytes = p.Hkv * D, page_bytes = row_bytes * kPage;
+  const int brow = lane / (D / 16), bchunk = lane % (D / 16);
+  const uint8_t* k_lane = p.k_pool + (int64_t)brow * row_bytes + bchunk * 16 + hd * D;
+  const uint8_t* v_lane = p.v_pool + (int64_t)brow * row_bytes + bchunk * 16 + hd * D;
+  const uint32_t to_lane = ring + box_offset<D>(brow, bchunk);
   auto issue = [&]() {
-    if (!more || __shfl_sync(0xffffffffu, *abort_p, 0)) return;
-    if (b_at == 32) refill();
-    const int st = n_issued % kStages;
-    const int pg = __shfl_sync(0xffffffffu, b_page, b_at);
-    const float ks = __shfl_sync(0xffffffffu, b_ks, b_at), vs = __shfl_sync(0xffffffffu, b_vs, b_at);
-    if (lane == 0) {
-      const uint32_t bar = bar0 + 8u * st, at = ring + (uint32_t)st * 2 * kBox;
-      my_scales[st] = make_float2(ks, vs);
-      mbar_expect_tx(bar, 2 * kBox);
-      tma_load_3d(at, &kmap, bar, ic.h * D, 0, pg);
-      tma_load_3d(at + kBox, &vmap, bar, ic.h * D, 0, pg);
+    if (more) {
+      if (b_at == 32) {   // the next 32 pages of the stream
+        const int q = i_q + lane, pg = i_first + (stream + q / PG * p.streams) * PG + q % PG;
+        b_page = -1;      // none
+        if (pg < ic.end) {
+          b_page = p.seqs.block_tables[(int64_t)ic.s * p.seqs.table_stride + pg];
+          if (b_page < 0 || b_page >= p.seqs.num_pages) {
+            b_page = p.seqs.num_pages;   // read as zeros
+            flag(p.status, KVRP_DEV_BAD_PAGE);
+          }
+        }
+        b_at = 0;
+      }
+      const uint32_t at = to_lane + (uint32_t)(i_st * C::kStage);
+#pragma unroll
+      for (int w = 0; w < PG; ++w) {
+        const int pg = __shfl_sync(0xffffffffu, b_page, b_at + w);
+        if (PG > 1 && pg < 0) {   // past the segment: no weight, whatever the box holds
+          if (lane == 0) my_scales[i_st * PG + w] = make_float2(0.f, 0.f);
+          continue;
+        }
+        const uint32_t bytes = pg < p.seqs.num_pages ? 16 : 0;
+        const int at_page = bytes ? pg : 0;
+        const uint8_t* kf = k_lane + (int64_t)at_page * page_bytes + ic.grp * p.hg * D;
+        const uint8_t* vf = v_lane + (int64_t)at_page * page_bytes + ic.grp * p.hg * D;
+#pragma unroll
+        for (int i = 0; i < kPage / kRows; ++i) {
+          // 128: rows brow + 4 i, whose swizzle differs in bit 2 of the chunk for odd i; 64: rows brow + 8 i
+          const uint32_t to = (at ^ (D == 128 && (i & 1) ? 64u : 0u)) + w * kBox + i * kRows * D;
+          copy16(to, kf, bytes);
+          copy16(to + PG * kBox, vf, bytes);
+          kf += kRows * row_bytes;
+          vf += kRows * row_bytes;
+        }
+        if (lane < 2)
+          copy4(smem_u32(my_scales + i_st * PG + w) + 4 * lane,
+                (lane ? p.v_scale : p.k_scale) + (int64_t)at_page * p.Hkv + ic.grp * p.hg + hd, bytes / 4);
+      }
+      i_st = i_st + 1 == kStages ? 0 : i_st + 1;
+      b_at += PG;
+      i_q += PG;
+      if (--i_left == 0) settle();
     }
-    ++b_at;
-    ++n_issued;
-    ic.page += kWarps;
-    settle();
+    copies_commit();   // an empty group past the share's end: the count of groups in flight stays the same
   };
+#pragma unroll 1
   for (int i = 0; i < kStages; ++i) issue();
 
-  int n_used = 0;
-  int4 meta = make_int4(-1, 0, 0, 0);
+  Cursor cc = plan.at;   // the segment being computed
+  Seq cq = plan.seq;
+  int c_st = 0;
+  int4 meta = make_int4(0, 0, 0, 0);   // of a unit that begins here and goes on: rows, head group, parts, first row
   while (true) {
-    // ---- a segment: the queries of its KV head ------------------------------------------
-    const int first = cc.page, cols = cq.rows * p.g, ctx = cq.len - cq.rows;
+    // ---- a segment: the queries of this warp's KV head ------------------------------------
+    const int first = cc.page, cols = cq.rows * p.g, ctx = cq.len - cq.rows, head = cc.grp * p.hg + hd;
     uint32_t qb[KT][NT][2];
     float fac[NT][2];
     int limit[NT][2];
@@ -266,7 +334,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
 #pragma unroll
       for (int kk = 0; kk < KT; ++kk) w[kk][0] = w[kk][1] = 0u;
       if (c < cols) {
-        const uint16_t* at = p.q + (cq.row0 + c / p.g) * p.q_stride + (int64_t)(cc.h * p.g + c % p.g) * D + tig * (D / 4);
+        const uint16_t* at = p.q + (cq.row0 + c / p.g) * p.q_stride + (int64_t)(head * p.g + c % p.g) * D + tig * (D / 4);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint4 u = reinterpret_cast<const uint4*>(at)[i];
@@ -313,24 +381,31 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
       for (int mt = 0; mt < KT; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
     }
 
-    for (int pg = first + warp; pg < cc.end; pg += kWarps) {
-      const int st = n_used % kStages;
-      wait_phase(bar0 + 8u * st, (n_used / kStages) & 1, abort_p, p.status);
-      __syncwarp();
-      ++n_used;
-      const uint32_t kat = ring + (uint32_t)st * 2 * kBox, vat = kat + kBox;
-      const float2 sc = my_scales[st];
+    const int steps = steps_of(first, cc.end);
+    int pg = first + stream * PG;
+#pragma unroll 1
+    for (int step = 0; step < steps; ++step, pg += p.streams * PG) {
+      const int st = c_st;
+      copies_wait<kStages - 1>();
+      __syncwarp();   // every lane's copies of the stage have landed
+      if (++c_st == kStages) c_st = 0;
+      const uint32_t kat = ring + (uint32_t)st * C::kStage, vat = kat + PG * kBox;
       // ---- S = K Q^T -----------------------------------------------------------------
-      float c[NT][4];
+      float c[PG][NT][4], f[PG][NT][2], lvs[PG];   // raw scores; x = c f; log2 of the value scales
+      // the pages next to the end: a row sees its own position and before; the share's end cuts a step
+      const bool tail = (pg + PG) * kPage > ctx + 1 || pg + PG > cc.end;
+      bool grow = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
-      {
+      for (int w = 0; w < PG; ++w) {
+        const float2 sc = my_scales[st * PG + w];
+        lvs[w] = lg2(sc.y);   // exact for a power of two; -inf for a zero scale
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) c[w][nt][0] = c[w][nt][1] = c[w][nt][2] = c[w][nt][3] = 0.f;
         uint32_t k0[KT], k1[KT];   // rows gid and gid + 8: features tig D/4 + 4 kk + {0..3}
 #pragma unroll
         for (int i = 0; i < KT / 4; ++i) {
           const int chunk = tig * (KT / 4) + i;
-          const uint32_t off = D == 128 ? (uint32_t)(gid * 128 + ((chunk ^ gid) << 4))
-                                        : (uint32_t)(gid * 64 + ((chunk ^ (gid >> 1)) << 4));
+          const uint32_t off = w * kBox + box_offset<D>(gid, chunk);
           asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                        : "=r"(k0[4 * i]), "=r"(k0[4 * i + 1]), "=r"(k0[4 * i + 2]), "=r"(k0[4 * i + 3]) : "r"(kat + off));
           asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
@@ -341,31 +416,51 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
           const uint32_t a[4] = {q8::e4m3x2_to_f16x2((uint16_t)k0[kk]), q8::e4m3x2_to_f16x2((uint16_t)k1[kk]),
                                  q8::e4m3x2_to_f16x2((uint16_t)(k0[kk] >> 16)), q8::e4m3x2_to_f16x2((uint16_t)(k1[kk] >> 16))};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816_f16(c[nt], a, qb[kk][nt][0], qb[kk][nt][1]);
+          for (int nt = 0; nt < NT; ++nt) mma16816_f16(c[w][nt], a, qb[kk][nt][0], qb[kk][nt][1]);
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) f[w][nt][b] = sc.x * fac[nt][b];
       }
-      const float lvs = lg2(sc.y);   // exact for a power of two; -inf for a zero scale
-      const bool tail = (pg + 1) * kPage > ctx + 1;
-      bool grow = false;
+      if (tail) {   // rare, and a branch: as selects it would cost every page a third of its instructions
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int w = 0; w < PG; ++w)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = c[nt][e] * (sc.x * fac[nt][e & 1]);
-          if (tail && pg * kPage + gid + (e >> 1) * 8 >= limit[nt][e & 1]) x = -INFINITY;
-          c[nt][e] = x;
-          grow |= x > m[nt][e & 1] + kLazy || x + lvs > om[nt][e & 1] + kLazy;
-        }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int seen = pg + w < cc.end ? limit[nt][b] - (pg + w) * kPage : 0;
+              if (f[w][nt][b] == 0.f) f[w][nt][b] = 1.f;   // no scale: the scores are 0, and -inf stays -inf
+              if (gid >= seen) make_minus_inf(c[w][nt][b]);
+              if (gid + 8 >= seen) make_minus_inf(c[w][nt][2 + b]);
+            }
+      }
+#pragma unroll
+      for (int w = 0; w < PG; ++w)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            grow |= fmaxf(c[w][nt][b], c[w][nt][2 + b]) * f[w][nt][b] > fminf(m[nt][b], om[nt][b] - lvs[w]) + kLazy;
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            float t = fmaxf(c[nt][b], c[nt][2 + b]);
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-            const float nm = fmaxf(m[nt][b], t), no = fmaxf(om[nt][b], t + lvs);
+            float t = -INFINITY, u = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < PG; ++w) {
+              const float x = fmaxf(c[w][nt][b], c[w][nt][2 + b]) * f[w][nt][b];
+              t = fmaxf(t, x);
+              u = fmaxf(u, x + lvs[w]);
+            }
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) {
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+              u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
+            }
+            const float nm = fmaxf(m[nt][b], t), no = fmaxf(om[nt][b], u);
             if (nm > m[nt][b]) l[nt][b] *= ex2(m[nt][b] - nm);     // a first maximum: 2^-inf = 0
             m[nt][b] = nm;
             const float r = no > om[nt][b] ? ex2(om[nt][b] - no) : 1.f;
@@ -377,21 +472,31 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
             }
           }
       }
-      uint32_t pb[NT][2];
+      uint32_t pb[PG][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
+        float mm[2], oo[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = c[nt][e], mm = m[nt][e & 1], oo = om[nt][e & 1];
-          l[nt][e & 1] += ex2(x - (mm == -INFINITY ? 0.f : mm));
-          w[e] = ex2(x + lvs - (oo == -INFINITY ? 0.f : oo) + kShift);
+        for (int b = 0; b < 2; ++b) {
+          mm[b] = m[nt][b] == -INFINITY ? 0.f : m[nt][b];
+          oo[b] = (om[nt][b] == -INFINITY ? 0.f : om[nt][b]) - kShift;
         }
-        pb[nt][0] = movmatrix_trans(pack_f16(w[0], w[1]));
-        pb[nt][1] = movmatrix_trans(pack_f16(w[2], w[3]));
+#pragma unroll
+        for (int w = 0; w < PG; ++w) {
+          float e4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = c[w][nt][e], k = f[w][nt][e & 1];
+            l[nt][e & 1] += ex2(fmaf(x, k, -mm[e & 1]));
+            e4[e] = ex2(fmaf(x, k, lvs[w] - oo[e & 1]));
+          }
+          pb[w][nt][0] = movmatrix_trans(pack_f16(e4[0], e4[1]));
+          pb[w][nt][1] = movmatrix_trans(pack_f16(e4[2], e4[3]));
+        }
       }
       // ---- O^T += V^T P^T --------------------------------------------------------------
-      {
+#pragma unroll
+      for (int w = 0; w < PG; ++w) {
         uint32_t v[4][FPL / 4];   // tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9: features gid FPL ..
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -399,18 +504,23 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
           if constexpr (D == 128) {
             asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
-                         : "r"(vat + (uint32_t)(t * 128 + ((gid ^ (t & 7)) << 4))));
+                         : "r"(vat + w * kBox + box_offset<D>(t, gid)));
           } else {
             asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
                          : "=r"(v[i][0]), "=r"(v[i][1])
-                         : "r"(vat + (uint32_t)(t * 64 + (((gid >> 1) ^ ((t >> 1) & 3)) << 4) + (gid & 1) * 8)));
-          }
-          if (tail && pg * kPage + t >= cq.len) {   // a slot past the sequence may hold anything, NaN included
-#pragma unroll
-            for (int j = 0; j < FPL / 4; ++j) v[i][j] = 0u;
+                         : "r"(vat + w * kBox + box_offset<D>(t, gid >> 1) + (gid & 1) * 8));
           }
         }
-        __syncwarp();   // every lane has read the stage
+        if (tail) {   // a slot past the sequence, or past the share, may hold anything, NaN included
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = 2 * tig + (i & 1) + (i >> 1) * 8;
+            if ((pg + w) * kPage + t >= cq.len || pg + w >= cc.end) {
+#pragma unroll
+              for (int j = 0; j < FPL / 4; ++j) make_zero(v[i][j]);
+            }
+          }
+        }
 #pragma unroll
         for (int j = 0; j < FPL / 4; ++j)
 #pragma unroll
@@ -420,12 +530,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
             const uint32_t a[4] = {q8::e4m3x2_to_f16x2((uint16_t)x), q8::e4m3x2_to_f16x2((uint16_t)(x >> 16)),
                                    q8::e4m3x2_to_f16x2((uint16_t)y), q8::e4m3x2_to_f16x2((uint16_t)(y >> 16))};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[2 * j + half][nt], a, pb[nt][0], pb[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[2 * j + half][nt], a, pb[w][nt][0], pb[w][nt][1]);
           }
       }
+      __syncwarp();   // every lane has read the stage
       issue();
     }
-    // ---- merge the warps: halves of the CTA into the other half, then quarters ------------
+    // ---- merge the streams of a head ----------------------------------------------------------
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -436,11 +547,16 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
         t += __shfl_xor_sync(0xffffffffu, t, 16);
         l[nt][b] = t;
       }
-    const int live = min(kWarps, cc.end - first);   // warps that had a page
-    for (int step = kWarps / 2; step > 0; step /= 2) {
-      if (step >= live) continue;
-      float* at = merge + (warp & (step - 1)) * kMerge + lane;
-      if (warp >= step && warp < 2 * step && warp < live) {
+    // Warps from, from + 1 into to, to + 1; with warp = stream * hg + head these are streams of
+    // the same heads, and one, two or four heads a group need the first four, three or two rounds.
+    const int live = min(p.streams, (cc.end - first + PG - 1) / PG) * p.hg;   // warps that had a page
+    for (int round = 0; round < p.rounds; ++round) {
+      const int from = round == 0 ? 6 : round == 1 ? 4 : round == 2 ? 2 : 1, to = round == 0 ? 2 : 0, count = round == 3 ? 1 : 2;
+      if (from >= live) continue;
+      const bool gives = warp >= from && warp < from + count && warp < live;
+      const bool takes = warp >= to && warp < to + count && warp - to + from < live;
+      float* at = merge + (warp - (gives ? from : to)) * kMerge + lane;
+      if (gives) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -456,7 +572,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
         }
       }
       __syncthreads();
-      if (warp < step && warp + step < live) {
+      if (takes) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -478,9 +594,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     }
     // ---- the segment's result: a whole unit goes out, a part goes to the combine -----------
     const bool begins = first == 0, ends = cc.end == cq.pages;
-    if (begins && !ends) meta.x = cc.s, meta.y = cc.h;
-    if (!begins) meta.z = ends ? 2 : 1;
-    if (warp == 0) {
+    if (begins && !ends) {
+      // the CTA whose share holds the unit's last page: the largest j with total j / n_cta <= that page
+      const int64_t last = plan.b - cc.left + cq.pages;
+      const int j = (int)div64(last * plan.n_cta - 1, plan.total);
+      meta = make_int4(cq.rows, cc.grp, j - (int)blockIdx.x + 1, cq.row0);
+    }
+    if (stream == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -489,7 +609,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
           if (c >= cols) continue;
           if (begins && ends) {
             const float r = l[nt][b] == 0.f ? 0.f : ex2(om[nt][b] - m[nt][b] - kShift) / l[nt][b];
-            const int64_t row = (int64_t)(cq.row0 + c / p.g) * p.Hq + cc.h * p.g + c % p.g;
+            const int64_t row = (int64_t)(cq.row0 + c / p.g) * p.Hq + head * p.g + c % p.g;
             uint32_t w[FPL / 2];
 #pragma unroll
             for (int mt = 0; mt < KT; ++mt) {
@@ -501,7 +621,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
             for (int i = 0; i < FPL / 8; ++i) to[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
             if (p.lse && gid == 0) p.lse[row] = (m[nt][b] + lg2(l[nt][b])) * kLn2;
           } else {
-            float* to = p.partial + ((int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * p.cols + c) * (D + 4);
+            float* to = p.partial + ((int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * p.cols + hd * p.max_rows * p.g + c) * (D + 4);
             float4* of = reinterpret_cast<float4*>(to + gid * FPL);
 #pragma unroll
             for (int i = 0; i < FPL / 4; ++i)
@@ -510,96 +630,137 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
           }
         }
     }
-    if (!next_segment(p, max_rows, cc, first, cq)) break;
+    if (!next_segment(p, cc, first, cq)) break;
   }
   if (tid == 0) p.meta[blockIdx.x] = meta;
-  write_idle(p, D);
-  if (*abort_p)   // let every copy land before the CTA exits
-    for (int i = max(0, n_issued - kStages); i < n_issued; ++i) drain_wait(bar0 + 8u * (i % kStages), (i / kStages) & 1, p.status);
+  if (plan.idle) write_idle(p, D);
 }
 
 // ---- combine ---------------------------------------------------------------------------
-// Block (i, c): column c of the unit that begins in CTA i and goes on in CTAs i + 1, ...
-constexpr int kCombineThreads = 128;
+// An item is one (head of the group, column) of a unit that begins in some CTA i and goes on in
+// CTAs i + 1, ...; every block lists those units from the CTAs' records.  A group of threads
+// holds an item's features, four each.  Where units have few parts each group takes an item of its
+// own; else a block takes one, its groups every kGroups-th part.
+constexpr int kCombineThreads = 128, kFewParts = 16;
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ Params p) {
-  constexpr int kLanes = D / 4, kGroups = kCombineThreads / kLanes;
-  __shared__ int last;
-  __shared__ float red[kCombineThreads / 32][3];
+__global__ void __launch_bounds__(kCombineThreads, 5) combine_kernel(const __grid_constant__ Params p) {
+  constexpr int kLanes = D / 4, kGroups = kCombineThreads / kLanes, kWarpsHere = kCombineThreads / 32;
   __shared__ float4 part[kGroups][kLanes];
+  __shared__ float stat[kGroups][3];
+  __shared__ int4 unit[kMaxCtas];   // its record, with the CTA in x's high half
+  __shared__ int count[kWarpsHere], total[kWarpsHere];
   pdl_wait();
   pdl_launch_dependents();
-  const int i = blockIdx.x, c = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-  const int4 mt = p.meta[i];
-  if (mt.x < 0) return;
-  int row0, rows, len;
-  sequence(p.seqs, mt.x, row0, rows, len);
-  if (c >= rows * p.g) return;
-  // the CTA that ends the unit
-  if (tid == 0) last = 0x7fffffff;
-  __syncthreads();
-  for (int j0 = i + 1; j0 < p.n_cta; j0 += kCombineThreads) {
+  const int tid = threadIdx.x, f = tid % kLanes, grp = tid / kLanes;
+  int units = 0, parts = 0;
+  for (int j0 = 0; j0 < p.n_cta; j0 += kCombineThreads) {
     const int j = j0 + tid;
-    if (j < p.n_cta && p.meta[j].z == 2) atomicMin(&last, j);
+    int4 mt = j < p.n_cta ? p.meta[j] : make_int4(0, 0, 0, 0);
+    const bool begins = mt.x > 0;
+    const uint32_t vote = __ballot_sync(0xffffffffu, begins);
+    const int sum = __reduce_add_sync(0xffffffffu, begins ? mt.z : 0);
+    if ((tid & 31) == 0) count[tid >> 5] = __popc(vote), total[tid >> 5] = sum;
     __syncthreads();
-    if (last != 0x7fffffff) break;
+    int at = units + __popc(vote & ((1u << (tid & 31)) - 1));
+#pragma unroll
+    for (int w = 0; w < kWarpsHere; ++w) {
+      if (w < (tid >> 5)) at += count[w];
+      units += count[w];
+      parts += total[w];
+    }
+    mt.x |= j << 16;   // a record's rows are at most 16
+    if (begins) unit[at] = mt;
     __syncthreads();
   }
-  const int n = min(last, p.n_cta - 1) - i + 1;
-  auto entry = [&](int k) { return p.partial + ((int64_t)((i + k) * 2 + (k == 0 ? 1 : 0)) * p.cols + c) * (D + 4); };
-  float m = -INFINITY, om = -INFINITY;
-  for (int k = tid; k < n; k += kCombineThreads) {
-    const float4 s = *reinterpret_cast<const float4*>(entry(k) + D);
-    m = fmaxf(m, s.x);
-    om = fmaxf(om, s.y);
-  }
+  const int most = p.max_rows * p.g;
+  const bool alone = parts <= kFewParts * units && units * p.cols > (int)gridDim.x;   // a group an item
+  const int per = alone ? kGroups : 1, step = alone ? 1 : kGroups;
+  for (int first = blockIdx.x * per; first < units * p.cols; first += gridDim.x * per) {
+    const int item = first + (alone ? grp : 0);
+    const int4 mt = unit[min(item, units * p.cols - 1) / p.cols];
+    const int i = mt.x >> 16, y = item % p.cols, hd = y / most, c = y % most;
+    const bool live = item < units * p.cols && c < (mt.x & 0xffff) * p.g;
+    const int n = live ? min(mt.z, p.n_cta - i) : 0;
+    float m = -INFINITY, om = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 8;   // parts in flight
+    for (int k0 = alone ? 0 : grp; k0 < n; k0 += kBatch * step) {
+      float4 s[kBatch], v[kBatch];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    om = fmaxf(om, __shfl_xor_sync(0xffffffffu, om, o));
-  }
-  if (lane == 0) red[tid >> 5][0] = m, red[tid >> 5][1] = om;
-  __syncthreads();
+      for (int b = 0; b < kBatch; ++b) {
+        const int k = k0 + b * step;
+        s[b] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+        v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < n) {
+          const float* e = p.partial + ((int64_t)((i + k) * 2 + (k == 0 ? 1 : 0)) * p.cols + y) * (D + 4);
+          s[b] = *reinterpret_cast<const float4*>(e + D);
+          v[b] = reinterpret_cast<const float4*>(e)[f];
+        }
+      }
+      float nm = m, no = om;
 #pragma unroll
-  for (int w = 0; w < kCombineThreads / 32; ++w) {
-    m = fmaxf(m, red[w][0]);
-    om = fmaxf(om, red[w][1]);
-  }
-  const int f = tid % kLanes, grp = tid / kLanes;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 8
-  for (int k = grp; k < n; k += kGroups) {
-    const float* e = entry(k);
-    const float4 s = *reinterpret_cast<const float4*>(e + D), v = reinterpret_cast<const float4*>(e)[f];
-    const float w = om == -INFINITY ? 0.f : ex2(s.y - om);
-    l += m == -INFINITY ? 0.f : s.z * ex2(s.x - m);
-    acc.x = fmaf(v.x, w, acc.x);
-    acc.y = fmaf(v.y, w, acc.y);
-    acc.z = fmaf(v.z, w, acc.z);
-    acc.w = fmaf(v.w, w, acc.w);
-  }
-  part[grp][f] = acc;
-  __shared__ float lsum[kGroups];
-  if (f == 0) lsum[grp] = l;
-  __syncthreads();
-  if (grp != 0) return;
-  l = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int b = 0; b < kBatch; ++b) {
+        nm = fmaxf(nm, s[b].x);
+        no = fmaxf(no, s[b].y);
+      }
+      const float zm = nm == -INFINITY ? 0.f : nm, zo = no == -INFINITY ? 0.f : no;   // 2^-inf = 0, and no inf - inf
+      l *= ex2(m - zm);
+      const float r = ex2(om - zo);
+      acc = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
+      m = nm;
+      om = no;
 #pragma unroll
-  for (int k = 0; k < kGroups; ++k) {
-    l += lsum[k];
-    acc.x += part[k][f].x;
-    acc.y += part[k][f].y;
-    acc.z += part[k][f].z;
-    acc.w += part[k][f].w;
+      for (int b = 0; b < kBatch; ++b) {
+        l = fmaf(s[b].z, ex2(s[b].x - zm), l);
+        const float w = ex2(s[b].y - zo);
+        acc.x = fmaf(v[b].x, w, acc.x);
+        acc.y = fmaf(v[b].y, w, acc.y);
+        acc.z = fmaf(v[b].z, w, acc.z);
+        acc.w = fmaf(v[b].w, w, acc.w);
+      }
+    }
+    if (!alone) {
+      __syncthreads();   // the last item's have been read
+      part[grp][f] = acc;
+      if (f == 0) stat[grp][0] = m, stat[grp][1] = om, stat[grp][2] = l;
+      __syncthreads();
+      if (grp != 0) continue;
+      m = om = -INFINITY;
+      l = 0.f;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        m = fmaxf(m, stat[k][0]);
+        om = fmaxf(om, stat[k][1]);
+      }
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float zm = m == -INFINITY ? 0.f : m, zo = om == -INFINITY ? 0.f : om;
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        l = fmaf(stat[k][2], ex2(stat[k][0] - zm), l);
+        const float w = ex2(stat[k][1] - zo);
+        acc.x = fmaf(part[k][f].x, w, acc.x);
+        acc.y = fmaf(part[k][f].y, w, acc.y);
+        acc.z = fmaf(part[k][f].z, w, acc.z);
+        acc.w = fmaf(part[k][f].w, w, acc.w);
+      }
+    }
+    if (!live) continue;
+    const float r = l == 0.f ? 0.f : ex2(om - m - kShift) / l;
+    const int64_t row = (int64_t)(mt.w + c / p.g) * p.Hq + (mt.y * p.hg + hd) * p.g + c % p.g;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * r, acc.y * r), hi = __floats2bfloat162_rn(acc.z * r, acc.w * r);
+    *reinterpret_cast<uint2*>(p.out + row * D + 4 * f) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    if (p.lse && f == 0) p.lse[row] = (m + lg2(l)) * kLn2;
   }
-  const float r = l == 0.f ? 0.f : ex2(om - m - kShift) / l;
-  const int64_t row = (int64_t)(row0 + c / p.g) * p.Hq + mt.y * p.g + c % p.g;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * r, acc.y * r), hi = __floats2bfloat162_rn(acc.z * r, acc.w * r);
-  *reinterpret_cast<uint2*>(p.out + row * D + 4 * f) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  if (p.lse && f == 0) p.lse[row] = (m + lg2(l)) * kLn2;
+}
+
+// KV heads that a CTA takes together: the largest power of two that divides them, at most its
+// warps.  A token's heads lie side by side, so the warps of a CTA then read neighbouring bytes
+// at about the same time, and there are fewer streams of a head to merge.
+int head_group(int n_kv_heads) {
+  int hg = 1;
+  while (hg < kWarps && n_kv_heads % (2 * hg) == 0) hg *= 2;
+  return hg;
 }
 
 int sm_count() {
@@ -609,7 +770,7 @@ int sm_count() {
     cudaGetLastError();
     n = 160;   // no device: a size for the checks of a host without one
   }
-  return n;
+  return std::min(n, kMaxCtas / kMaxCtasPerSm);
 }
 
 size_t meta_bytes(int n_cta) { return ((size_t)n_cta * sizeof(int4) + 255) / 256 * 256; }
@@ -627,7 +788,8 @@ extern "C" {
 size_t kv_attend_q8_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_rows) {
   if (check_heads("kv_attend_q8_workspace_size", n_q_heads, n_kv_heads, head_dim) != KVRP_OK || max_rows <= 0) return 0;
   const bool few = (int64_t)max_rows * (n_q_heads / n_kv_heads) <= attend_q8::kMaxCols;
-  return few ? attend_q8::workspace_bytes(attend_q8::kMaxCtasPerSm * attend_q8::sm_count(), attend_q8::kMaxCols, head_dim)
+  return few ? attend_q8::workspace_bytes(attend_q8::kMaxCtasPerSm * attend_q8::sm_count(),
+                                          attend_q8::head_group(n_kv_heads) * max_rows * (n_q_heads / n_kv_heads), head_dim)
              : attend_q8::workspace_bytes(attend_q8::sm_count(), attend_q8::kPromptRows, head_dim);
 }
 
@@ -657,7 +819,7 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   if (!workspace || workspace_bytes < need) return fail(KVRP_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
   const int g = n_q_heads / n_kv_heads;
   const bool few = (int64_t)max_rows * g <= attend_q8::kMaxCols;
-  const int cols = few ? max_rows * g : attend_q8::kPromptRows;
+  const int hg = attend_q8::head_group(n_kv_heads);
   int sms = 0, smem_optin = 0;
   st = current_device_sms(&sms, &smem_optin);
   if (st != KVRP_OK) return st;
@@ -668,6 +830,8 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   p.q_stride = q_stride;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
+  p.k_pool = static_cast<const uint8_t*>(k_pool);
+  p.v_pool = static_cast<const uint8_t*>(v_pool);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.seqs = *seqs;
@@ -675,25 +839,29 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   p.Hq = n_q_heads;
   p.Hkv = n_kv_heads;
   p.g = g;
-  p.n_cta = few ? attend_q8::kMaxCtasPerSm * sms : sms;
-  p.cols = few ? attend_q8::kMaxCols : attend_q8::kPromptRows;
+  p.n_cta = std::min(attend_q8::kMaxCtas, few ? attend_q8::kMaxCtasPerSm * sms : sms);
+  p.cols = few ? hg * max_rows * g : attend_q8::kPromptRows;
   p.max_rows = max_rows;
+  p.hg = hg;
+  p.n_grp = n_kv_heads / hg;
+  p.streams = attend_q8::kWarps / hg;
+  p.rounds = hg == 1 ? 4 : hg == 2 ? 3 : hg == 4 ? 2 : 0;
   p.scale = softmax_scale * 1.4426950408889634f;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
   p.meta = reinterpret_cast<int4*>(base);
   p.partial = reinterpret_cast<float*>(base + attend_q8::meta_bytes(p.n_cta));
-  CUtensorMap kmap, vmap;
-  st = encode_q8_pool(&kmap, k_pool, seqs->num_pages, n_kv_heads * head_dim, head_dim);
-  if (st == KVRP_OK) st = encode_q8_pool(&vmap, v_pool, seqs->num_pages, n_kv_heads * head_dim, head_dim);
-  if (st != KVRP_OK) return st;
-
   if (!few) {
+    CUtensorMap kmap, vmap;
+    st = encode_q8_pool(&kmap, k_pool, seqs->num_pages, n_kv_heads * head_dim, head_dim);
+    if (st == KVRP_OK) st = encode_q8_pool(&vmap, v_pool, seqs->num_pages, n_kv_heads * head_dim, head_dim);
+    if (st != KVRP_OK) return st;
     const cudaError_t e = attend_q8::launch_prompt(kmap, vmap, p, head_dim, stream);
     if (e != cudaSuccess) return fail(KVRP_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     g_last_launches = 2;
     return KVRP_OK;
   }
-  const bool two = cols > 8;
+  const bool two = max_rows * g > 8;
+  if (two && head_dim == 128) p.n_cta = std::min(p.n_cta, attend_q8::Decode<128, 2>::kCtas * sms);
   auto kernel = head_dim == 64 ? (two ? attend_q8::decode_kernel<64, 2> : attend_q8::decode_kernel<64, 1>)
                                : (two ? attend_q8::decode_kernel<128, 2> : attend_q8::decode_kernel<128, 1>);
   const int smem = head_dim == 64 ? (two ? attend_q8::Decode<64, 2>::kSmem : attend_q8::Decode<64, 1>::kSmem)
@@ -707,11 +875,11 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(p.n_cta);
-  cfg.blockDim = dim3(32 * attend_q8::kWarps);
+  cfg.blockDim = dim3(attend_q8::kThreads);
   cfg.dynamicSmemBytes = smem;
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, kmap, vmap, p);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e == cudaSuccess) {
-    cfg.gridDim = dim3(p.n_cta, cols);
+    cfg.gridDim = dim3(5 * sms);
     cfg.blockDim = dim3(attend_q8::kCombineThreads);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, head_dim == 64 ? attend_q8::combine_kernel<64> : attend_q8::combine_kernel<128>, p);

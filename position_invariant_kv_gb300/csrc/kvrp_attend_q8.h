@@ -22,7 +22,7 @@ using q8::sequence;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kShift = 7.f;       // weights of the accumulator are exp2(. + 7)
 constexpr float kLazy = 8.f;        // how far a score may pass the running maximum
-constexpr int kMaxCtasPerSm = 2;
+constexpr int kMaxCtasPerSm = 2, kMaxCtas = 1024;   // bounds of the grid
 constexpr int kMaxCols = 16;        // rows x group of the decode kernel
 
 struct Params {
@@ -30,13 +30,17 @@ struct Params {
   int64_t q_stride;
   uint16_t* out;
   float* lse;
+  const uint8_t *k_pool, *v_pool;
   const float *k_scale, *v_scale;
   kvrp_seqs seqs;
   uint32_t* status;
-  float* partial;       // [n_cta][2][cols][D + 4]: O, then max, accumulator max, sum
-  int4* meta;           // [n_cta]: x, y = sequence and head whose first part this CTA holds (x < 0: none),
-                        //          z = 0 no part of a unit begun before, 1 a middle part, 2 the last part
-  int Hq, Hkv, g, n_cta, cols, max_rows;
+  float* partial;       // [n_cta][2][cols][D + 4]: O, then max, accumulator max, sum; of a unit begun
+                        // before this CTA's share, and of one that goes on after it
+  int4* meta;           // [n_cta][2]: the unit whose first, not last, part this CTA holds
+  int Hq, Hkv, g, n_cta, max_rows;
+  int cols;             // (head, row) columns of a part: heads of a group x max_rows x g, or kPromptRows
+  int hg, n_grp;        // few rows: KV heads a CTA takes together, their groups,
+  int streams, rounds;  // warps that share a head's pages, rounds that merge them
   float scale;          // softmax_scale * log2(e)
 };
 
