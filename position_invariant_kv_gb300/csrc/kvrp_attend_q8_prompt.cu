@@ -92,14 +92,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -109,7 +107,47 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Until this thread's TMEM loads have arrived; names the registers they fill, so that nothing that
+// reads them can be moved ahead of the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), 
+        "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), 
+        "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), 
+        "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+      :
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), 
+        "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+      :
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---- units and shares ------------------------------------------------------------------------
@@ -256,22 +294,23 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
   auto cempty = [&](int i) { return bar0 + 8u * (12 + i); };
   auto qfull = [&](int t) { return bar0 + 8u * (14 + t); };
   auto sfull = [&](int t) { return bar0 + 8u * (16 + t); };    // scores in TMEM
-  auto pfull = [&](int t) { return bar0 + 8u * (18 + t); };    // weights in TMEM, accumulator corrected
-  auto ofull = [&](int t) { return bar0 + 8u * (20 + t); };    // accumulator updated
-  const uint32_t drained = bar0 + 8u * 22;
+  auto pfull = [&](int t, int half) { return bar0 + 8u * (18 + 2 * t + half); };   // weights in TMEM, accumulator corrected
+  auto ofull = [&](int t) { return bar0 + 8u * (22 + t); };    // accumulator updated
+  auto drained = [&](int t) { return bar0 + 8u * (24 + t); };
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(kfull(i), 1), mbar_init(kempty(i), 1);
+    for (int i = 0; i < 3; ++i) mbar_init(kfull(i), 1), mbar_init(kempty(i), 2);   // both Q tiles
     for (int i = 0; i < 2; ++i) {
       mbar_init(vfull(i), 1);
       mbar_init(vempty(i), 128);
       mbar_init(cfull(i), 128);
-      mbar_init(cempty(i), 1);
+      mbar_init(cempty(i), 2);
       mbar_init(qfull(i), 128);
       mbar_init(sfull(i), 1);
-      mbar_init(pfull(i), 128);
+      mbar_init(pfull(i, 0), 128);
+      mbar_init(pfull(i, 1), 128);
       mbar_init(ofull(i), 1);
+      mbar_init(drained(i), 1);
     }
-    mbar_init(drained, 1);
     sh.abort_flag = 0;
     mbar_init_fence();
   }
@@ -343,75 +382,79 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       for (int i = max(0, nk - L::kKst); i < nk; ++i) drain_wait(kfull(i % L::kKst), (i / L::kKst) & 1, p.status);
       for (int i = max(0, nv - L::kVst); i < nv; ++i) drain_wait(vfull(i % L::kVst), (i / L::kVst) & 1, p.status);
     }
-  } else if (warp == 13) {
-    // ---- MMA --------------------------------------------------------------------------------
+  } else if (warp == 13 || warp == 14) {
+    // ---- MMA: a warp a Q tile, so that one tile's waits leave the tensor cores to the other ----
+    const int t = warp - 13;
     // descriptor: fp32 accumulator, M = 128; e4m3 (0) or f16 (0) operands; the second product's B is N-major
     const uint32_t id_qk = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
     const uint32_t id_pv = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-    int n = 0;                       // tiles begun
-    uint32_t nq[2] = {0, 0}, np[2] = {0, 0};   // units begun and tiles weighted, of each Q tile
+    int n = 0;                   // tiles begun
+    uint32_t nq = 0, np = 0;     // units begun and tiles weighted, of this Q tile
     bool ok = true;
-    auto scores = [&](int t, int tile) {   // S_t = (Q_hi + Q_lo) K^T
-      if (lane == 0) {
-        const uint32_t k = smem + L::kOffK + (tile % L::kKst) * L::kKV;
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            mma_e4m3(tmem + t * kTile, desc_rows<D>(smem + (2 * t + part) * L::kQ + 32 * i), desc_rows<D>(k + 32 * i), id_qk,
-                     (part | i) != 0);
-        mma_commit(sfull(t));
-      }
-      __syncwarp();
-    };
     do {
       const int act = active_tiles(p, u);
-      for (int t = 0; t < act && ok; ++t) {
-        ok = wait(qfull(t), nq[t]++ & 1);
-        if (ok && t == 0) ok = wait(kfull(n % L::kKst), (n / L::kKst) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        scores(t, n);
+      if (t >= act) {            // no rows: the stages pass by, every phase observed (a wait tests a parity only)
+        for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
+          ok = wait(kfull(n % L::kKst), (n / L::kKst) & 1);
+          if (ok && lane == 0) mbar_arrive(kempty(n % L::kKst));
+          ok = ok && wait(cfull(n & 1), (n >> 1) & 1);
+          if (ok && lane == 0) mbar_arrive(cempty(n & 1));
+          __syncwarp();
+        }
+        continue;
       }
+      auto scores = [&](int tile) {   // S_t = (Q_hi + Q_lo) K^T
+        if (lane == 0) {
+          const uint32_t k = smem + L::kOffK + (tile % L::kKst) * L::kKV;
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              mma_e4m3(tmem + t * kTile, desc_rows<D>(smem + (2 * t + part) * L::kQ + 32 * i), desc_rows<D>(k + 32 * i), id_qk,
+                       (part | i) != 0);
+          mma_commit(sfull(t));
+          mma_commit(kempty(tile % L::kKst));
+        }
+        __syncwarp();
+      };
+      ok = wait(qfull(t), nq++ & 1) && wait(kfull(n % L::kKst), (n / L::kKst) & 1);
       if (!ok) break;
-      if (lane == 0) mma_commit(kempty(n % L::kKst));
-      __syncwarp();
-      for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
+      tc_fence_after();
+      scores(n);
+      for (int j = u.j0; j < u.j1; ++j, ++n, ++np) {
         const int vb = n & 1;
-        const bool more = j + 1 < u.j1;
-        for (int t = 0; t < act && ok; ++t) {
-          ok = wait(pfull(t), np[t] & 1);
-          if (ok && t == 0) ok = wait(cfull(vb), (n >> 1) & 1);
+        for (int half = 0; half < 2 && ok; ++half) {
+          ok = wait(pfull(t, half), np & 1);
+          if (ok && half == 0) ok = wait(cfull(vb), (n >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
           if (lane == 0) {
             const uint32_t v = smem + L::kOffVc + vb * L::kVc;
 #pragma unroll
-            for (int i = 0; i < kTile / 16; ++i)
-              mma_f16_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * i, desc_cols(v + 2048 * i), id_pv, j > u.j0 || i > 0);
-            mma_commit(ofull(t));
+            for (int i = 0; i < kTile / 32; ++i) {
+              const int k = half * (kTile / 32) + i;
+              mma_f16_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * k, desc_cols(v + 2048 * k), id_pv, j > u.j0 || k > 0);
+            }
           }
           __syncwarp();
-          if (more) {   // the next scores take the place of these weights: wait until they have been read
-            ok = wait(ofull(t), np[t] & 1);
-            if (ok && t == 0) ok = wait(kfull((n + 1) % L::kKst), ((n + 1) / L::kKst) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            scores(t, n + 1);
-          }
-          ++np[t];
         }
         if (!ok) break;
         if (lane == 0) {
+          mma_commit(ofull(t));
           mma_commit(cempty(vb));
-          if (more) mma_commit(kempty((n + 1) % L::kKst));
         }
         __syncwarp();
+        if (j + 1 < u.j1) {   // the next scores take the place of these weights: wait until they have been read
+          ok = wait(kfull((n + 1) % L::kKst), ((n + 1) / L::kKst) & 1) && wait(ofull(t), np & 1);
+          if (!ok) break;
+          tc_fence_after();
+          scores(n + 1);
+        }
       }
     } while (ok && next_unit(p, u));
     if (!ok && lane == 0) {   // let the tensor cores finish before TMEM is freed
-      mma_commit(drained);
-      drain_wait(drained, 0, p.status);
+      mma_commit(drained(t));
+      drain_wait(drained(t), 0, p.status);
     }
     __syncwarp();
   } else if (warp >= 8 && warp < 12) {
@@ -533,33 +576,45 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         if (!ok) break;
         tc_fence_after();
         const float* ks = sh.ks[n % kScaleSlots];
-        const bool masked = (j + 1) * kTile > first_limit;
         const int seen = limit - j * kTile;   // columns below this are visible
+        const bool masked = (j + 1) * kTile > first_limit;
+        // Two passes over the row, 32 scores at a time, the next 32 on their way from TMEM meanwhile:
+        // a row in registers would leave none for the rest.
+        uint32_t r[2][32];
+        auto fetch = [&](int b) { tmem_ld32(S + 32 * b, r[b & 1]); };
+        auto hide = [&](int b) {
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * b + i >= seen) asm volatile("mov.b32 %0, 0xff800000;" : "=r"(r[b & 1][i]));   // -inf
+          }
+        };
+        float f[kPagesPerTile];
         float top = -INFINITY;
+        fetch(0);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          uint32_t r[32];
-          tmem_ld32(S + 32 * b, r);
-          tmem_wait_ld();
+          tmem_wait_ld(r[b & 1]);
+          fetch((b + 1) & 3);
+          hide(b);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float a = -INFINITY;
+          for (int h = 0; h < 2; ++h) {
+            const int q = 2 * b + h;
+            f[q] = ks[q] * c;
+            if (f[q] == 0.f) f[q] = 1.f;   // no scale: no page, or one of zeros; -inf stays -inf
+            float a = __uint_as_float(r[b & 1][16 * h]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x = __uint_as_float(r[16 * half + i]);
-              if (masked && 32 * b + 16 * half + i >= seen) x = -INFINITY;
-              a = fmaxf(a, x);
-            }
-            top = fmaxf(top, a * (ks[2 * b + half] * c));   // a page with no scale (0) gives NaN or 0: no maximum above the others'
+            for (int i = 1; i < 16; ++i) a = fmaxf(a, __uint_as_float(r[b & 1][16 * h + i]));
+            top = fmaxf(top, a * f[q]);
           }
         }
         const float nvref = next_vref(vref, sh.vs[n % kScaleSlots]);
         const bool grow = top > m + kLazy;
         float fix = 1.f;   // what the accumulator is multiplied with
         if (grow) {
-          const float r = ex2(m - top);   // 0 at the first
-          l *= r;
-          fix = r;
+          const float g = ex2(m - top);   // 0 at the first
+          l *= g;
+          fix = g;
           m = top;
         }
         if (nvref != vref) fix *= vref / nvref;
@@ -569,42 +624,43 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int b = 0; b < D / 32; ++b) {
-            uint32_t r[32];
-            tmem_ld32(O + 32 * b, r);
-            tmem_wait_ld();
+          for (int b = 0; b < D / 16; ++b) {
+            uint32_t o[16];
+            tmem_ld16(O + 16 * b, o);
+            tmem_wait_ld(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * fix);
-            tmem_st32(O + 32 * b, r);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+            tmem_st16(O + 16 * b, o);
           }
         }
-        const float base = (m == -INFINITY ? 0.f : m) - kShift;
+        const float base = kShift - (m == -INFINITY ? 0.f : m);
+        const uint64_t base2 = pair2(base, base);
+        uint64_t sum2 = 0;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          uint32_t r[32], w[16];
-          tmem_ld32(S + 32 * b, r);
-          tmem_wait_ld();
+          tmem_wait_ld(r[b & 1]);
+          if (b < 3) fetch(b + 1);
+          hide(b);
+          uint32_t w[16];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float f = ks[2 * b + half] * c;
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float x = ex2(fmaf(__uint_as_float(r[16 * half + i]), f, -base));
-              float y = ex2(fmaf(__uint_as_float(r[16 * half + i + 1]), f, -base));
-              if (masked) {
-                if (32 * b + 16 * half + i >= seen) x = 0.f;
-                if (32 * b + 16 * half + i + 1 >= seen) y = 0.f;
-              }
-              l += x + y;
-              const __half2 h = __floats2half2_rn(x, y);
-              w[8 * half + i / 2] = *reinterpret_cast<const uint32_t*>(&h);
-            }
+          for (int i = 0; i < 16; ++i) {
+            const float fq = f[2 * b + i / 8];
+            const float2 x = unpair2(fma2(pair2(__uint_as_float(r[b & 1][2 * i]), __uint_as_float(r[b & 1][2 * i + 1])),
+                                          pair2(fq, fq), base2));
+            const float e0 = ex2(x.x), e1 = ex2(x.y);
+            sum2 = add2(sum2, pair2(e0, e1));
+            const __half2 h = __floats2half2_rn(e0, e1);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
           }
           tmem_st16(S + 16 * b, w);   // over scores that this thread has read
+          if (b & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(pfull(t, b / 2));
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(pfull(t));
+        const float2 sum = unpair2(sum2);
+        l += sum.x + sum.y;
       }
       if (!ok) break;
       // ---- the part's result -----------------------------------------------------------------
@@ -619,7 +675,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         for (int b = 0; b < D / 32; ++b) {
           uint32_t r[32], w[16];
           tmem_ld32(O + 32 * b, r);
-          tmem_wait_ld();
+          tmem_wait_ld(r);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[2 * i]) * f, __uint_as_float(r[2 * i + 1]) * f);
@@ -637,7 +693,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         for (int b = 0; b < D / 32; ++b) {
           uint32_t r[32];
           tmem_ld32(O + 32 * b, r);
-          tmem_wait_ld();
+          tmem_wait_ld(r);
           if (live)
 #pragma unroll
             for (int i = 0; i < 8; ++i)

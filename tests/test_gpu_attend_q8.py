@@ -150,6 +150,7 @@ PROMPT = {
     "any_scale": dict(ctx=[300], rows=[30], hq=4, hkv=2, d=128, pow2=False),
     "value_scales": dict(ctx=[400], rows=[30], hq=4, hkv=2, d=128, v_spread=6),
     "idle": dict(ctx=[40, 10, 0], rows=[20, 5, 30], hq=4, hkv=4, d=64, idle=(1,)),
+    "mixed_tiles": dict(ctx=[2500 + 90 * i for i in range(10)], rows=[150, 20, 130, 9, 20, 140, 1, 30, 129, 128], hq=8, hkv=8, d=64),
     "unspoken_bound": dict(ctx=[9, 8], rows=[19, 14], hq=4, hkv=4, d=128, max_rows=0),
 }
 
