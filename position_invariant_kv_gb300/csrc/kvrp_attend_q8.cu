@@ -191,10 +191,6 @@ __device__ __forceinline__ uint32_t box_offset(int row, int chunk) {
 __device__ __forceinline__ void make_minus_inf(float& x) { asm volatile("mov.b32 %0, 0xff800000;" : "=f"(x)); }
 __device__ __forceinline__ void make_zero(uint32_t& x) { asm volatile("mov.b32 %0, 0;" : "=r"(x)); }
 
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // ---- decode ----------------------------------------------------------------------------
 constexpr int kMergeSlots = 2;   // warps that hand over their results at a time

@@ -53,6 +53,11 @@ cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // Bounded wait that ignores the abort flag: lets this CTA's own copies land before it exits.
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint32_t* status) {
   const long long t0 = clock64();

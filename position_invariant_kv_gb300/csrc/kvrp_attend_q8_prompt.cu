@@ -6,20 +6,24 @@
 //   - A unit is 256 rows of one (sequence, KV head): the rows x group pairs (token, query
 //     head) in order, so every row of the tile is used whatever the group, and K and V are
 //     loaded once for all query heads that share them.  It runs over its visible tokens in
-//     tiles of 128.  The list of (unit, token tile) is cut into equal contiguous shares, one
-//     a CTA, on the device; a unit that several CTAs share goes through the combine.
+//     tiles of 80 (head_dim 128) or 128 (64).  The list of (unit, token tile) is cut into equal
+//     contiguous shares, one a CTA, on the device; a unit that several CTAs share goes through
+//     the combine.
 //   - S = Q K^T by tcgen05 kind::f8f6f4: K goes from memory to the tensor cores as stored.
 //     q is split into two e4m3 parts, high and low, after its row was divided by a power of
 //     two: bf16's 8 significant bits are 4 + 4, so the parts are q exactly down to 2^-10 of
 //     the row's largest element and off by at most 2^-18 of it below.  Two products at
 //     twice the f16 rate cost what one would, without converting K.
-//   - O += P V by kind::f16: P as f16 from TMEM (it takes the place of its scores), V as f16 in
-//     shared memory, converted from e4m3 by four warps together with the page's scale
-//     relative to a running reference (a power of two): exact for power-of-two scales
-//     within 2^14 of each other.
-//   - Warps: two groups of four hold 128 rows each, a thread a row, and turn scores into
-//     weights while the tensor cores work on the other group's tile; four convert V; one
-//     issues TMA boxes (a page and head each), one the MMAs.
+//   - O += P V by kind::f16: P as f16 from TMEM, V as f16 in shared memory, converted from e4m3
+//     by four warps together with the page's scale relative to a running reference (a power
+//     of two): exact for power-of-two scales within 2^14 of each other.
+//   - Two 128-row Q tiles a CTA, each with its own softmax warps (a thread a row) and its own
+//     MMA issuer.  TMEM holds for each the accumulator, the scores and, apart from them, the
+//     weights: the next tile's scores are formed while this one's are being turned into
+//     weights.  That is why a token tile is 80 at head_dim 128: 80 columns of scores + 40 of
+//     weights + 128 of accumulator, twice, are what 512 columns hold.  (With 128 tokens and
+//     the weights in the scores' place each tile waited for both products: 911 TFLOP/s on
+//     4096 rows over 16441 tokens.)
 #include <algorithm>
 
 #include "kvrp_attend_q8.h"
@@ -29,20 +33,32 @@ namespace attend_q8 {
 
 namespace {
 
-constexpr int kTile = 128;                 // tokens of a K, V tile; rows of a Q tile
-constexpr int kPagesPerTile = kTile / kPage;
+constexpr int kRows = 128;                 // rows of a Q tile
 constexpr int kWarpsAll = 16, kThreadsAll = 32 * kWarpsAll;
-constexpr int kScaleSlots = 8;             // tiles whose scales are kept: K runs at most kKst + 1 ahead of the softmax
+constexpr int kScaleSlots = 8;             // tiles whose scales are kept
+constexpr int kMostPages = 8;              // pages of a token tile
 constexpr float kVShift = 7.f;             // V enters as v * vs * 2^7 / vref: up to 448 * 128 in f16
 
 template <int D>
 struct Prompt {
-  static constexpr int kQ = kTile * D;             // bytes of one e4m3 part of a Q tile
-  static constexpr int kKV = kTile * D;            // bytes of a raw K or V tile
-  static constexpr int kKst = 3, kVst = 2;         // stages of K, of raw V
-  static constexpr int kVc = kTile * D * 2;        // bytes of a converted V tile (two buffers)
+  static constexpr int kN = D == 128 ? 80 : 128;   // tokens of a tile
+  static constexpr int kP = kN / kPage;            // its pages
+  static constexpr int kP0 = (kP + 1) / 2;         // the pages whose weights are handed over first
+  static constexpr int kQ = kRows * D;             // bytes of one e4m3 part of a Q tile
+  static constexpr int kKV = kN * D;               // bytes of a raw K or V tile
+  static constexpr int kKst = 4, kVst = 3, kCst = 3;   // stages of K, of raw and of converted V
+  static constexpr int kVc = kN * D * 2;           // bytes of a converted V tile
+  // TMEM columns of Q tile t: scores, weights (two a column), accumulator
+  static __host__ __device__ constexpr int tmem_s(int t) { return t * 128; }
+  static __host__ __device__ constexpr int tmem_p(int t) { return D == 128 ? t * 128 + 80 : 256 + t * 64; }
+  static __host__ __device__ constexpr int tmem_o(int t) { return D == 128 ? 256 + t * 128 : 384 + t * 64; }
+  // Registers a thread of the softmax (which holds a row of scores), V and other warps: the
+  // 4 x 128 that the warp groups were launched with, shared out anew.
+  static constexpr int kRegsRow = D == 128 ? 168 : 184, kRegsV = 88, kRegsMisc = D == 128 ? 88 : 56;
+  static_assert(2 * kRegsRow + kRegsV + kRegsMisc <= 4 * 128, "more registers than the block holds");
   static constexpr int kOffK = 4 * kQ, kOffV = kOffK + kKst * kKV, kOffVc = kOffV + kVst * kKV;
-  static constexpr int kSmem = 1024 + kOffVc + 2 * kVc;
+  static constexpr int kSmem = 1024 + kOffVc + kCst * kVc;
+  static_assert(kSmem <= 227 * 1024 - 2048, "shared memory");
 };
 
 // ---- tensor-core pieces ------------------------------------------------------------------
@@ -57,9 +73,10 @@ __device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
   return d;
 }
 // N-major (the transposed operand): 64 f16 columns = 128 swizzled bytes a token, 8 tokens an atom.
+template <int N>
 __device__ __forceinline__ uint64_t desc_cols(uint32_t addr) {
   uint64_t d = (uint64_t)((addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(kTile * 128 >> 4) << 16;           // next 64 columns
+  d |= (uint64_t)(N * 128 >> 4) << 16;               // next 64 columns
   d |= (uint64_t)(1024 >> 4) << 32;                  // next 8 tokens
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
@@ -100,12 +117,25 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
+}
+// A value that is the same in all lanes, and known to be.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+// True in one lane, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(r));
+  return r != 0;
 }
 // Two fp32 operations an instruction.
 __device__ __forceinline__ uint64_t pair2(float a, float b) {
@@ -128,6 +158,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 // Until this thread's TMEM loads have arrived; names the registers they fill, so that nothing that
 // reads them can be moved ahead of the wait.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
@@ -158,9 +192,10 @@ struct Unit {
   int n_rt, n_kv, j0, j1;
   int64_t left;             // tiles of the share from j0 on
 };
+template <int N>
 __device__ __forceinline__ int tiles_of(int row0_col, int g, int rows, int len) {   // token tiles of a row tile
   const int last = min(rows - 1, (row0_col + kPromptRows - 1) / g);                 // its last token among the rows
-  return (len - rows + last + kTile) / kTile;
+  return (len - rows + last + N) / N;
 }
 __device__ __forceinline__ bool load_seq(const Params& p, int s, Unit& u, bool tell = false) {
   const bool ok = sequence(p.seqs, s, u.row0, u.rows, u.len) && u.rows <= p.max_rows;
@@ -169,28 +204,32 @@ __device__ __forceinline__ bool load_seq(const Params& p, int s, Unit& u, bool t
   return u.n_rt > 0;
 }
 // The tiles of sequence s over all its row tiles, by one warp (one head's worth).
+template <int N>
 __device__ __forceinline__ int64_t seq_cost(const Params& p, int s, bool tell) {
   Unit u;
   int64_t sum = 0;
   if (load_seq(p, s, u, tell && (threadIdx.x & 31) == 0))
-    for (int rt = threadIdx.x & 31; rt < u.n_rt; rt += 32) sum += tiles_of(rt * kPromptRows, p.g, u.rows, u.len);
+    for (int rt = threadIdx.x & 31; rt < u.n_rt; rt += 32) sum += tiles_of<N>(rt * kPromptRows, p.g, u.rows, u.len);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
 }
 struct Shared {
-  __align__(8) uint64_t bars[32];
-  float ks[kScaleSlots][kPagesPerTile], vs[kScaleSlots][kPagesPerTile];
+  __align__(8) uint64_t bars[40];
+  __align__(16) float ks[kScaleSlots][kMostPages];   // a tile's scales of K,
+  float vs[kScaleSlots][kMostPages];                 // of V,
+  float vs_top[kScaleSlots];                         // and the largest of V's
   int64_t cost[kWarpsAll];
   Unit first;
   int found;
   int abort_flag;
   uint32_t tmem;
 };
+template <int N>
 __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.seqs.n_seqs;
   int64_t mine = 0;
-  for (int s = warp; s < n; s += kWarpsAll) mine += seq_cost(p, s, blockIdx.x == 0) * p.Hkv;
+  for (int s = warp; s < n; s += kWarpsAll) mine += seq_cost<N>(p, s, blockIdx.x == 0) * p.Hkv;
   if (lane == 0) sh.cost[warp] = mine;
   __syncthreads();
   int64_t total = 0;
@@ -202,7 +241,7 @@ __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
   int s = 0;
   for (int s0 = 0; s0 < n; s0 += kWarpsAll) {   // the sequence that holds tile a
     __syncthreads();
-    const int64_t c = s0 + warp < n ? seq_cost(p, s0 + warp, false) * p.Hkv : 0;
+    const int64_t c = s0 + warp < n ? seq_cost<N>(p, s0 + warp, false) * p.Hkv : 0;
     if (lane == 0) sh.cost[warp] = c;
     __syncthreads();
     bool here = false;
@@ -220,7 +259,7 @@ __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
     int64_t at = a - before;   // tiles into the sequence
     for (int r0 = 0; r0 < u.n_rt; r0 += 32) {
       const int rt = r0 + lane;
-      const int t = rt < u.n_rt ? tiles_of(rt * kPromptRows, p.g, u.rows, u.len) : 0;
+      const int t = rt < u.n_rt ? tiles_of<N>(rt * kPromptRows, p.g, u.rows, u.len) : 0;
       int64_t sum = (int64_t)t * p.Hkv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -246,6 +285,7 @@ __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
   return true;
 }
 // The share's next unit; false at its end.
+template <int N>
 __device__ __forceinline__ bool next_unit(const Params& p, Unit& u) {
   u.left -= u.j1 - u.j0;
   if (u.left <= 0) return false;
@@ -256,21 +296,18 @@ __device__ __forceinline__ bool next_unit(const Params& p, Unit& u) {
       do ++u.s;
       while (!load_seq(p, u.s, u));
     }
-    u.n_kv = tiles_of(u.rt * kPromptRows, p.g, u.rows, u.len);
+    u.n_kv = tiles_of<N>(u.rt * kPromptRows, p.g, u.rows, u.len);
   }
   u.j0 = 0;
   u.j1 = (int)min((int64_t)u.n_kv, u.left);
   return true;
 }
 __device__ __forceinline__ int active_tiles(const Params& p, const Unit& u) {   // Q tiles with rows in them
-  return (int64_t)u.rows * p.g - (int64_t)u.rt * kPromptRows > kTile ? 2 : 1;
+  return (int64_t)u.rows * p.g - (int64_t)u.rt * kPromptRows > kRows ? 2 : 1;
 }
 // The reference of the value scales after a tile: a power of two at least the largest scale,
 // two octaves above it when it moves, so that it moves seldom.
-__device__ __forceinline__ float next_vref(float vref, const float* vs) {
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPagesPerTile; ++i) top = fmaxf(top, vs[i]);
+__device__ __forceinline__ float next_vref(float vref, float top) {
   if (!(top > vref)) return vref;
   const uint32_t e = (__float_as_uint(top) + 0x7fffffu) >> 23;   // 2^ceil(log2 top)
   return __uint_as_float(min(e + 2u, 254u) << 23);
@@ -281,35 +318,36 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ Params p) {
   using L = Prompt<D>;
+  constexpr int N = L::kN;
   extern __shared__ uint8_t raw_smem[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem = (smem_u32(raw_smem) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_u32(sh.bars);
   auto kfull = [&](int i) { return bar0 + 8u * i; };
-  auto kempty = [&](int i) { return bar0 + 8u * (3 + i); };
-  auto vfull = [&](int i) { return bar0 + 8u * (6 + i); };
-  auto vempty = [&](int i) { return bar0 + 8u * (8 + i); };
-  auto cfull = [&](int i) { return bar0 + 8u * (10 + i); };    // converted V
-  auto cempty = [&](int i) { return bar0 + 8u * (12 + i); };
-  auto qfull = [&](int t) { return bar0 + 8u * (14 + t); };
-  auto sfull = [&](int t) { return bar0 + 8u * (16 + t); };    // scores in TMEM
-  auto pfull = [&](int t, int half) { return bar0 + 8u * (18 + 2 * t + half); };   // weights in TMEM, accumulator corrected
-  auto ofull = [&](int t) { return bar0 + 8u * (22 + t); };    // accumulator updated
-  auto drained = [&](int t) { return bar0 + 8u * (24 + t); };
+  auto kempty = [&](int i) { return bar0 + 8u * (4 + i); };
+  auto vfull = [&](int i) { return bar0 + 8u * (8 + i); };
+  auto vempty = [&](int i) { return bar0 + 8u * (11 + i); };
+  auto cfull = [&](int i) { return bar0 + 8u * (14 + i); };    // converted V
+  auto cempty = [&](int i) { return bar0 + 8u * (17 + i); };
+  auto qfull = [&](int t) { return bar0 + 8u * (20 + t); };
+  auto sfull = [&](int t) { return bar0 + 8u * (22 + t); };    // scores in TMEM
+  auto sread = [&](int t) { return bar0 + 8u * (24 + t); };    // scores read, their place is free
+  auto pfull = [&](int t, int half) { return bar0 + 8u * (26 + 2 * t + half); };   // weights in TMEM, accumulator corrected
+  auto ofull = [&](int t) { return bar0 + 8u * (30 + t); };    // accumulator updated, the weights' place is free
+  auto drained = [&](int t) { return bar0 + 8u * (32 + t); };
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(kfull(i), 1), mbar_init(kempty(i), 2);   // both Q tiles
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(vfull(i), 1);
-      mbar_init(vempty(i), 128);
-      mbar_init(cfull(i), 128);
-      mbar_init(cempty(i), 2);
-      mbar_init(qfull(i), 128);
-      mbar_init(sfull(i), 1);
-      mbar_init(pfull(i, 0), 128);
-      mbar_init(pfull(i, 1), 128);
-      mbar_init(ofull(i), 1);
-      mbar_init(drained(i), 1);
+    for (int i = 0; i < L::kKst; ++i) mbar_init(kfull(i), 1), mbar_init(kempty(i), 2);   // both Q tiles
+    for (int i = 0; i < L::kVst; ++i) mbar_init(vfull(i), 1), mbar_init(vempty(i), 128);
+    for (int i = 0; i < L::kCst; ++i) mbar_init(cfull(i), 128), mbar_init(cempty(i), 2);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(qfull(t), 128);
+      mbar_init(sfull(t), 1);
+      mbar_init(sread(t), 128);
+      mbar_init(pfull(t, 0), 128);
+      mbar_init(pfull(t, 1), 128);
+      mbar_init(ofull(t), 1);
+      mbar_init(drained(t), 1);
     }
     sh.abort_flag = 0;
     mbar_init_fence();
@@ -321,194 +359,225 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
   }
   pdl_wait();
   pdl_launch_dependents();
-  const bool any = find_share(p, sh);
+  const bool any = find_share<N>(p, sh);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   volatile int* abort_p = &sh.abort_flag;
-  auto wait = [&](uint32_t bar, uint32_t parity) {   // the same answer in the whole warp
-    const bool ok = wait_phase(bar, parity, abort_p, p.status);
+  auto wait = [&](uint32_t bar, uint32_t parity) {   // bounded; the same answer in the whole warp
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+      const long long t0 = clock64();
+      while (!ok && !*abort_p) {
+        ok = mbar_try_wait(bar, parity);
+        if (!ok && clock64() - t0 > kTimeoutCycles) {
+          *abort_p = 1;
+          flag(p.status, KVRP_DEV_TIMEOUT);
+        }
+      }
+    }
     return __all_sync(0xffffffffu, ok) != 0;
   };
   Unit u = sh.first;
 
   if (!any) {
     if (tid == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  } else if (warp == 12) {
-    // ---- TMA: a lane a page ---------------------------------------------------------------
-    int n = 0, nk = 0, nv = 0;   // the tile, K and V tiles issued
-    bool ok = true;
-    do {
-      const int pages = (u.len + kPage - 1) / kPage;
-      for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
-        const int ks = n % L::kKst, vs = n % L::kVst, slot = n % kScaleSlots;
-        const int pg = j * kPagesPerTile + lane;
-        const bool mine = lane < kPagesPerTile && pg < pages;
-        int page = p.seqs.num_pages;   // past the pool: the box reads zeros
-        float fk = 0.f, fv = 0.f;
-        if (mine) {
-          const int e = p.seqs.block_tables[(int64_t)u.s * p.seqs.table_stride + pg];
-          if (e >= 0 && e < p.seqs.num_pages) {
-            page = e;
-            fk = p.k_scale[(int64_t)e * p.Hkv + u.h];
-            fv = p.v_scale[(int64_t)e * p.Hkv + u.h];
-          } else {
-            flag(p.status, KVRP_DEV_BAD_PAGE);
-          }
-        }
-        ok = wait(kempty(ks), ((n / L::kKst) & 1) ^ 1);   // the first pass finds the stage free
-        if (!ok) break;
-        // tile n - kScaleSlots has been turned into weights long ago: K runs at most kKst ahead
-        if (lane < kPagesPerTile) {
-          sh.ks[slot][lane] = fk;
-          sh.vs[slot][lane] = fv;
-        }
-        const uint32_t bytes = (uint32_t)min(kPagesPerTile, pages - j * kPagesPerTile) * kPage * D;
-        __syncwarp();
-        if (lane == 0) mbar_expect_tx(kfull(ks), bytes);
-        __syncwarp();
-        if (mine) tma_load_3d(smem + L::kOffK + ks * L::kKV + lane * kPage * D, &kmap, kfull(ks), u.h * D, 0, page);
-        ++nk;
-        ok = wait(vempty(vs), ((n / L::kVst) & 1) ^ 1);
-        if (!ok) break;
-        if (lane == 0) mbar_expect_tx(vfull(vs), bytes);
-        __syncwarp();
-        if (mine) tma_load_3d(smem + L::kOffV + vs * L::kKV + lane * kPage * D, &vmap, vfull(vs), u.h * D, 0, page);
-        ++nv;
-      }
-    } while (ok && next_unit(p, u));
-    if (!ok && lane == 0) {   // every issued copy lands before the CTA exits
-      for (int i = max(0, nk - L::kKst); i < nk; ++i) drain_wait(kfull(i % L::kKst), (i / L::kKst) & 1, p.status);
-      for (int i = max(0, nv - L::kVst); i < nv; ++i) drain_wait(vfull(i % L::kVst), (i / L::kVst) & 1, p.status);
-    }
-  } else if (warp == 13 || warp == 14) {
-    // ---- MMA: a warp a Q tile, so that one tile's waits leave the tensor cores to the other ----
-    const int t = warp - 13;
-    // descriptor: fp32 accumulator, M = 128; e4m3 (0) or f16 (0) operands; the second product's B is N-major
-    const uint32_t id_qk = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-    const uint32_t id_pv = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-    int n = 0;                   // tiles begun
-    uint32_t nq = 0, np = 0;     // units begun and tiles weighted, of this Q tile
-    bool ok = true;
-    do {
-      const int act = active_tiles(p, u);
-      if (t >= act) {            // no rows: the stages pass by, every phase observed (a wait tests a parity only)
+  } else if (warp >= 12) {
+    fewer_registers<L::kRegsMisc>();
+    if (warp == 12) {
+      // ---- TMA: a lane a page ---------------------------------------------------------------
+      int n = 0, nk = 0, nv = 0;   // the tile, K and V tiles issued
+      bool ok = true;
+      do {
+        const int pages = (u.len + kPage - 1) / kPage;
         for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
-          ok = wait(kfull(n % L::kKst), (n / L::kKst) & 1);
-          if (ok && lane == 0) mbar_arrive(kempty(n % L::kKst));
-          ok = ok && wait(cfull(n & 1), (n >> 1) & 1);
-          if (ok && lane == 0) mbar_arrive(cempty(n & 1));
+          const int ks = n % L::kKst, vs = n % L::kVst, slot = n % kScaleSlots;
+          const int pg = j * L::kP + lane;
+          const bool mine = lane < L::kP && pg < pages;
+          int page = p.seqs.num_pages;   // past the pool: the box reads zeros
+          float fk = 0.f, fv = 0.f;
+          if (mine) {
+            const int e = p.seqs.block_tables[(int64_t)u.s * p.seqs.table_stride + pg];
+            if (e >= 0 && e < p.seqs.num_pages) {
+              page = e;
+              fk = p.k_scale[(int64_t)e * p.Hkv + u.h];
+              fv = p.v_scale[(int64_t)e * p.Hkv + u.h];
+            } else {
+              flag(p.status, KVRP_DEV_BAD_PAGE);
+            }
+          }
+          ok = wait(kempty(ks), ((n / L::kKst) & 1) ^ 1);   // the first pass finds the stage free
+          if (!ok) break;
+          // Both issuers have done tile n - 4's scores, so both softmax groups have read tile n - 5's, and
+          // V's warps are past tile n - 5: nobody needs slot n - 8 any more.
+          if (lane < kMostPages) {
+            sh.ks[slot][lane] = fk;
+            sh.vs[slot][lane] = fv;
+          }
+          float most = fv;   // 0 in the lanes without a page
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          if (lane == 0) sh.vs_top[slot] = most;
+          const uint32_t bytes = (uint32_t)min(L::kP, pages - j * L::kP) * kPage * D;
           __syncwarp();
+          if (lane == 0) mbar_expect_tx(kfull(ks), bytes);
+          __syncwarp();
+          if (mine) tma_load_3d(smem + L::kOffK + ks * L::kKV + lane * kPage * D, &kmap, kfull(ks), u.h * D, 0, page);
+          ++nk;
+          ok = wait(vempty(vs), ((n / L::kVst) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(vfull(vs), bytes);
+          __syncwarp();
+          if (mine) tma_load_3d(smem + L::kOffV + vs * L::kKV + lane * kPage * D, &vmap, vfull(vs), u.h * D, 0, page);
+          ++nv;
         }
-        continue;
+      } while (ok && next_unit<N>(p, u));
+      if (!ok && lane == 0) {   // every issued copy lands before the CTA exits
+        for (int i = max(0, nk - L::kKst); i < nk; ++i) drain_wait(kfull(i % L::kKst), (i / L::kKst) & 1, p.status);
+        for (int i = max(0, nv - L::kVst); i < nv; ++i) drain_wait(vfull(i % L::kVst), (i / L::kVst) & 1, p.status);
       }
+    } else if (warp < 15) {
+      // ---- MMA: a warp a Q tile, so that one tile's waits leave the tensor cores to the other ----
+      // What the products take has to be the same in the whole warp, and to be seen to be.
+      const int t = (int)uniform(warp - 13);
+      const uint32_t s_tmem = uniform(tmem + L::tmem_s(t)), o_tmem = uniform(tmem + L::tmem_o(t)), p_tmem = uniform(tmem + L::tmem_p(t));
+      const uint64_t qd = desc_rows<D>(uniform(smem + 2 * t * L::kQ));   // an address is its low bits, in units of 16 bytes
+      // descriptor: fp32 accumulator, M = 128; e4m3 (0) or f16 (0) operands; the second product's B is N-major
+      const uint32_t id_qk = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+      const uint32_t id_pv = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+      int n = 0;                   // tiles begun
+      uint32_t nq = 0, np = 0;     // units begun and tiles weighted, of this Q tile
+      bool ok = true;
       auto scores = [&](int tile) {   // S_t = (Q_hi + Q_lo) K^T
-        if (lane == 0) {
-          const uint32_t k = smem + L::kOffK + (tile % L::kKst) * L::kKV;
+        const uint64_t kd = desc_rows<D>(uniform(smem + L::kOffK + (tile % L::kKst) * L::kKV));
+        if (elect_one()) {
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
-              mma_e4m3(tmem + t * kTile, desc_rows<D>(smem + (2 * t + part) * L::kQ + 32 * i), desc_rows<D>(k + 32 * i), id_qk,
-                       (part | i) != 0);
+              mma_e4m3(s_tmem, qd + (part * L::kQ + 32 * i) / 16, kd + 2 * i, id_qk, (part | i) != 0);
           mma_commit(sfull(t));
           mma_commit(kempty(tile % L::kKst));
         }
         __syncwarp();
       };
-      ok = wait(qfull(t), nq++ & 1) && wait(kfull(n % L::kKst), (n / L::kKst) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      scores(n);
-      for (int j = u.j0; j < u.j1; ++j, ++n, ++np) {
-        const int vb = n & 1;
-        for (int half = 0; half < 2 && ok; ++half) {
-          ok = wait(pfull(t, half), np & 1);
-          if (ok && half == 0) ok = wait(cfull(vb), (n >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t v = smem + L::kOffVc + vb * L::kVc;
+      auto values = [&](int tile, int from, int to, uint32_t more) {   // O_t += P_t V, pages [from, to) of the tile
+        const uint64_t vd = desc_cols<N>(uniform(smem + L::kOffVc + (tile % L::kCst) * L::kVc));
+        if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < kTile / 32; ++i) {
-              const int k = half * (kTile / 32) + i;
-              mma_f16_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * k, desc_cols(v + 2048 * k), id_pv, j > u.j0 || k > 0);
-            }
+          for (int i = from; i < to; ++i) mma_f16_ts(o_tmem, p_tmem + 8 * i, vd + 128 * i, id_pv, i > 0 ? 1u : more);
+          if (to == L::kP) {
+            mma_commit(ofull(t));
+            mma_commit(cempty(tile % L::kCst));
           }
-          __syncwarp();
-        }
-        if (!ok) break;
-        if (lane == 0) {
-          mma_commit(ofull(t));
-          mma_commit(cempty(vb));
         }
         __syncwarp();
-        if (j + 1 < u.j1) {   // the next scores take the place of these weights: wait until they have been read
-          ok = wait(kfull((n + 1) % L::kKst), ((n + 1) / L::kKst) & 1) && wait(ofull(t), np & 1);
+      };
+      do {
+        if (t >= active_tiles(p, u)) {   // no rows: the stages pass by, every phase observed (a wait tests a parity only)
+          for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
+            ok = wait(kfull(n % L::kKst), (n / L::kKst) & 1);
+            if (ok && lane == 0) mbar_arrive(kempty(n % L::kKst));
+            ok = ok && wait(cfull(n % L::kCst), (n / L::kCst) & 1);
+            if (ok && lane == 0) mbar_arrive(cempty(n % L::kCst));
+            __syncwarp();
+          }
+          continue;
+        }
+        ok = wait(qfull(t), nq++ & 1) && wait(kfull(n % L::kKst), (n / L::kKst) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        scores(n);
+        for (int j = u.j0; j < u.j1; ++j, ++n, ++np) {
+          ok = wait(sread(t), np & 1);
+          if (ok && j + 1 < u.j1) {   // the next scores, while these are being weighted
+            ok = wait(kfull((n + 1) % L::kKst), ((n + 1) / L::kKst) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            scores(n + 1);
+          }
+          ok = ok && wait(pfull(t, 0), np & 1) && wait(cfull(n % L::kCst), (n / L::kCst) & 1);
           if (!ok) break;
           tc_fence_after();
-          scores(n + 1);
+          const uint32_t more = uniform(j > u.j0);
+          values(n, 0, L::kP0, more);
+          ok = wait(pfull(t, 1), np & 1);
+          if (!ok) break;
+          tc_fence_after();
+          values(n, L::kP0, L::kP, 1);
         }
+      } while (ok && next_unit<N>(p, u));
+      if (!ok && elect_one()) {   // let the tensor cores finish before TMEM is freed
+        mma_commit(drained(t));
+        drain_wait(drained(t), 0, p.status);
       }
-    } while (ok && next_unit(p, u));
-    if (!ok && lane == 0) {   // let the tensor cores finish before TMEM is freed
-      mma_commit(drained(t));
-      drain_wait(drained(t), 0, p.status);
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp >= 8 && warp < 12) {
-    // ---- V: e4m3 to f16, a thread a token -----------------------------------------------------
-    const int tok = tid - 256;
+  } else if (warp >= 8) {
+    fewer_registers<L::kRegsV>();
+    // ---- V: e4m3 to f16, 16 features of a token at a time ---------------------------------------
+    constexpr int kChunks = D / 16, kEach = N * kChunks / 128;
+    const int at0 = tid - 256;
     int n = 0;
     bool ok = true;
     do {
       float vref = 0.f;
       for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
-        const int vs = n % L::kVst, vb = n & 1;
+        const int vs = n % L::kVst, vb = n % L::kCst, slot = n % kScaleSlots;
         ok = wait(vfull(vs), (n / L::kVst) & 1);
         if (!ok) break;
-        vref = next_vref(vref, sh.vs[n % kScaleSlots]);
-        const float mine = sh.vs[n % kScaleSlots][tok / kPage];
-        const float ratio = mine > 0.f ? mine / vref * 128.f : 0.f;
-        const __half2 r2 = __float2half2_rn(ratio);
-        const bool held = j * kTile + tok < u.len;   // a slot past the sequence may hold anything, NaN included
-        const uint32_t from = smem + L::kOffV + vs * L::kKV + tok * D;
-        uint32_t w[D / 4];
+        vref = next_vref(vref, sh.vs_top[slot]);
+        const int held = u.len - j * N;   // a slot past the sequence may hold anything, NaN included
+        const float scale = vref > 0.f ? 128.f / vref : 0.f;
+        const uint32_t from = smem + L::kOffV + vs * L::kKV;
+        uint4 w[kEach];
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint32_t at = from + (D == 128 ? ((c ^ (tok & 7)) << 4) : ((c ^ ((tok >> 1) & 3)) << 4));
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3]) : "r"(at));
+        for (int i = 0; i < kEach; ++i) {
+          const int tok = (at0 + 128 * i) / kChunks, c = (at0 + 128 * i) % kChunks;
+          const uint32_t at = from + tok * D + (D == 128 ? ((c ^ (tok & 7)) << 4) : ((c ^ ((tok >> 1) & 3)) << 4));
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w) : "r"(at));
+          if (tok >= held) w[i] = make_uint4(0, 0, 0, 0);
         }
         mbar_arrive(vempty(vs));
-        ok = wait(cempty(vb), ((n >> 1) & 1) ^ 1);
+        ok = wait(cempty(vb), ((n / L::kCst) & 1) ^ 1);
         if (!ok) break;
-        const uint32_t to = smem + L::kOffVc + vb * L::kVc + tok * 128;
+        const uint32_t to = smem + L::kOffVc + vb * L::kVc;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {   // 8 features, 16 bytes
-          uint32_t h[4];
+        for (int i = 0; i < kEach; ++i) {
+          const int tok = (at0 + 128 * i) / kChunks, c = (at0 + 128 * i) % kChunks;
+          const __half2 r2 = __float2half2_rn(sh.vs[slot][tok / kPage] * scale);
+          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          uint32_t h[8];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t x = held ? w[2 * c + i] : 0u;
-            const uint32_t a = q8::e4m3x2_to_f16x2((uint16_t)x), b = q8::e4m3x2_to_f16x2((uint16_t)(x >> 16));
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a = q8::e4m3x2_to_f16x2((uint16_t)x[e]), b = q8::e4m3x2_to_f16x2((uint16_t)(x[e] >> 16));
             const __half2 fa = __hmul2(*reinterpret_cast<const __half2*>(&a), r2);
             const __half2 fb = __hmul2(*reinterpret_cast<const __half2*>(&b), r2);
-            h[2 * i] = *reinterpret_cast<const uint32_t*>(&fa);
-            h[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&fb);
+            h[2 * e] = *reinterpret_cast<const uint32_t*>(&fa);
+            h[2 * e + 1] = *reinterpret_cast<const uint32_t*>(&fb);
           }
-          const uint32_t at = to + (c / 8) * (kTile * 128) + (((c % 8) ^ (tok & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+          // 32 bytes of the 64-column block c / 4, in two stores; the second block's threads take them in
+          // the other order, so that 8 threads touch 8 different 16-byte columns
+          const uint32_t row = to + (c / 4) * (N * 128) + tok * 128;
+          const bool other = (c & 4) != 0;
+          const int first = 2 * (c % 4) + (other ? 1 : 0);
+          const uint32_t a0 = row + ((first ^ (tok & 7)) << 4), a1 = row + (((first ^ 1) ^ (tok & 7)) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a0), "r"(other ? h[4] : h[0]), "r"(other ? h[5] : h[1]),
+                       "r"(other ? h[6] : h[2]), "r"(other ? h[7] : h[3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a1), "r"(other ? h[0] : h[4]), "r"(other ? h[1] : h[5]),
+                       "r"(other ? h[2] : h[6]), "r"(other ? h[3] : h[7]) : "memory");
         }
         fence_proxy_async_smem();
         mbar_arrive(cfull(vb));
       }
-    } while (ok && next_unit(p, u));
-  } else if (warp < 8) {
+    } while (ok && next_unit<N>(p, u));
+  } else {
+    more_registers<L::kRegsRow>();
     // ---- softmax: a thread a row ----------------------------------------------------------------
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t S = tmem + lanes + t * kTile, O = tmem + lanes + 2 * kTile + t * D;
+    const uint32_t S = tmem + lanes + L::tmem_s(t), O = tmem + lanes + L::tmem_o(t), P = tmem + lanes + L::tmem_p(t);
     int n = 0;                  // tiles of the share
     uint32_t ns = 0;            // of them, this Q tile's
     bool ok = true;
@@ -521,11 +590,11 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         n += u.j1 - u.j0;
         continue;
       }
-      const int64_t col = (int64_t)u.rt * kPromptRows + t * kTile + row;   // (token, query head) pair
+      const int64_t col = (int64_t)u.rt * kPromptRows + t * kRows + row;   // (token, query head) pair
       const bool live = col < (int64_t)u.rows * p.g;
       const int tok = (int)(col / p.g);
       const int limit = live ? u.len - u.rows + tok + 1 : 0;               // tokens the row sees
-      const int first_limit = u.len - u.rows + (int)(((int64_t)u.rt * kPromptRows + t * kTile) / p.g) + 1;
+      const int first_limit = u.len - u.rows + (int)(((int64_t)u.rt * kPromptRows + t * kRows) / p.g) + 1;
       const int64_t out_row = live ? (int64_t)(u.row0 + tok) * p.Hq + u.h * p.g + (int)(col % p.g) : 0;
       float c;   // scores times this are x, the exponent in base 2
       {
@@ -575,40 +644,36 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         ok = wait(sfull(t), ns & 1);
         if (!ok) break;
         tc_fence_after();
-        const float* ks = sh.ks[n % kScaleSlots];
-        const int seen = limit - j * kTile;   // columns below this are visible
-        const bool masked = (j + 1) * kTile > first_limit;
-        // Two passes over the row, 32 scores at a time, the next 32 on their way from TMEM meanwhile:
-        // a row in registers would leave none for the rest.
-        uint32_t r[2][32];
-        auto fetch = [&](int b) { tmem_ld32(S + 32 * b, r[b & 1]); };
-        auto hide = [&](int b) {
-          if (masked) {
+        uint32_t r[L::kP][16];   // the row's scores, by pages
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * b + i >= seen) asm volatile("mov.b32 %0, 0xff800000;" : "=r"(r[b & 1][i]));   // -inf
-          }
-        };
-        float f[kPagesPerTile];
-        float top = -INFINITY;
-        fetch(0);
+        for (int q = 0; q < L::kP; ++q) tmem_ld16(S + 16 * q, r[q]);
+        float f[L::kP];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          tmem_wait_ld(r[b & 1]);
-          fetch((b + 1) & 3);
-          hide(b);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int q = 2 * b + h;
-            f[q] = ks[q] * c;
-            if (f[q] == 0.f) f[q] = 1.f;   // no scale: no page, or one of zeros; -inf stays -inf
-            float a = __uint_as_float(r[b & 1][16 * h]);
-#pragma unroll
-            for (int i = 1; i < 16; ++i) a = fmaxf(a, __uint_as_float(r[b & 1][16 * h + i]));
-            top = fmaxf(top, a * f[q]);
-          }
+        for (int q = 0; q < L::kP; ++q) {
+          f[q] = sh.ks[n % kScaleSlots][q] * c;
+          if (f[q] == 0.f) f[q] = 1.f;   // no scale: no page, or one of zeros; -inf stays -inf
         }
-        const float nvref = next_vref(vref, sh.vs[n % kScaleSlots]);
+        const float nvref = next_vref(vref, sh.vs_top[n % kScaleSlots]);
+#pragma unroll
+        for (int q = 0; q < L::kP; ++q) tmem_wait_ld(r[q]);
+        tc_fence_before();
+        mbar_arrive(sread(t));
+        if (__builtin_expect((j + 1) * N > first_limit, 0)) {
+          const int seen = limit - j * N;   // columns below this are visible
+#pragma unroll
+          for (int q = 0; q < L::kP; ++q)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (16 * q + i >= seen) asm volatile("mov.b32 %0, 0xff800000;" : "=r"(r[q][i]));   // -inf
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < L::kP; ++q) {
+          float a = __uint_as_float(r[q][0]);
+#pragma unroll
+          for (int i = 1; i < 16; ++i) a = fmaxf(a, __uint_as_float(r[q][i]));
+          top = fmaxf(top, a * f[q]);
+        }
         const bool grow = top > m + kLazy;
         float fix = 1.f;   // what the accumulator is multiplied with
         if (grow) {
@@ -619,44 +684,41 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         }
         if (nvref != vref) fix *= vref / nvref;
         vref = nvref;
-        if (j > u.j0 && __any_sync(0xffffffffu, fix != 1.f)) {
+        if (j > u.j0) {   // the last tile's product has been added, and its weights read
           ok = wait(ofull(t), (ns - 1) & 1);
           if (!ok) break;
-          tc_fence_after();
+          if (__any_sync(0xffffffffu, fix != 1.f)) {
+            tc_fence_after();
 #pragma unroll
-          for (int b = 0; b < D / 16; ++b) {
-            uint32_t o[16];
-            tmem_ld16(O + 16 * b, o);
-            tmem_wait_ld(o);
+            for (int b = 0; b < D / 16; ++b) {
+              uint32_t o[16];
+              tmem_ld16(O + 16 * b, o);
+              tmem_wait_ld(o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
-            tmem_st16(O + 16 * b, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+              tmem_st16(O + 16 * b, o);
+            }
           }
         }
         const float base = kShift - (m == -INFINITY ? 0.f : m);
         const uint64_t base2 = pair2(base, base);
         uint64_t sum2 = 0;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          tmem_wait_ld(r[b & 1]);
-          if (b < 3) fetch(b + 1);
-          hide(b);
-          uint32_t w[16];
+        for (int q = 0; q < L::kP; ++q) {
+          uint32_t w[8];
+          const uint64_t f2 = pair2(f[q], f[q]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float fq = f[2 * b + i / 8];
-            const float2 x = unpair2(fma2(pair2(__uint_as_float(r[b & 1][2 * i]), __uint_as_float(r[b & 1][2 * i + 1])),
-                                          pair2(fq, fq), base2));
+          for (int i = 0; i < 8; ++i) {
+            const float2 x = unpair2(fma2(pair2(__uint_as_float(r[q][2 * i]), __uint_as_float(r[q][2 * i + 1])), f2, base2));
             const float e0 = ex2(x.x), e1 = ex2(x.y);
             sum2 = add2(sum2, pair2(e0, e1));
-            const __half2 h = __floats2half2_rn(e0, e1);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            w[i] = pack_f16(e0, e1);
           }
-          tmem_st16(S + 16 * b, w);   // over scores that this thread has read
-          if (b & 1) {
+          tmem_st8(P + 8 * q, w);
+          if (q == L::kP0 - 1 || q == L::kP - 1) {
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(pfull(t, b / 2));
+            mbar_arrive(pfull(t, q == L::kP - 1));
           }
         }
         const float2 sum = unpair2(sum2);
@@ -688,7 +750,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         }
         if (live && p.lse) p.lse[out_row] = (m + lg2(l)) * kLn2;
       } else {
-        float* to = p.partial + ((int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * p.cols + t * kTile + row) * (D + 4);
+        float* to = p.partial + ((int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * p.cols + t * kRows + row) * (D + 4);
 #pragma unroll
         for (int b = 0; b < D / 32; ++b) {
           uint32_t r[32];
@@ -702,7 +764,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         if (live) *reinterpret_cast<float4*>(to + D) = make_float4(m, om, l, 0.f);
       }
       tc_fence_before();   // the accumulator is read before the next unit's first product
-    } while (ok && next_unit(p, u));
+    } while (ok && next_unit<N>(p, u));
     if (tid == 0) p.meta[blockIdx.x] = meta;
   }
   __syncwarp();

@@ -7,8 +7,8 @@ units, each with one or two Q tiles that hold rows and some K, V tiles; every ro
 same list.  The model replays the waits and arrivals with the hardware's parity semantics
 (`Bar.try_wait` also checks the true phase) under random interleavings and latencies of
 copies and matrix products, and tracks what each buffer holds.  It fails on a wait that a
-wrong phase satisfies, on a product that reads another tile's operands, on scores that
-overwrite weights still being read, on a scale slot refilled too early, and on a deadlock.
+wrong phase satisfies, on a product that reads another tile's operands, on scores or weights
+that overwrite ones still to be read, on a scale slot refilled too early, and on a deadlock.
 
 The variant in which an issuer whose Q tile holds no rows lets the stages of that unit pass
 without observing them fails: it comes back more than one phase ahead of a stage's barrier
@@ -19,18 +19,18 @@ import pytest
 
 from test_pipeline_protocol import Bar
 
-KST, VST, SLOTS = 3, 2, 8
+KST, VST, CST, SLOTS = 4, 3, 3, 8
 
 
 def simulate(seed, units, observe=True, slots=SLOTS):
     rnd = random.Random(seed)
     kfull, kempty = [Bar(1) for _ in range(KST)], [Bar(2) for _ in range(KST)]
     vfull, vempty = [Bar(1) for _ in range(VST)], [Bar(1) for _ in range(VST)]
-    cfull, cempty = [Bar(1) for _ in range(2)], [Bar(2) for _ in range(2)]
-    qfull, sfull, ofull = ([Bar(1) for _ in range(2)] for _ in range(3))
+    cfull, cempty = [Bar(1) for _ in range(CST)], [Bar(2) for _ in range(CST)]
+    qfull, sfull, sread, ofull = ([Bar(1) for _ in range(2)] for _ in range(4))
     pfull = [[Bar(1), Bar(1)] for _ in range(2)]
-    k_held, v_held, c_held, slot_held = [None] * KST, [None] * VST, [None] * 2, [None] * slots
-    region = [None, None]            # what S_t / P_t's columns hold
+    k_held, v_held, c_held, slot_held = [None] * KST, [None] * VST, [None] * CST, [None] * slots
+    s_held, p_held = [None, None], [None, None]   # what S_t's and P_t's columns hold; P: (tile, halves) or a tile read
     clock, events = [0], []
     queue = [[], []]                 # each issuer's products and commits, executed in order
 
@@ -67,15 +67,16 @@ def simulate(seed, units, observe=True, slots=SLOTS):
         n = 0
         for act, tiles in units:
             for _ in range(tiles):
-                vs, vb = n % VST, n & 1
+                vs, vb = n % VST, n % CST
                 while not vfull[vs].try_wait(n // VST):
                     yield
                 assert v_held[vs] == n and slot_held[n % slots] == n
                 yield
                 assert v_held[vs] == n
                 vempty[vs].arrive()
-                while not cempty[vb].try_wait((n >> 1) - 1) if n >= 2 else False:
+                while not cempty[vb].try_wait(n // CST - 1) if n >= CST else False:
                     yield
+                assert slot_held[n % slots] == n, "the tile's scales were overwritten"
                 c_held[vb] = n
                 yield
                 cfull[vb].arrive()
@@ -92,16 +93,21 @@ def simulate(seed, units, observe=True, slots=SLOTS):
             for j in range(tiles):
                 while not sfull[t].try_wait(ns):
                     yield
-                assert region[t] == ("S", n), (region[t], n)
+                assert s_held[t] == n, (s_held[t], n)
                 assert slot_held[n % slots] == n, "the tile's scales were overwritten"
-                if j and rnd.random() < 0.4:         # the accumulator is corrected
+                yield
+                assert s_held[t] == n
+                s_held[t] = None                     # read
+                sread[t].arrive()
+                yield
+                if j:
                     while not ofull[t].try_wait(ns - 1):
                         yield
                 for half in range(2):
                     for _ in range(rnd.randint(1, 3)):
                         yield
-                    assert slot_held[n % slots] == n
-                    region[t] = ("P", n, half)
+                    assert half or p_held[t] is None, "weights still being read"
+                    p_held[t] = (n, half)
                     pfull[t][half].arrive()
                 n, ns = n + 1, ns + 1
             while not ofull[t].try_wait(ns - 1):
@@ -113,11 +119,22 @@ def simulate(seed, units, observe=True, slots=SLOTS):
         def scores(n):
             def run():
                 assert k_held[n % KST] == n, "scores of another tile's keys"
-                assert region[t] is None or region[t][0] == "read", region[t]
-                region[t] = ("S", n)
+                assert s_held[t] is None, "scores over scores that were not read"
+                s_held[t] = n
             queue[t].append(run)
             queue[t].append(sfull[t].arrive)
             queue[t].append(kempty[n % KST].arrive)
+
+        def values(n, half):
+            def run():
+                assert c_held[n % CST] == n, "weights times another tile's values"
+                assert p_held[t] and p_held[t][0] == n and p_held[t][1] >= half, (p_held[t], n, half)
+                if half:
+                    p_held[t] = None
+            queue[t].append(run)
+            if half:
+                queue[t].append(ofull[t].arrive)
+                queue[t].append(cempty[n % CST].arrive)
         for act, tiles in units:
             if t >= act:
                 for _ in range(tiles):
@@ -125,12 +142,12 @@ def simulate(seed, units, observe=True, slots=SLOTS):
                         while not kfull[n % KST].try_wait(n // KST):
                             yield
                         kempty[n % KST].arrive()
-                        while not cfull[n & 1].try_wait(n >> 1):
+                        while not cfull[n % CST].try_wait(n // CST):
                             yield
-                        cempty[n & 1].arrive()
+                        cempty[n % CST].arrive()
                     else:                            # the other issuer arrives twice instead
                         queue[t].append(kempty[n % KST].arrive)
-                        queue[t].append(cempty[n & 1].arrive)
+                        queue[t].append(cempty[n % CST].arrive)
                     n += 1
                 continue
             while not qfull[t].try_wait(nq):
@@ -140,27 +157,19 @@ def simulate(seed, units, observe=True, slots=SLOTS):
                 yield
             scores(n)
             for j in range(tiles):
+                while not sread[t].try_wait(np):
+                    yield
+                if j + 1 < tiles:
+                    while not kfull[(n + 1) % KST].try_wait((n + 1) // KST):
+                        yield
+                    scores(n + 1)
                 for half in range(2):
                     while not pfull[t][half].try_wait(np):
                         yield
                     if half == 0:
-                        while not cfull[n & 1].try_wait(n >> 1):
+                        while not cfull[n % CST].try_wait(n // CST):
                             yield
-
-                    def product(n=n, half=half):
-                        assert c_held[n & 1] == n, "weights times another tile's values"
-                        assert region[t][0] == "P" and region[t][1] == n and region[t][2] >= half
-                        if half:
-                            region[t] = ("read", n)
-                    queue[t].append(product)
-                queue[t].append(ofull[t].arrive)
-                queue[t].append(cempty[n & 1].arrive)
-                if j + 1 < tiles:
-                    while not kfull[(n + 1) % KST].try_wait((n + 1) // KST):
-                        yield
-                    while not ofull[t].try_wait(np):
-                        yield
-                    scores(n + 1)
+                    values(n, half)
                 n, np = n + 1, np + 1
                 yield
 
@@ -220,4 +229,4 @@ def test_model_catches_an_issuer_that_does_not_observe_a_unit():
 
 
 def test_model_catches_too_few_scale_slots():
-    assert _failures(slots=2) > 10
+    assert _failures(slots=3) > 10
