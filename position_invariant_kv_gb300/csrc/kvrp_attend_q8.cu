@@ -187,11 +187,6 @@ __device__ __forceinline__ uint32_t box_offset(int row, int chunk) {
   return (uint32_t)((row >> 1) * 128 + (((row ^ (row >> 1)) & 1) << 6) + ((chunk ^ ((row >> 1) & 2)) << 4));
 }
 
-// Assignments that the compiler keeps inside their branch.
-__device__ __forceinline__ void make_minus_inf(float& x) { asm volatile("mov.b32 %0, 0xff800000;" : "=f"(x)); }
-__device__ __forceinline__ void make_zero(uint32_t& x) { asm volatile("mov.b32 %0, 0;" : "=r"(x)); }
-
-
 // ---- decode ----------------------------------------------------------------------------
 constexpr int kMergeSlots = 2;   // warps that hand over their results at a time
 template <int D, int NT>
@@ -815,6 +810,8 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   if (!workspace || workspace_bytes < need) return fail(KVRP_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
   const int g = n_q_heads / n_kv_heads;
   const bool few = (int64_t)max_rows * g <= attend_q8::kMaxCols;
+  if ((int64_t)seqs->n_rows * g > INT32_MAX - attend_q8::kPromptRows)
+    return fail(KVRP_ERR_UNSUPPORTED, "%s: n_rows x n_q_heads / n_kv_heads must stay below 2^31", fn);
   const int hg = attend_q8::head_group(n_kv_heads);
   int sms = 0, smem_optin = 0;
   st = current_device_sms(&sms, &smem_optin);

@@ -53,6 +53,10 @@ cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Assignments that the compiler keeps inside their branch.
+__device__ __forceinline__ void make_minus_inf(float& x) { asm volatile("mov.b32 %0, 0xff800000;" : "=f"(x)); }
+__device__ __forceinline__ void make_zero(uint32_t& x) { asm volatile("mov.b32 %0, 0;" : "=r"(x)); }
+
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);

@@ -129,6 +129,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
+// Two f16 values to e4m3 (NaN stays NaN; nothing here is above 448).
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+  return r;
+}
 // A value that is the same in all lanes, and known to be.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 // True in one lane, the same one each time.
@@ -185,12 +191,17 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---- units and shares ------------------------------------------------------------------------
+// Beginning and ending a unit (its queries, the first scores, the results) takes a CTA as long as some
+// tiles do; the shares count that, or the CTAs of a batch's many short units finish last.
+constexpr int kUnitTiles = 4;
+
 // A unit's part inside this CTA's share: tiles [j0, j1) of its n_kv.
 struct Unit {
   int s, rt, h;             // sequence, row tile, KV head
   int row0, rows, len;      // the sequence
   int n_rt, n_kv, j0, j1;
-  int64_t left;             // tiles of the share from j0 on
+  int spent;                // cost of this part
+  int64_t left;             // cost of the share from here on
 };
 template <int N>
 __device__ __forceinline__ int tiles_of(int row0_col, int g, int rows, int len) {   // token tiles of a row tile
@@ -203,16 +214,23 @@ __device__ __forceinline__ bool load_seq(const Params& p, int s, Unit& u, bool t
   u.n_rt = ok ? (int)(((int64_t)u.rows * p.g + kPromptRows - 1) / kPromptRows) : 0;
   return u.n_rt > 0;
 }
-// The tiles of sequence s over all its row tiles, by one warp (one head's worth).
+// The cost of sequence s over all its row tiles, by one warp (one head's worth).
 template <int N>
 __device__ __forceinline__ int64_t seq_cost(const Params& p, int s, bool tell) {
   Unit u;
   int64_t sum = 0;
   if (load_seq(p, s, u, tell && (threadIdx.x & 31) == 0))
-    for (int rt = threadIdx.x & 31; rt < u.n_rt; rt += 32) sum += tiles_of<N>(rt * kPromptRows, p.g, u.rows, u.len);
+    for (int rt = threadIdx.x & 31; rt < u.n_rt; rt += 32) sum += kUnitTiles + tiles_of<N>(rt * kPromptRows, p.g, u.rows, u.len);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
+}
+// The unit's tiles among the costs [from, from + left): its first kUnitTiles stand for beginning and ending it.
+__device__ __forceinline__ void take(Unit& u, int from) {
+  const int to = (int)min((int64_t)u.n_kv + kUnitTiles, from + u.left);
+  u.j0 = max(0, from - kUnitTiles);
+  u.j1 = max(0, to - kUnitTiles);
+  u.spent = to - from;
 }
 struct Shared {
   __align__(8) uint64_t bars[40];
@@ -234,7 +252,7 @@ __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
   __syncthreads();
   int64_t total = 0;
   for (int w = 0; w < kWarpsAll; ++w) total += sh.cost[w];
-  const int64_t n_cta = min((int64_t)p.n_cta, total);
+  const int64_t n_cta = min((int64_t)p.n_cta, (total + kUnitTiles + 1) / (kUnitTiles + 2));
   if ((int)blockIdx.x >= n_cta) return false;
   const int64_t a = total * blockIdx.x / n_cta, b = total * (blockIdx.x + 1) / n_cta;
   int64_t before = 0;
@@ -259,22 +277,22 @@ __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
     int64_t at = a - before;   // tiles into the sequence
     for (int r0 = 0; r0 < u.n_rt; r0 += 32) {
       const int rt = r0 + lane;
-      const int t = rt < u.n_rt ? tiles_of<N>(rt * kPromptRows, p.g, u.rows, u.len) : 0;
-      int64_t sum = (int64_t)t * p.Hkv;
+      const int t = rt < u.n_rt ? tiles_of<N>(rt * kPromptRows, p.g, u.rows, u.len) : -kUnitTiles;
+      const int cost = t + kUnitTiles;
+      int64_t sum = (int64_t)cost * p.Hkv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += v;
       }
-      const int64_t lo = sum - (int64_t)t * p.Hkv;
+      const int64_t lo = sum - (int64_t)cost * p.Hkv;
       if (at >= lo && at < sum) {
         u.s = s;
         u.rt = rt;
         u.n_kv = t;
-        u.h = (int)((at - lo) / t);
-        u.j0 = (int)((at - lo) % t);
+        u.h = (int)((at - lo) / cost);
         u.left = b - a;
-        u.j1 = (int)min((int64_t)t, u.j0 + u.left);
+        take(u, (int)((at - lo) % cost));
         sh.first = u;
       }
       at -= __shfl_sync(0xffffffffu, sum, 31);
@@ -282,12 +300,12 @@ __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
     }
   }
   __syncthreads();
-  return true;
+  return sh.first.j1 > sh.first.j0 || sh.first.left > sh.first.spent;
 }
 // The share's next unit; false at its end.
 template <int N>
 __device__ __forceinline__ bool next_unit(const Params& p, Unit& u) {
-  u.left -= u.j1 - u.j0;
+  u.left -= u.spent;
   if (u.left <= 0) return false;
   if (++u.h == p.Hkv) {
     u.h = 0;
@@ -298,9 +316,8 @@ __device__ __forceinline__ bool next_unit(const Params& p, Unit& u) {
     }
     u.n_kv = tiles_of<N>(u.rt * kPromptRows, p.g, u.rows, u.len);
   }
-  u.j0 = 0;
-  u.j1 = (int)min((int64_t)u.n_kv, u.left);
-  return true;
+  take(u, 0);
+  return u.j1 > 0;
 }
 __device__ __forceinline__ int active_tiles(const Params& p, const Unit& u) {   // Q tiles with rows in them
   return (int64_t)u.rows * p.g - (int64_t)u.rt * kPromptRows > kRows ? 2 : 1;
@@ -335,7 +352,8 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
   auto sread = [&](int t) { return bar0 + 8u * (24 + t); };    // scores read, their place is free
   auto pfull = [&](int t, int half) { return bar0 + 8u * (26 + 2 * t + half); };   // weights in TMEM, accumulator corrected
   auto ofull = [&](int t) { return bar0 + 8u * (30 + t); };    // accumulator updated, the weights' place is free
-  auto drained = [&](int t) { return bar0 + 8u * (32 + t); };
+  auto pread = [&](int t) { return bar0 + 8u * (32 + t); };    // the first part of the weights read
+  auto drained = [&](int t) { return bar0 + 8u * (34 + t); };
   if (tid == 0) {
     for (int i = 0; i < L::kKst; ++i) mbar_init(kfull(i), 1), mbar_init(kempty(i), 2);   // both Q tiles
     for (int i = 0; i < L::kVst; ++i) mbar_init(vfull(i), 1), mbar_init(vempty(i), 128);
@@ -347,6 +365,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       mbar_init(pfull(t, 0), 128);
       mbar_init(pfull(t, 1), 128);
       mbar_init(ofull(t), 1);
+      mbar_init(pread(t), 1);
       mbar_init(drained(t), 1);
     }
     sh.abort_flag = 0;
@@ -412,7 +431,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           // Both issuers have done tile n - 4's scores, so both softmax groups have read tile n - 5's, and
           // V's warps are past tile n - 5: nobody needs slot n - 8 any more.
           if (lane < kMostPages) {
-            sh.ks[slot][lane] = fk;
+            sh.ks[slot][lane] = fmaxf(fk, 1e-30f);   // above 0, so that a masked score stays -inf
             sh.vs[slot][lane] = fv;
           }
           float most = fv;   // 0 in the lanes without a page
@@ -470,6 +489,8 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           if (to == L::kP) {
             mma_commit(ofull(t));
             mma_commit(cempty(tile % L::kCst));
+          } else {
+            mma_commit(pread(t));
           }
         }
         __syncwarp();
@@ -518,7 +539,12 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     fewer_registers<L::kRegsV>();
     // ---- V: e4m3 to f16, 16 features of a token at a time ---------------------------------------
     constexpr int kChunks = D / 16, kEach = N * kChunks / 128;
-    const int at0 = tid - 256;
+    // Thread x takes chunks x, x + 128, ...: four chunks of two tokens to 8 threads, whose stores (every
+    // other 16-byte column of a token's row, swizzled by its lowest bits) then touch all banks.
+    const int x0 = tid - 256;
+    const int tok0 = D == 128 ? (x0 >> 4) * 2 + ((x0 >> 2) & 1) : x0 >> 2;
+    const int c = D == 128 ? (x0 & 3) | ((x0 >> 1) & 4) : x0 & 3;
+    constexpr int kHop = 128 / kChunks;   // tokens between a thread's chunks: a multiple of 16
     int n = 0;
     bool ok = true;
     do {
@@ -534,10 +560,15 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         uint4 w[kEach];
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-          const int tok = (at0 + 128 * i) / kChunks, c = (at0 + 128 * i) % kChunks;
+          const int tok = tok0 + kHop * i;
           const uint32_t at = from + tok * D + (D == 128 ? ((c ^ (tok & 7)) << 4) : ((c ^ ((tok >> 1) & 3)) << 4));
           asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w) : "r"(at));
-          if (tok >= held) w[i] = make_uint4(0, 0, 0, 0);
+          if (__builtin_expect(tok >= held, 0)) {
+            make_zero(w[i].x);
+            make_zero(w[i].y);
+            make_zero(w[i].z);
+            make_zero(w[i].w);
+          }
         }
         mbar_arrive(vempty(vs));
         ok = wait(cempty(vb), ((n / L::kCst) & 1) ^ 1);
@@ -545,28 +576,25 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         const uint32_t to = smem + L::kOffVc + vb * L::kVc;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-          const int tok = (at0 + 128 * i) / kChunks, c = (at0 + 128 * i) % kChunks;
+          const int tok = tok0 + kHop * i;
           const __half2 r2 = __float2half2_rn(sh.vs[slot][tok / kPage] * scale);
           const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          uint32_t h[8];
+          const uint32_t row = to + (c / 4) * (N * 128) + tok * 128;   // of the 64-column block c / 4
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t a = q8::e4m3x2_to_f16x2((uint16_t)x[e]), b = q8::e4m3x2_to_f16x2((uint16_t)(x[e] >> 16));
-            const __half2 fa = __hmul2(*reinterpret_cast<const __half2*>(&a), r2);
-            const __half2 fb = __hmul2(*reinterpret_cast<const __half2*>(&b), r2);
-            h[2 * e] = *reinterpret_cast<const uint32_t*>(&fa);
-            h[2 * e + 1] = *reinterpret_cast<const uint32_t*>(&fb);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t v = x[2 * half + e];
+              const uint32_t a = q8::e4m3x2_to_f16x2((uint16_t)v), b = q8::e4m3x2_to_f16x2((uint16_t)(v >> 16));
+              const __half2 fa = __hmul2(*reinterpret_cast<const __half2*>(&a), r2);
+              const __half2 fb = __hmul2(*reinterpret_cast<const __half2*>(&b), r2);
+              h[2 * e] = *reinterpret_cast<const uint32_t*>(&fa);
+              h[2 * e + 1] = *reinterpret_cast<const uint32_t*>(&fb);
+            }
+            const uint32_t at = row + (((2 * (c % 4) + half) ^ (tok & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
           }
-          // 32 bytes of the 64-column block c / 4, in two stores; the second block's threads take them in
-          // the other order, so that 8 threads touch 8 different 16-byte columns
-          const uint32_t row = to + (c / 4) * (N * 128) + tok * 128;
-          const bool other = (c & 4) != 0;
-          const int first = 2 * (c % 4) + (other ? 1 : 0);
-          const uint32_t a0 = row + ((first ^ (tok & 7)) << 4), a1 = row + (((first ^ 1) ^ (tok & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a0), "r"(other ? h[4] : h[0]), "r"(other ? h[5] : h[1]),
-                       "r"(other ? h[6] : h[2]), "r"(other ? h[7] : h[3]) : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a1), "r"(other ? h[0] : h[4]), "r"(other ? h[1] : h[5]),
-                       "r"(other ? h[2] : h[6]), "r"(other ? h[3] : h[7]) : "memory");
         }
         fence_proxy_async_smem();
         mbar_arrive(cfull(vb));
@@ -582,6 +610,11 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     uint32_t ns = 0;            // of them, this Q tile's
     bool ok = true;
     int4 meta = make_int4(-1, 0, 0, 0);
+    // Where 16-byte chunk x of row r is in part 0 (high) or 1 (low) of this Q tile; between units the
+    // two rows of a thread's row are where its results are laid out for whole-row stores.
+    auto row_chunk = [&](int part, int r, int x) {
+      return smem + (2 * t + part) * L::kQ + r * D + (D == 128 ? ((x ^ (r & 7)) << 4) : ((x ^ ((r >> 1) & 3)) << 4));
+    };
     do {
       const bool begins = u.j0 == 0, ends = u.j1 == u.n_kv;
       if (begins && !ends) meta.x = u.s, meta.y = u.h, meta.w = u.rt;
@@ -590,51 +623,63 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         n += u.j1 - u.j0;
         continue;
       }
-      const int64_t col = (int64_t)u.rt * kPromptRows + t * kRows + row;   // (token, query head) pair
-      const bool live = col < (int64_t)u.rows * p.g;
-      const int tok = (int)(col / p.g);
+      const int col = u.rt * kPromptRows + t * kRows + row;   // (token, query head) pair: below 2^31, n_rows x group is
+      const bool live = col < u.rows * p.g;
+      const int tok = col / p.g;
       const int limit = live ? u.len - u.rows + tok + 1 : 0;               // tokens the row sees
-      const int first_limit = u.len - u.rows + (int)(((int64_t)u.rt * kPromptRows + t * kRows) / p.g) + 1;
-      const int64_t out_row = live ? (int64_t)(u.row0 + tok) * p.Hq + u.h * p.g + (int)(col % p.g) : 0;
-      float c;   // scores times this are x, the exponent in base 2
+      const int first_limit = u.len - u.rows + (u.rt * kPromptRows + t * kRows) / p.g + 1;
+      const int64_t out_row = live ? (int64_t)(u.row0 + tok) * p.Hq + u.h * p.g + col % p.g : 0;
+      // ---- q / 2^(e - 7) = high + low, both e4m3 -------------------------------------------------
+      // A warp its 32 rows, D / 16 lanes a row, so that a load takes whole rows (a row a thread took
+      // 4 us of load instructions).  The scores of the unit before have all been computed.
+      float c = 0.f;   // scores times this are x, the exponent in base 2
       {
-        // q / 2^(e - 7) = high + low, both e4m3; the scores of the unit before have all been computed
-        const uint4* at = reinterpret_cast<const uint4*>(
-            p.q + (live ? (u.row0 + tok) * p.q_stride + (int64_t)(u.h * p.g + (int)(col % p.g)) * D : 0));
-        uint32_t top = 0;
-        if (live)
+        constexpr int kLanes = D / 16, kStep = 32 / kLanes, kSteps = 32 / kStep;
+        const int first = u.rt * kPromptRows + t * kRows + (warp & 3) * 32, x = lane % kLanes;
+        const int cols = u.rows * p.g;
+        uint4 v[kSteps][2];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 v = at[i];
-            for (uint32_t x : {v.x, v.y, v.z, v.w}) top = max(top, max(x & 0x7fffu, (x >> 16) & 0x7fffu));
+        for (int i = 0; i < kSteps; ++i) {
+          const int rc = first + i * kStep + lane / kLanes;
+          v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+          if (rc < cols) {
+            const uint4* at = reinterpret_cast<const uint4*>(p.q + (u.row0 + rc / p.g) * p.q_stride +
+                                                             (int64_t)(u.h * p.g + rc % p.g) * D) + 2 * x;
+            v[i][0] = at[0];
+            v[i][1] = at[1];
           }
-        int e = (int)(top >> 7) - 127;
-        if (e == 128 || top == 0) e = 0;
-        e = min(max(e, -110), 126);
-        const float down = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-        c = p.scale * __uint_as_float((uint32_t)(127 - 7 + e) << 23);
-        const uint32_t to = smem + 2 * t * L::kQ + row * D;
+        }
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {   // 16 features
+        for (int i = 0; i < kSteps; ++i) {
+          const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+          uint32_t top = 0;   // the row's largest magnitude, as bf16 bits
+#pragma unroll
+          for (int k = 0; k < 8; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = top == 0 ? 0 : min(max((int)(top >> 7) - 127, -110), 126);
+          // a row with inf or NaN becomes NaN; |q| below 256 has 8 bits in f16 too, down to 2^-14
+          const float down = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + 7 - e) << 23);
           uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint4 v = live ? at[2 * i + k] : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int k = 0; k < 4; ++k) {
+            uint16_t h8[2], l8[2];
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-              float f[4] = {bf_lo(w[2 * z]) * down, bf_hi(w[2 * z]) * down, bf_lo(w[2 * z + 1]) * down, bf_hi(w[2 * z + 1]) * down};
-              const uint32_t h8 = q8::to_e4m3x4(f[0], f[1], f[2], f[3], 1.f);
-              const uint32_t ha = q8::e4m3x2_to_f16x2((uint16_t)h8), hb = q8::e4m3x2_to_f16x2((uint16_t)(h8 >> 16));
-              const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&ha));
-              const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&hb));
-              hi[2 * k + z] = h8;
-              lo[2 * k + z] = q8::to_e4m3x4(f[0] - fa.x, f[1] - fa.y, f[2] - fb.x, f[3] - fb.y, 1.f);
+              const uint32_t q2 = pack_f16(bf_lo(w[2 * k + z]) * down, bf_hi(w[2 * k + z]) * down);
+              h8[z] = f16x2_to_e4m3x2(q2);
+              const uint32_t back = q8::e4m3x2_to_f16x2(h8[z]);
+              const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&q2), *reinterpret_cast<const __half2*>(&back));
+              l8[z] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
             }
+            hi[k] = (uint32_t)h8[0] | ((uint32_t)h8[1] << 16);
+            lo[k] = (uint32_t)l8[0] | ((uint32_t)l8[1] << 16);
           }
-          const uint32_t off = to + (D == 128 ? ((i ^ (row & 7)) << 4) : ((i ^ ((row >> 1) & 3)) << 4));
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(off), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(off + L::kQ), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+          const uint32_t at = row_chunk(0, (warp & 3) * 32 + i * kStep + lane / kLanes, x);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::kQ), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+          const float mine = __shfl_sync(0xffffffffu, p.scale * __uint_as_float((uint32_t)(127 - 7 + e) << 23), (lane % kStep) * kLanes);
+          if (i == lane / kStep) c = mine;
         }
         fence_proxy_async_smem();
         mbar_arrive(qfull(t));
@@ -649,10 +694,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         for (int q = 0; q < L::kP; ++q) tmem_ld16(S + 16 * q, r[q]);
         float f[L::kP];
 #pragma unroll
-        for (int q = 0; q < L::kP; ++q) {
-          f[q] = sh.ks[n % kScaleSlots][q] * c;
-          if (f[q] == 0.f) f[q] = 1.f;   // no scale: no page, or one of zeros; -inf stays -inf
-        }
+        for (int q = 0; q < L::kP; ++q) f[q] = sh.ks[n % kScaleSlots][q] * c;
         const float nvref = next_vref(vref, sh.vs_top[n % kScaleSlots]);
 #pragma unroll
         for (int q = 0; q < L::kP; ++q) tmem_wait_ld(r[q]);
@@ -684,10 +726,12 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         }
         if (nvref != vref) fix *= vref / nvref;
         vref = nvref;
-        if (j > u.j0) {   // the last tile's product has been added, and its weights read
-          ok = wait(ofull(t), (ns - 1) & 1);
-          if (!ok) break;
-          if (__any_sync(0xffffffffu, fix != 1.f)) {
+        const bool correct = __any_sync(0xffffffffu, fix != 1.f);
+        if (j > u.j0) {
+          ok = wait(pread(t), (ns - 1) & 1);   // the place of the first part of the weights is free
+          if (ok && correct) {
+            ok = wait(ofull(t), (ns - 1) & 1);
+            if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int b = 0; b < D / 16; ++b) {
@@ -699,6 +743,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
               tmem_st16(O + 16 * b, o);
             }
           }
+          if (!ok) break;
         }
         const float base = kShift - (m == -INFINITY ? 0.f : m);
         const uint64_t base2 = pair2(base, base);
@@ -714,6 +759,10 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
             sum2 = add2(sum2, pair2(e0, e1));
             w[i] = pack_f16(e0, e1);
           }
+          if (q == L::kP0 && j > u.j0) {   // and the place of the second part
+            ok = wait(ofull(t), (ns - 1) & 1);
+            if (!ok) break;
+          }
           tmem_st8(P + 8 * q, w);
           if (q == L::kP0 - 1 || q == L::kP - 1) {
             tmem_wait_st();
@@ -721,6 +770,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
             mbar_arrive(pfull(t, q == L::kP - 1));
           }
         }
+        if (!ok) break;
         const float2 sum = unpair2(sum2);
         l += sum.x + sum.y;
       }
@@ -731,37 +781,62 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       tc_fence_after();
       l *= 0x1p-7f;   // 2^-kShift
       const float om = m + lg2(vref) - kVShift;   // the accumulator holds sums of 2^(x - om + 7) times v
-      if (begins && ends) {
-        const float f = l == 0.f ? 0.f : vref * 0x1p-14f / l;
+      // Rows are laid out in shared memory, in the Q tile that the finished unit no longer needs, and
+      // leave by whole rows (32 rows' 16 bytes an instruction took 2 us a unit): kRowChunks chunks a pass.
+      constexpr int kRowChunks = D / 8, kHalf = D / 16;   // 16-byte chunks of the two parts, of one
+      const bool whole = begins && ends;
+      const float f = l == 0.f ? 0.f : vref * 0x1p-14f / l;
+      float* part = p.partial + ((int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * p.cols + t * kRows) * (D + 4);
+      auto stage = [&](int x, uint32_t a, uint32_t b2, uint32_t c2, uint32_t d) {
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row_chunk(x / kHalf, row, x % kHalf)), "r"(a), "r"(b2), "r"(c2), "r"(d) : "memory");
+      };
+      for (int pass = 0; pass < (whole ? 1 : 2); ++pass) {
+        if (whole) {
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) {
-          uint32_t r[32], w[16];
-          tmem_ld32(O + 32 * b, r);
-          tmem_wait_ld(r);
+          for (int b = 0; b < D / 32; ++b) {
+            uint32_t r[32], w[16];
+            tmem_ld32(O + 32 * b, r);
+            tmem_wait_ld(r);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[2 * i]) * f, __uint_as_float(r[2 * i + 1]) * f);
-            w[i] = *reinterpret_cast<const uint32_t*>(&v);
+            for (int i = 0; i < 16; ++i) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[2 * i]) * f, __uint_as_float(r[2 * i + 1]) * f);
+              w[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) stage(4 * b + i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           }
-          if (live)
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              reinterpret_cast<uint4*>(p.out + out_row * D + 32 * b)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          for (int b = 0; b < D / 64; ++b) {
+            uint32_t r[32];
+            tmem_ld32(O + pass * (D / 2) + 32 * b, r);
+            tmem_wait_ld(r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) stage(8 * b + i, r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+          }
         }
-        if (live && p.lse) p.lse[out_row] = (m + lg2(l)) * kLn2;
-      } else {
-        float* to = p.partial + ((int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * p.cols + t * kRows + row) * (D + 4);
-#pragma unroll
-        for (int b = 0; b < D / 32; ++b) {
-          uint32_t r[32];
-          tmem_ld32(O + 32 * b, r);
-          tmem_wait_ld(r);
-          if (live)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<uint4*>(to + 32 * b)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        __syncwarp();
+        constexpr int kAtOnce = 32 / kRowChunks;
+        const int x = lane % kRowChunks;
+#pragma unroll 4
+        for (int i = 0; i < 32 / kAtOnce; ++i) {
+          const int from = i * kAtOnce + lane / kRowChunks;   // the lane whose row this is
+          const int64_t to_row = __shfl_sync(0xffffffffu, out_row, from);
+          const bool to_live = __shfl_sync(0xffffffffu, live, from);
+          const int r = (warp & 3) * 32 + from;
+          uint4 v;
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(row_chunk(x / kHalf, r, x % kHalf)));
+          if (to_live) {
+            if (whole) reinterpret_cast<uint4*>(p.out + to_row * D)[x] = v;
+            else reinterpret_cast<uint4*>(part + (int64_t)r * (D + 4) + pass * (D / 2))[x] = v;
+          }
         }
-        if (live) *reinterpret_cast<float4*>(to + D) = make_float4(m, om, l, 0.f);
+        __syncwarp();
+      }
+      if (live) {
+        if (!whole) *reinterpret_cast<float4*>(part + (int64_t)row * (D + 4) + D) = make_float4(m, om, l, 0.f);
+        else if (p.lse) p.lse[out_row] = (m + lg2(l)) * kLn2;
       }
       tc_fence_before();   // the accumulator is read before the next unit's first product
     } while (ok && next_unit<N>(p, u));

@@ -27,10 +27,10 @@ def simulate(seed, units, observe=True, slots=SLOTS):
     kfull, kempty = [Bar(1) for _ in range(KST)], [Bar(2) for _ in range(KST)]
     vfull, vempty = [Bar(1) for _ in range(VST)], [Bar(1) for _ in range(VST)]
     cfull, cempty = [Bar(1) for _ in range(CST)], [Bar(2) for _ in range(CST)]
-    qfull, sfull, sread, ofull = ([Bar(1) for _ in range(2)] for _ in range(4))
+    qfull, sfull, sread, pread, ofull = ([Bar(1) for _ in range(2)] for _ in range(5))
     pfull = [[Bar(1), Bar(1)] for _ in range(2)]
     k_held, v_held, c_held, slot_held = [None] * KST, [None] * VST, [None] * CST, [None] * slots
-    s_held, p_held = [None, None], [None, None]   # what S_t's and P_t's columns hold; P: (tile, halves) or a tile read
+    s_held, p_held = [None, None], [[None, None], [None, None]]   # the tiles in S_t's columns and in P_t's two parts
     clock, events = [0], []
     queue = [[], []]                 # each issuer's products and commits, executed in order
 
@@ -100,14 +100,16 @@ def simulate(seed, units, observe=True, slots=SLOTS):
                 s_held[t] = None                     # read
                 sread[t].arrive()
                 yield
-                if j:
-                    while not ofull[t].try_wait(ns - 1):
-                        yield
+                correct = j and rnd.random() < 0.3
                 for half in range(2):
                     for _ in range(rnd.randint(1, 3)):
                         yield
-                    assert half or p_held[t] is None, "weights still being read"
-                    p_held[t] = (n, half)
+                    if j:                            # the accumulator is corrected, or this part's place is free
+                        while not (ofull if half or correct else pread)[t].try_wait(ns - 1):
+                            yield
+                    assert p_held[t][half] is None, "weights still being read"
+                    assert not correct or half or p_held[t][1] is None
+                    p_held[t][half] = n
                     pfull[t][half].arrive()
                 n, ns = n + 1, ns + 1
             while not ofull[t].try_wait(ns - 1):
@@ -128,11 +130,12 @@ def simulate(seed, units, observe=True, slots=SLOTS):
         def values(n, half):
             def run():
                 assert c_held[n % CST] == n, "weights times another tile's values"
-                assert p_held[t] and p_held[t][0] == n and p_held[t][1] >= half, (p_held[t], n, half)
-                if half:
-                    p_held[t] = None
+                assert p_held[t][half] == n, (p_held[t], n, half)
+                p_held[t][half] = None
             queue[t].append(run)
-            if half:
+            if not half:
+                queue[t].append(pread[t].arrive)
+            else:
                 queue[t].append(ofull[t].arrive)
                 queue[t].append(cempty[n % CST].arrive)
         for act, tiles in units:
