@@ -810,8 +810,8 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   if (!workspace || workspace_bytes < need) return fail(KVRP_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
   const int g = n_q_heads / n_kv_heads;
   const bool few = (int64_t)max_rows * g <= attend_q8::kMaxCols;
-  if ((int64_t)seqs->n_rows * g > INT32_MAX - attend_q8::kPromptRows)
-    return fail(KVRP_ERR_UNSUPPORTED, "%s: n_rows x n_q_heads / n_kv_heads must stay below 2^31", fn);
+  if ((int64_t)seqs->n_rows * n_q_heads >= 1ll << 32 || (int64_t)seqs->n_rows * g >= (1 << 28) - attend_q8::kPromptRows)
+    return fail(KVRP_ERR_UNSUPPORTED, "%s: n_rows x n_q_heads must stay below 2^32, n_rows x group below 2^28", fn);
   const int hg = attend_q8::head_group(n_kv_heads);
   int sms = 0, smem_optin = 0;
   st = current_device_sms(&sms, &smem_optin);
@@ -832,6 +832,7 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   p.Hq = n_q_heads;
   p.Hkv = n_kv_heads;
   p.g = g;
+  p.g_inverse = ((1ull << 32) + g - 1) / g;
   p.n_cta = std::min(attend_q8::kMaxCtas, few ? attend_q8::kMaxCtasPerSm * sms : sms);
   p.cols = few ? hg * max_rows * g : attend_q8::kPromptRows;
   p.max_rows = max_rows;

@@ -37,6 +37,7 @@ constexpr int kRows = 128;                 // rows of a Q tile
 constexpr int kWarpsAll = 16, kThreadsAll = 32 * kWarpsAll;
 constexpr int kScaleSlots = 8;             // tiles whose scales are kept
 constexpr int kMostPages = 8;              // pages of a token tile
+constexpr uint32_t kNoRow = 0xffffffffu;   // a row of the tile that no query fills
 constexpr float kVShift = 7.f;             // V enters as v * vs * 2^7 / vref: up to 448 * 128 in f16
 
 template <int D>
@@ -193,7 +194,7 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // ---- units and shares ------------------------------------------------------------------------
 // Beginning and ending a unit (its queries, the first scores, the results) takes a CTA as long as some
 // tiles do; the shares count that, or the CTAs of a batch's many short units finish last.
-constexpr int kUnitTiles = 4;
+constexpr int kUnitTiles = 6;
 
 // A unit's part inside this CTA's share: tiles [j0, j1) of its n_kv.
 struct Unit {
@@ -322,6 +323,8 @@ __device__ __forceinline__ bool next_unit(const Params& p, Unit& u) {
 __device__ __forceinline__ int active_tiles(const Params& p, const Unit& u) {   // Q tiles with rows in them
   return (int64_t)u.rows * p.g - (int64_t)u.rt * kPromptRows > kRows ? 2 : 1;
 }
+// x / g for 0 <= x < 2^28 (the host keeps rows x group below): by a product with 2^32 / g, rounded up.
+__device__ __forceinline__ int over_group(const Params& p, int x) { return (int)((uint64_t)(uint32_t)x * p.g_inverse >> 32); }
 // The reference of the value scales after a tile: a power of two at least the largest scale,
 // two octaves above it when it moves, so that it moves seldom.
 __device__ __forceinline__ float next_vref(float vref, float top) {
@@ -625,10 +628,10 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       }
       const int col = u.rt * kPromptRows + t * kRows + row;   // (token, query head) pair: below 2^31, n_rows x group is
       const bool live = col < u.rows * p.g;
-      const int tok = col / p.g;
+      const int tok = over_group(p, col);
       const int limit = live ? u.len - u.rows + tok + 1 : 0;               // tokens the row sees
-      const int first_limit = u.len - u.rows + (u.rt * kPromptRows + t * kRows) / p.g + 1;
-      const int64_t out_row = live ? (int64_t)(u.row0 + tok) * p.Hq + u.h * p.g + col % p.g : 0;
+      const int first_limit = u.len - u.rows + over_group(p, u.rt * kPromptRows + t * kRows) + 1;
+      const uint32_t out_row = live ? (uint32_t)(u.row0 + tok) * p.Hq + u.h * p.g + (col - tok * p.g) : kNoRow;
       // ---- q / 2^(e - 7) = high + low, both e4m3 -------------------------------------------------
       // A warp its 32 rows, D / 16 lanes a row, so that a load takes whole rows (a row a thread took
       // 4 us of load instructions).  The scores of the unit before have all been computed.
@@ -643,18 +646,20 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           const int rc = first + i * kStep + lane / kLanes;
           v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
           if (rc < cols) {
-            const uint4* at = reinterpret_cast<const uint4*>(p.q + (u.row0 + rc / p.g) * p.q_stride +
-                                                             (int64_t)(u.h * p.g + rc % p.g) * D) + 2 * x;
+            const int tk = over_group(p, rc);
+            const uint4* at = reinterpret_cast<const uint4*>(p.q + (u.row0 + tk) * p.q_stride + (u.h * p.g + rc - tk * p.g) * D) + 2 * x;
             v[i][0] = at[0];
             v[i][1] = at[1];
           }
         }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
-          uint32_t top = 0;   // the row's largest magnitude, as bf16 bits
+          const uint4 v0 = v[i][0], v1 = v[i][1];
+          const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+          uint32_t most = 0;   // the row's largest magnitude, as bf16 bits
 #pragma unroll
-          for (int k = 0; k < 8; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+          for (int k = 0; k < 8; ++k) most = __vmaxu2(most, w[k] & 0x7fff7fffu);
+          uint32_t top = max(most & 0xffffu, most >> 16);
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
           const int e = top == 0 ? 0 : min(max((int)(top >> 7) - 127, -110), 126);
@@ -790,6 +795,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       auto stage = [&](int x, uint32_t a, uint32_t b2, uint32_t c2, uint32_t d) {
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row_chunk(x / kHalf, row, x % kHalf)), "r"(a), "r"(b2), "r"(c2), "r"(d) : "memory");
       };
+#pragma unroll 1
       for (int pass = 0; pass < (whole ? 1 : 2); ++pass) {
         if (whole) {
 #pragma unroll
@@ -816,20 +822,22 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           }
         }
         __syncwarp();
+        // kAtOnce rows an instruction; the rows' swizzle differs by constants, so an address is one xor away
         constexpr int kAtOnce = 32 / kRowChunks;
-        const int x = lane % kRowChunks;
-#pragma unroll 4
+        const int x = lane % kRowChunks, sub = lane / kRowChunks;
+        const uint32_t from = row_chunk(x / kHalf, (warp & 3) * 32 + sub, x % kHalf);
+        uint8_t* to_out = reinterpret_cast<uint8_t*>(p.out) + 16 * x;
+        uint8_t* to_part = reinterpret_cast<uint8_t*>(part + (int64_t)((warp & 3) * 32 + sub) * (D + 4) + pass * (D / 2)) + 16 * x;
+#pragma unroll
         for (int i = 0; i < 32 / kAtOnce; ++i) {
-          const int from = i * kAtOnce + lane / kRowChunks;   // the lane whose row this is
-          const int64_t to_row = __shfl_sync(0xffffffffu, out_row, from);
-          const bool to_live = __shfl_sync(0xffffffffu, live, from);
-          const int r = (warp & 3) * 32 + from;
+          const uint32_t to_row = __shfl_sync(0xffffffffu, out_row, i * kAtOnce + sub);
+          const uint32_t swizzle = (D == 128 ? (i * kAtOnce) & 6 : (i * kAtOnce / 2) & 2) << 4;
           uint4 v;
           asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(row_chunk(x / kHalf, r, x % kHalf)));
-          if (to_live) {
-            if (whole) reinterpret_cast<uint4*>(p.out + to_row * D)[x] = v;
-            else reinterpret_cast<uint4*>(part + (int64_t)r * (D + 4) + pass * (D / 2))[x] = v;
+                       : "r"((from ^ swizzle) + i * kAtOnce * D));
+          if (to_row != kNoRow) {
+            if (whole) *reinterpret_cast<uint4*>(to_out + (int64_t)to_row * (2 * D)) = v;
+            else *reinterpret_cast<uint4*>(to_part + i * kAtOnce * (D + 4) * 4) = v;
           }
         }
         __syncwarp();
