@@ -7,18 +7,26 @@
 // a_i = position * theta^(-2i/d), all in fp32 and rounded once at the store; values
 // pass through.  What it costs is bytes: every row is read once and written once.
 //   - The unit is a run: the new rows of one sequence inside one 16-token page, for one
-//     head, held by one warp in registers (16 values a lane and step).  A run is exactly
-//     the part of an 8-bit block that the call writes, so the block's amax is a warp
-//     reduction and the rows are rounded once, straight from fp32.
+//     head, held by one warp in registers as they came.  A run is exactly the part of an
+//     8-bit block that the call writes, so the block's amax is a warp reduction and the rows
+//     are rounded once, straight from fp32.
 //   - A CTA takes one run and a share of its heads.  cos and sin of the run's rows are
 //     formed once per CTA, in shared memory, while the first head's loads are in flight:
 //     per head they would cost more issue slots than the rotation.
 //   - The angle mod 2 pi comes from 64-bit integer arithmetic: the frequency as a
 //     fraction of a turn in units of 2^-64, times the position, wraps by itself; fp64
 //     (1/64 of the fp32 rate here) is not touched.
+//   - 80 registers a thread, three CTAs an SM: what bounds a prompt is how many loads are in
+//     flight.  The 8-bit form loads the next head's rows as it is done with this one's; in the
+//     bf16 form that measured slower (40.7 against 35.6 us) and it loads a head at a time.
+//   Measured: 8 sequences, 8218 rows of 28 + 2 x 4 heads x 128 with norms and M-RoPE, 160 MB, 35.6 us
+//   (4.5 TB/s, 67% of a copy); 6.1 thousand rows of 32 + 2 x 32 heads into 8 bits, 278 MB, 57.9 us (72%);
+//   one row of each of 16 sequences 3.0 us, of 64 into 8 bits 4.5 us (launch and latency).
 //
-// pack_kernel.  One warp a block: 16 rows of one head of one layer in registers, amax,
-// scale, one rounding, 16 rows out.
+// pack_kernel.  One warp a block: 16 rows of one head of one layer in registers, amax (two bf16
+// magnitudes an instruction), scale, one rounding, 16 rows out.  63 registers keep 32 warps of loads
+// in flight on an SM: 28 layers x 4096 tokens x 4 heads x 128, 352 MB, in 52.7 us, a copy's rate
+// (72.4 us when the largest magnitude was taken in fp32: 106 registers, half the warps).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -26,6 +34,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "kvrp.h"
 #include "kvrp_plan.h"
@@ -127,14 +136,25 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* x) {
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ uint4 pack8(const float* x) {
+// The same as fp32 pairs, and back.
+__device__ __forceinline__ void widen8(const uint4& u, uint64_t* x) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = pair2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ uint4 narrow8(const uint64_t* x) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    const float2 v = unpair2(x[i]);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint32_t pairs_to_e4m3x4(uint64_t a, uint64_t b, float inv) {
+  const float2 x = unpair2(a), y = unpair2(b);
+  return q8::to_e4m3x4(x.x, x.y, y.x, y.y, inv);
 }
 __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
@@ -168,7 +188,7 @@ __device__ __forceinline__ void rescale_block(uint8_t* block, int64_t row_stride
 }
 
 template <int D, bool kQ8>
-__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_constant__ Params p) {
   constexpr int kLanes = D / 16;          // lanes of a row: 8 features and their 8 partners each
   constexpr int kStep = 32 / kLanes;      // rows a warp holds side by side
   constexpr int kSteps = kPage / kStep;
@@ -184,25 +204,26 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
   const int heads = p.Hq + 2 * p.Hkv, half = D / 2;
   const int first = p.h0 + (blockIdx.x % p.splits) * kWarps + warp, hop = p.splits * kWarps;
 
+  // The rows of one head, as they came: a lane's 8 features and their partners, for each step of rows.
   uint4 raw[kSteps][2];
-  auto load = [&](int h) {
+  auto load_step = [&](int h, int i) {
     const uint16_t* base;
     int64_t stride;
     if (h < p.Hq) base = p.q + (int64_t)h * D, stride = p.q_stride;
     else if (h < p.Hq + p.Hkv) base = p.k + (int64_t)(h - p.Hq) * D, stride = p.k_stride;
     else base = p.v + (int64_t)(h - p.Hq - p.Hkv) * D, stride = p.v_stride;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int r = i * kStep + sub;
-      raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
-      if (r < run.n) {
-        const uint16_t* at = base + (run.row0 + r) * stride + l * 8;
-        raw[i][0] = *reinterpret_cast<const uint4*>(at);
-        raw[i][1] = *reinterpret_cast<const uint4*>(at + half);
-      }
+    const int r = i * kStep + sub;
+    raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
+    if (r < run.n) {
+      const uint16_t* at = base + (run.row0 + r) * stride + l * 8;
+      raw[i][0] = *reinterpret_cast<const uint4*>(at);
+      raw[i][1] = *reinterpret_cast<const uint4*>(at + half);
     }
   };
-  if (first < heads) load(first);
+  if (first < heads) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) load_step(first, i);
+  }
 
   const int page = p.seqs.block_tables[(int64_t)run.seq * p.seqs.table_stride + run.pos0 / kPage];
   const int slot0 = run.pos0 % kPage;
@@ -227,111 +248,124 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
   }
   __syncthreads();
 
-  for (int h = first; h < heads; h += hop) {
-    if (h != first) load(h);
+  // A step's rows of a query or key head, normed and turned: features in pairs, two an instruction.
+  auto turn = [&](int i, const uint4 (&w)[2], bool normed, uint64_t (&x)[8]) {
+    widen8(raw[i][0], x);
+    widen8(raw[i][1], x + 4);
+    if (normed) {
+      uint64_t ss2 = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss2 = fma2(x[e], x[e], ss2);
+      const float2 s2 = unpair2(ss2);
+      float ss = s2.x + s2.y;
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+      const uint64_t inv2 = pair2(inv, inv);
+      uint64_t w2[8];
+      widen8(w[0], w2);
+      widen8(w[1], w2 + 4);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = mul2(x[e], mul2(w2[e], inv2));
+    }
+    const int r = i * kStep + sub;
+    const uint64_t minus = pair2(-1.f, -1.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 cs = table[((r < run.n ? r : 0) * 4 + j) * kLanes + l];
+      const uint64_t c = pair2(cs.x, cs.y), s = pair2(cs.z, cs.w);
+      const uint64_t a = x[j], b = x[4 + j];
+      x[j] = fma2(a, c, mul2(b, mul2(s, minus)));
+      x[4 + j] = fma2(b, c, mul2(a, s));
+    }
+  };
+
+  // One head; kLive of the run's steps have rows.  Without a way out between the steps they overlap.
+  auto do_head = [&](int h, auto live_steps) {
+    constexpr int kLive = decltype(live_steps)::value;
     const bool is_q = h < p.Hq, turned = h < p.Hq + p.Hkv;
     const int hk = h - p.Hq - (turned ? 0 : p.Hkv);   // the KV head of a key or value slot
-    float* scale_at = nullptr;
-    float old_scale = 0.f;
-    if (kQ8 && !is_q && page_ok) {
-      scale_at = (turned ? p.k_scale : p.v_scale) + (int64_t)page * p.Hkv + hk;
-      if (slot0 > 0) old_scale = *scale_at;
+    if (!kQ8 && h != first) {
+#pragma unroll
+      for (int i = 0; i < kLive; ++i) load_step(h, i);
     }
-    float x[kSteps][16];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      unpack8(raw[i][0], x[i]);
-      unpack8(raw[i][1], x[i] + 8);
+    uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    const uint16_t* weights = is_q ? p.q_norm : p.k_norm;
+    const bool normed = turned && weights != nullptr;
+    if (normed) {
+      w[0] = *reinterpret_cast<const uint4*>(weights + l * 8);
+      w[1] = *reinterpret_cast<const uint4*>(weights + half + l * 8);
     }
-    if (turned) {
-      const uint16_t* w = is_q ? p.q_norm : p.k_norm;
-      if (w) {
-        float wf[16];
-        unpack8(*reinterpret_cast<const uint4*>(w + l * 8), wf);
-        unpack8(*reinterpret_cast<const uint4*>(w + half + l * 8), wf + 8);
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) ss = fmaf(x[i][e], x[i][e], ss);
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[i][e] *= inv * wf[e];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int r = i * kStep + sub;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 cs = table[((r < run.n ? r : 0) * 4 + j) * kLanes + l];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float c = e ? cs.y : cs.x, s = e ? cs.w : cs.z;
-            const float a = x[i][2 * j + e], b = x[i][8 + 2 * j + e];
-            x[i][2 * j + e] = fmaf(a, c, -(b * s));
-            x[i][8 + 2 * j + e] = fmaf(b, c, a * s);
-          }
-        }
-      }
-    }
-    if (is_q) {
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int r = i * kStep + sub;
-        if (r < run.n) {
-          uint16_t* at = p.q_out + ((int64_t)(run.row0 + r) * p.Hq + h) * D + l * 8;
-          *reinterpret_cast<uint4*>(at) = pack8(x[i]);
-          *reinterpret_cast<uint4*>(at + half) = pack8(x[i] + 8);
-        }
-      }
-      continue;
-    }
-    if (!page_ok) continue;
     const int64_t row_values = (int64_t)p.Hkv * D;
     const int64_t block = (int64_t)page * kPage * row_values + (int64_t)hk * D;
-    if (!kQ8) {
-      uint16_t* pool = static_cast<uint16_t*>(turned ? p.k_pool : p.v_pool) + block;
+    uint8_t* pool8 = static_cast<uint8_t*>(turned ? p.k_pool : p.v_pool) + block;
+    float inv = 1.f;
+    if (kQ8 && !is_q && page_ok) {
+      // The block's scale comes first.  A key is turned once for it and once for the store: holding the
+      // run's turned rows instead takes 64 registers a lane, and the warps that hide the loads.
+      float* scale_at = (turned ? p.k_scale : p.v_scale) + (int64_t)page * p.Hkv + hk;
+      const float old_scale = slot0 > 0 ? *scale_at : 0.f;   // a fresh block begins at 0
+      float amax = 0.f;   // rows past the run are zeros
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int r = i * kStep + sub;
-        if (r < run.n) {
-          uint16_t* at = pool + (slot0 + r) * row_values + l * 8;
-          // a value goes through as it came: converting back and forth would quiet a NaN's payload
-          *reinterpret_cast<uint4*>(at) = turned ? pack8(x[i]) : raw[i][0];
-          *reinterpret_cast<uint4*>(at + half) = turned ? pack8(x[i] + 8) : raw[i][1];
+      for (int i = 0; i < kLive; ++i) {
+        uint64_t x[8];
+        if (turned) {
+          turn(i, w, normed, x);
+        } else {
+          widen8(raw[i][0], x);
+          widen8(raw[i][1], x + 4);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 v = unpair2(x[e]);
+          amax = fmaxf(amax, fmaxf(finite_abs(v.x), finite_abs(v.y)));
         }
       }
-      continue;
+      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+      const float scale = fmaxf(q8::scale_of(amax), old_scale);
+      if (slot0 > 0 && scale > old_scale) rescale_block<D>(pool8, row_values, slot0, old_scale / scale);
+      if (lane == 0 && scale != old_scale) *scale_at = scale;
+      inv = 1.f / scale;
     }
-    float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
-      if (i * kStep + sub < run.n) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[i][e]));
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float scale = fmaxf(q8::scale_of(amax), old_scale);   // a fresh block's old_scale is 0
-    uint8_t* pool = static_cast<uint8_t*>(turned ? p.k_pool : p.v_pool) + block;
-    if (slot0 > 0 && scale > old_scale) rescale_block<D>(pool, row_values, slot0, old_scale / scale);
-    if (lane == 0 && scale != old_scale) *scale_at = scale;
-    const float inv = 1.f / scale;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < kLive; ++i) {
       const int r = i * kStep + sub;
-      if (r < run.n) {
-        uint8_t* at = pool + (slot0 + r) * row_values + l * 8;
-        const float* y = x[i];
-        *reinterpret_cast<uint2*>(at) =
-            make_uint2(q8::to_e4m3x4(y[0], y[1], y[2], y[3], inv), q8::to_e4m3x4(y[4], y[5], y[6], y[7], inv));
-        *reinterpret_cast<uint2*>(at + half) =
-            make_uint2(q8::to_e4m3x4(y[8], y[9], y[10], y[11], inv), q8::to_e4m3x4(y[12], y[13], y[14], y[15], inv));
+      const bool live = r < run.n;
+      uint64_t x[8];
+      if (turned) {
+        turn(i, w, normed, x);
+      } else if (kQ8) {
+        widen8(raw[i][0], x);
+        widen8(raw[i][1], x + 4);
+      } else if (live && page_ok) {   // a bf16 value goes through as it came, a NaN's payload too
+        uint16_t* at = static_cast<uint16_t*>(p.v_pool) + block + (slot0 + r) * row_values + l * 8;
+        *reinterpret_cast<uint4*>(at) = raw[i][0];
+        *reinterpret_cast<uint4*>(at + half) = raw[i][1];
+      }
+      if (kQ8 && h + hop < heads) load_step(h + hop, i);   // in flight while the later rows are turned
+      if (is_q) {
+        if (live) {
+          uint16_t* at = p.q_out + ((int64_t)(run.row0 + r) * p.Hq + h) * D + l * 8;
+          *reinterpret_cast<uint4*>(at) = narrow8(x);
+          *reinterpret_cast<uint4*>(at + half) = narrow8(x + 4);
+        }
+      } else if (!kQ8) {
+        if (turned && live && page_ok) {
+          uint16_t* at = static_cast<uint16_t*>(p.k_pool) + block + (slot0 + r) * row_values + l * 8;
+          *reinterpret_cast<uint4*>(at) = narrow8(x);
+          *reinterpret_cast<uint4*>(at + half) = narrow8(x + 4);
+        }
+      } else if (live && page_ok) {
+        uint8_t* at = pool8 + (slot0 + r) * row_values + l * 8;
+        *reinterpret_cast<uint2*>(at) = make_uint2(pairs_to_e4m3x4(x[0], x[1], inv), pairs_to_e4m3x4(x[2], x[3], inv));
+        *reinterpret_cast<uint2*>(at + half) = make_uint2(pairs_to_e4m3x4(x[4], x[5], inv), pairs_to_e4m3x4(x[6], x[7], inv));
       }
     }
+  };
+  if (run.n <= kStep) {
+    for (int h = first; h < heads; h += hop) do_head(h, std::integral_constant<int, 1>());
+  } else {
+    for (int h = first; h < heads; h += hop) do_head(h, std::integral_constant<int, kSteps>());
   }
 }
 
@@ -347,7 +381,7 @@ struct PackParams {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ PackParams p) {
+__global__ void __launch_bounds__(kThreads, 4) pack_kernel(const __grid_constant__ PackParams p) {
   constexpr int kLanes = D / 8;           // lanes of a row, 8 features each
   constexpr int kStep = 32 / kLanes;
   constexpr int kSteps = kPage / kStep;
@@ -377,24 +411,40 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ 
     const int r = s * kStep + sub;
     raw[s] = r < n ? *reinterpret_cast<const uint4*>(from + r * row_values) : make_uint4(0, 0, 0, 0);
   }
-  float amax = 0.f;
+  // the largest magnitude, as bf16 bits: two values an instruction
+  uint32_t most = 0;
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    float x[8];
-    unpack8(raw[s], x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(x[e]));
+    most = __vmaxu2(__vmaxu2(most, raw[s].x & 0x7fff7fffu), raw[s].y & 0x7fff7fffu);
+    most = __vmaxu2(__vmaxu2(most, raw[s].z & 0x7fff7fffu), raw[s].w & 0x7fff7fffu);
   }
+  uint32_t top = max(most & 0xffffu, most >> 16);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool finite = top < 0x7f80u;
+  float amax = __uint_as_float(top << 16);
+  if (!finite) {   // some value is inf or NaN: the largest of the others
+    amax = 0.f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      float x[8];
+      unpack8(raw[s], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(x[e]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  }
   const float scale = q8::scale_of(amax), inv = 1.f / scale;
   uint8_t* to = (is_v ? p.v_pool : p.k_pool) + layer * p.pool_layer_stride + dst * kPage * row_values + h * D + l * 8;
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     float x[8];
     unpack8(raw[s], x);
-    *reinterpret_cast<uint2*>(to + (s * kStep + sub) * row_values) =
-        make_uint2(q8::to_e4m3x4(x[0], x[1], x[2], x[3], inv), q8::to_e4m3x4(x[4], x[5], x[6], x[7], inv));
+    uint2 v;
+    if (finite) v = make_uint2(q8::finite_to_e4m3x4(x[0], x[1], x[2], x[3], inv), q8::finite_to_e4m3x4(x[4], x[5], x[6], x[7], inv));
+    else v = make_uint2(q8::to_e4m3x4(x[0], x[1], x[2], x[3], inv), q8::to_e4m3x4(x[4], x[5], x[6], x[7], inv));
+    *reinterpret_cast<uint2*>(to + (s * kStep + sub) * row_values) = v;
   }
   if (lane == 0) (is_v ? p.v_scale : p.k_scale)[layer * p.scale_layer_stride + (int64_t)dst * p.heads + h] = scale;
 }
@@ -489,10 +539,15 @@ kvrp_status run(const char* fn, bool q8, const void* q, const void* k, const voi
   // A sequence of n rows has at most (n - 1) / 16 + 2 runs, and at most n.
   const int64_t runs = !seqs->row_start ? seqs->n_seqs
                                         : std::min<int64_t>(seqs->n_rows, seqs->n_rows / kPage + 2 * (int64_t)seqs->n_seqs);
-  // A run's heads are shared out while that still adds warps the GPU has room for (two
-  // CTAs an SM): a decode step is a few runs, and its time is one warp's chain of loads.
+  // A run's heads are shared out among CTAs while the GPU has room for more (three CTAs an SM): a
+  // decode step is a few runs, and its time is one warp's chain of loads.  A prompt a little above
+  // one filling of the GPU (530 runs for 456 places) takes two CTAs a run as well, 35.6 us against
+  // 37.8 with one; below one filling and from two on the second table of angles costs more than the
+  // evener end gives (412 runs, 96 heads: 57.9 us with one, 59.7 with two).
+  const int64_t places = 3 * (int64_t)sms;
   const int rounds = (n_q_heads - p.h0 + 2 * n_kv_heads + kWarps - 1) / kWarps;
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(rounds, 2 * (int64_t)sms / std::max<int64_t>(runs, 1)));
+  const int64_t wanted = runs > places && runs < 2 * places ? 2 : places / runs;
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(rounds, wanted));
   if (runs * p.splits > INT32_MAX) return fail(KVRP_ERR_UNSUPPORTED, "%s: too many rows", fn);
 
   cudaLaunchAttribute attr[1];

@@ -45,7 +45,14 @@ __device__ __forceinline__ float scale_of(float amax) {
   const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
   return __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
 }
-// Four values to e4m3 bytes (x * inv, |x * inv| <= 448); inf and NaN become NaN.
+// Four finite values to e4m3 bytes (x * inv, |x * inv| <= 448).
+__device__ __forceinline__ uint32_t finite_to_e4m3x4(float a, float b, float c, float d, float inv) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fmul_rn(b, inv)), "f"(__fmul_rn(a, inv)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fmul_rn(d, inv)), "f"(__fmul_rn(c, inv)));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+// The same for any values; inf and NaN become NaN.
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d, float inv) {
   a = __fmaf_rn(a, 0.f, __fmul_rn(a, inv));   // + 0 for a finite value, NaN for inf and NaN
   b = __fmaf_rn(b, 0.f, __fmul_rn(b, inv));
