@@ -70,16 +70,25 @@ __device__ __forceinline__ Seq seq_at(const Params& p, int s, bool* idle = nullp
   return r;
 }
 
-// A segment: pages [page, end) of (sequence, head group), and the pages left of the share
-// from `page` on.
+// A segment: pages [page, end) of (sequence, head group).  Shares are cut by cost: a page counts 1
+// and a unit, (sequence, head group), p.unit_pages more for its queries and results, or the CTAs of a
+// batch's short sequences finish last (24 uneven multi-head sequences: 100 us without, see below).
 struct Cursor {
   int s, grp, page, end;
-  int64_t left;
+  int from, spent;      // the segment's costs [from, from + spent) of its unit
+  int64_t left;         // cost of the share from here on
 };
+__device__ __forceinline__ void take(const Params& p, Cursor& c, int pages, int from) {
+  const int to = (int)min((int64_t)pages + p.unit_pages, from + c.left);
+  c.from = from;
+  c.spent = to - from;
+  c.page = max(0, from - p.unit_pages);
+  c.end = max(0, to - p.unit_pages);
+}
 struct Plan {
   Cursor at;
   Seq seq;
-  int64_t total, b;   // pages in all, the share's end
+  int64_t total, b;   // the cost in all, the share's end
   int n_cta;
   bool idle;          // some place of the batch is idle
 };
@@ -96,8 +105,9 @@ constexpr int kLeast = 2;
 __device__ __forceinline__ bool find_share(const Params& p, Plan* out, PlanSmem& sh) {
   const int n = p.seqs.n_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool idle = false;
-  int64_t later = 0;   // pages of the sequences past the first kThreads
-  for (int s = kThreads + tid; s < n; s += kThreads) later += seq_at(p, s, &idle, blockIdx.x == 0).pages;
+  auto cost = [&](const Seq& q) { return q.pages > 0 ? q.pages + p.unit_pages : 0; };   // of one head group
+  int64_t later = 0;   // the sequences past the first kThreads
+  for (int s = kThreads + tid; s < n; s += kThreads) later += cost(seq_at(p, s, &idle, blockIdx.x == 0));
   if (n > kThreads) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) later += __shfl_xor_sync(0xffffffffu, later, o);
@@ -112,7 +122,8 @@ __device__ __forceinline__ bool find_share(const Params& p, Plan* out, PlanSmem&
     const int s = s0 + tid;
     Seq q = {0, 0, 0, 0};
     if (s < n) q = s0 == 0 ? seq_at(p, s, &idle, blockIdx.x == 0) : seq_at(p, s);
-    int64_t sum = q.pages;
+    const int mine = cost(q);
+    int64_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t t = __shfl_up_sync(0xffffffffu, sum, o);
@@ -121,7 +132,7 @@ __device__ __forceinline__ bool find_share(const Params& p, Plan* out, PlanSmem&
     if (lane == 31) sh.sum[warp] = sum;
     if (tid == 0) sh.found = -1;
     out->idle = __syncthreads_or(idle);
-    int64_t lo = before + sum - q.pages;
+    int64_t lo = before + sum - mine;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) lo += sh.sum[w];
@@ -134,7 +145,7 @@ __device__ __forceinline__ bool find_share(const Params& p, Plan* out, PlanSmem&
       a = div64(out->total * blockIdx.x, out->n_cta);
       out->b = div64(out->total * (blockIdx.x + 1), out->n_cta);
     }
-    if (a >= lo * p.n_grp && a < (lo + q.pages) * p.n_grp) {
+    if (a >= lo * p.n_grp && a < (lo + mine) * p.n_grp) {
       sh.found = s;
       sh.before = lo * p.n_grp;
       sh.seq = q;
@@ -146,24 +157,23 @@ __device__ __forceinline__ bool find_share(const Params& p, Plan* out, PlanSmem&
   out->seq = sh.seq;
   out->at.s = sh.found;
   const int64_t at = a - sh.before;
-  out->at.grp = (int)div64(at, out->seq.pages);
-  out->at.page = (int)(at - (int64_t)out->at.grp * out->seq.pages);
+  const int unit = out->seq.pages + p.unit_pages;
+  out->at.grp = (int)div64(at, unit);
   out->at.left = out->b - a;
-  out->at.end = (int)min((int64_t)out->seq.pages, out->at.page + out->at.left);
-  return true;
+  take(p, out->at, out->seq.pages, (int)(at - (int64_t)out->at.grp * unit));
+  return out->at.end > out->at.page;   // else the share ends before its unit's first page
 }
-// The next segment of the share after one that began at page `first`; false at the share's end.
-__device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, int first, Seq& q) {
-  c.left -= c.end - first;
+// The next segment of the share; false at its end.
+__device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Seq& q) {
+  c.left -= c.spent;
   if (c.left <= 0) return false;
   if (++c.grp == p.n_grp) {
     c.grp = 0;
     do q = seq_at(p, ++c.s);
     while (q.pages == 0);
   }
-  c.page = 0;
-  c.end = (int)min((int64_t)q.pages, c.left);
-  return true;
+  take(p, c, q.pages, 0);
+  return c.end > 0;
 }
 
 // Asynchronous copies to shared memory (zeros past the first `bytes`), and their groups.
@@ -194,9 +204,9 @@ struct Decode {
   static constexpr int kPages = 128 / D;                      // pages of a step
   static constexpr int kBox = kPage * D;                      // bytes of one head's K (or V) of a page
   static constexpr int kStage = 2 * kPages * kBox;            // 4 KB
-  // Two CTAs an SM, 12 KB in flight a warp.  16 columns of head_dim 128 need 200 registers a thread:
-  // one CTA, 24 KB a warp.
-  static constexpr int kCtas = D == 128 && NT == 2 ? 1 : 2;
+  // Two CTAs an SM, 12 KB in flight a warp; with two column tiles one CTA, 24 KB a warp: in 128
+  // registers they spill (32 sequences of 4 rows x 4 x 64: 56.6 us with two CTAs, 44.8 with one).
+  static constexpr int kCtas = NT == 2 ? 1 : 2;
   static constexpr int kStages = kCtas == 1 ? 6 : 3;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kMerge = 32 * (D / 16 * NT * 4 + NT * 6);   // words of one warp's accumulator and statistics
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
   int i_st = 0;
   bool more = true;
   auto settle = [&]() {   // to the next segment that has a step for this stream
-    while (i_left == 0 && (more = next_segment(p, ic, i_first, iq))) {
+    while (i_left == 0 && (more = next_segment(p, ic, iq))) {
       i_first = i_q = 0;
       i_left = steps_of(0, ic.end);
       b_at = 32;
@@ -586,8 +596,8 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
     // ---- the segment's result: a whole unit goes out, a part goes to the combine -----------
     const bool begins = first == 0, ends = cc.end == cq.pages;
     if (begins && !ends) {
-      // the CTA whose share holds the unit's last page: the largest j with total j / n_cta <= that page
-      const int64_t last = plan.b - cc.left + cq.pages;
+      // the CTA whose share holds the unit's last page: the largest j with total j / n_cta below the unit's end
+      const int64_t last = plan.b - cc.left - cc.from + cq.pages + p.unit_pages;
       const int j = (int)div64(last * plan.n_cta - 1, plan.total);
       meta = make_int4(cq.rows, cc.grp, j - (int)blockIdx.x + 1, cq.row0);
     }
@@ -621,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
           }
         }
     }
-    if (!next_segment(p, cc, first, cq)) break;
+    if (!next_segment(p, cc, cq)) break;
   }
   if (tid == 0) p.meta[blockIdx.x] = meta;
   if (plan.idle) write_idle(p, D);
@@ -839,6 +849,7 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   p.hg = hg;
   p.n_grp = n_kv_heads / hg;
   p.streams = attend_q8::kWarps / hg;
+  p.unit_pages = std::max(1, 2048 / (hg * head_dim));   // about 2 us of a CTA's share of the bandwidth
   p.rounds = hg == 1 ? 4 : hg == 2 ? 3 : hg == 4 ? 2 : 0;
   p.scale = softmax_scale * 1.4426950408889634f;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
@@ -855,7 +866,7 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
     return KVRP_OK;
   }
   const bool two = max_rows * g > 8;
-  if (two && head_dim == 128) p.n_cta = std::min(p.n_cta, attend_q8::Decode<128, 2>::kCtas * sms);
+  if (two) p.n_cta = std::min(p.n_cta, attend_q8::Decode<128, 2>::kCtas * sms);
   auto kernel = head_dim == 64 ? (two ? attend_q8::decode_kernel<64, 2> : attend_q8::decode_kernel<64, 1>)
                                : (two ? attend_q8::decode_kernel<128, 2> : attend_q8::decode_kernel<128, 1>);
   const int smem = head_dim == 64 ? (two ? attend_q8::Decode<64, 2>::kSmem : attend_q8::Decode<64, 1>::kSmem)

@@ -41,6 +41,7 @@ struct Params {
   int cols;             // (head, row) columns of a part: heads of a group x max_rows x g, or kPromptRows
   int hg, n_grp;        // few rows: KV heads a CTA takes together, their groups,
   int streams, rounds;  // warps that share a head's pages, rounds that merge them
+  int unit_pages;       // a unit's cost beside its pages
   uint64_t g_inverse;   // 2^32 / g, rounded up
   float scale;          // softmax_scale * log2(e)
 };
