@@ -568,8 +568,11 @@ kvrp_status kv_pack_q8(
  * with a bad length, or more rows than max_rows, is flagged and its rows are left as
  * they were.  A bad table entry sets KVRP_DEV_BAD_PAGE and reads as a page of
  * zeros.  Slots past a sequence's length are never used, whatever they hold.
- * The output does not depend on how the work is split over the GPU beyond fp32
- * rounding, and the same call gives the same bits.  Asynchronous on `stream`; may
+ * rows x group up to 16 take a kernel for few rows, more one that fills tensor-core
+ * tiles with rows; n_rows x n_q_heads must stay below 2^32, n_rows x group below 2^28
+ * (UNSUPPORTED).  KVRP_DEV_TIMEOUT is OR-ed in if an internal pipeline wait gave up
+ * (the output is then undefined).  The output does not depend on how the work is split
+ * over the GPU beyond fp32 rounding, and the same call gives the same bits.  Asynchronous on `stream`; may
  * be captured into a graph and replayed as lengths and tables change.
  */
 size_t kv_attend_q8_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_rows);

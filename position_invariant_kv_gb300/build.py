@@ -22,7 +22,8 @@ SOURCES = [os.path.join(HERE, "csrc", "kvrp_kernel.cu"), os.path.join(HERE, "csr
            os.path.join(HERE, "csrc", "kvrp_host.cpp")]
 HEADERS = [os.path.join(ROOT, "include", "kvrp.h"), os.path.join(HERE, "csrc", "kvrp_plan.h"),
            os.path.join(HERE, "csrc", "kvrp_ptx.h"), os.path.join(HERE, "csrc", "kvrp_q8.h"),
-           os.path.join(HERE, "csrc", "kvrp_attend_q8.h")]
+           os.path.join(HERE, "csrc", "kvrp_attend_q8.h"),
+           os.path.join(HERE, "csrc", "kvrp_ptx_math.h")]
 
 
 def nvcc_command(out: str = LIB, ptxas_verbose: bool = False) -> list:

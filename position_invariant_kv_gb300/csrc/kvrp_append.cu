@@ -19,8 +19,8 @@
 //   - 80 registers a thread, three CTAs an SM: what bounds a prompt is how many loads are in
 //     flight.  The 8-bit form loads the next head's rows as it is done with this one's; in the
 //     bf16 form that measured slower (40.7 against 35.6 us) and it loads a head at a time.
-//   Measured: 8 sequences, 8218 rows of 28 + 2 x 4 heads x 128 with norms and M-RoPE, 160 MB, 35.6 us
-//   (4.5 TB/s, 67% of a copy); 6.1 thousand rows of 32 + 2 x 32 heads into 8 bits, 278 MB, 57.9 us (72%);
+//   Measured: 8 sequences, 8719 rows of 28 + 2 x 4 heads x 128 with norms and M-RoPE, 160 MB, 35.6 us
+//   (4.5 TB/s, 67% of a copy); 6790 rows of 32 + 2 x 32 heads into 8 bits, 278 MB, 57.9 us (72%);
 //   one row of each of 16 sequences 3.0 us, of 64 into 8 bits 4.5 us (launch and latency).
 //
 // pack_kernel.  One warp a block: 16 rows of one head of one layer in registers, amax (two bf16
@@ -39,6 +39,7 @@
 #include "kvrp.h"
 #include "kvrp_plan.h"
 #include "kvrp_ptx.h"
+#include "kvrp_ptx_math.h"
 #include "kvrp_q8.h"
 
 namespace kvrp {
@@ -541,9 +542,9 @@ kvrp_status run(const char* fn, bool q8, const void* q, const void* k, const voi
                                         : std::min<int64_t>(seqs->n_rows, seqs->n_rows / kPage + 2 * (int64_t)seqs->n_seqs);
   // A run's heads are shared out among CTAs while the GPU has room for more (three CTAs an SM): a
   // decode step is a few runs, and its time is one warp's chain of loads.  A prompt a little above
-  // one filling of the GPU (530 runs for 456 places) takes two CTAs a run as well, 35.6 us against
+  // one filling of the GPU (560 runs for 456 places) takes two CTAs a run as well, 35.6 us against
   // 37.8 with one; below one filling and from two on the second table of angles costs more than the
-  // evener end gives (412 runs, 96 heads: 57.9 us with one, 59.7 with two).
+  // evener end gives (432 runs, 96 heads: 57.9 us with one, 59.7 with two).
   const int64_t places = 3 * (int64_t)sms;
   const int rounds = (n_q_heads - p.h0 + 2 * n_kv_heads + kWarps - 1) / kWarps;
   const int64_t wanted = runs > places && runs < 2 * places ? 2 : places / runs;

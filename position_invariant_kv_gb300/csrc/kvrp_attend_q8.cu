@@ -9,13 +9,17 @@
 // (e4m3 values are f16 values exactly).
 //
 // decode_kernel: few rows a sequence (rows x group <= 16).  Bound by the bytes of K and V.
-//   - Work is the list of (sequence, KV head, page); each CTA takes an equal contiguous
-//     share, so every SM streams the same bytes whatever the lengths; a share's part of one
-//     (sequence, head) is a segment.  The shares are computed on the device from the
-//     lengths there: a captured graph keeps its balance as sequences grow.
-//   - A warp is a pipeline of its own: it takes every 8th page of the segment through a
-//     private ring of TMA boxes (16 x head_dim bytes of K and of V) on its own mbarriers,
-//     which runs on across segments.  No warp waits for another inside a segment.
+//   - Work is the list of (sequence, head group, page); each CTA takes a contiguous share of
+//     equal cost, so every SM streams about the same bytes whatever the lengths; a share's part
+//     of one (sequence, head group) is a segment.  The shares are computed on the device from
+//     the lengths there: a captured graph keeps its balance as sequences grow.
+//   - A head group is up to 8 KV heads, a warp each (or several warps, streams, a head where the
+//     group is smaller).  A token's heads lie side by side, so the CTA's warps read whole
+//     neighbouring pieces of the same rows at about the same time: 24 uneven sequences of 32 KV
+//     heads took 253 us with a head a CTA and 109 with a head a warp.
+//   - A warp is a pipeline of its own: it takes its stream's pages through a private ring of
+//     16-byte asynchronous copies, swizzled on the way, which runs on across segments.  No warp
+//     waits for another inside a segment.  (TMA boxes of a page and head took the same time.)
 //   - mma.sync m16n8k16 with f16 operands and tokens as the product's rows: S = K Q^T, 16
 //     tokens x 8 heads a tile, then O^T += V^T P^T with P^T transposed in registers.  A page
 //     is exactly the 16 rows (and the 16-deep contraction of the second product), so its
@@ -28,9 +32,17 @@
 //   - Two running maxima a row: of the scores x (for the sum of weights), and of x + log2 vs
 //     (for the accumulator, whose weights are exp2(x + log2 vs - max)).  The second keeps
 //     the f16 weights in range however far the pages' value scales lie apart.
-//   - Maxima move only when a score passes them by 2^8 (one vote a page instead of six
+//   - Maxima move only when a score passes them by 2^8 (one vote a step instead of six
 //     shuffles); weights then stay below 2^15, inside f16.
-// combine_kernel: merges the partial results of (sequence, head)s that more than one CTA shared.
+// combine_kernel: merges the partial results of units that more than one CTA shared.
+//
+// Measured: 16 sequences x 16384 tokens, 28 / 4 heads x 128 (269 MB): 55.7 us, 4.8 TB/s, 72% of a
+// copy.  From the first data to the last page the reads run at the memory's rate (about 34 us); 6 us
+// go before them (the shares, the first table entries, the first pages), SMs end up to 5 us apart,
+// merging and combining take 6.  24 uneven multi-head sequences (566 MB): 99 us, 85%.  4 rows x 4
+// heads x 64 over 32 sequences (118 MB): 43.8 us, 40%: 8 warps an SM, each bound by the latency of its
+// own chain of products and powers.  One sequence of 1000 tokens: 11 us, two launches and about ten
+// dependent trips to memory.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,7 +55,6 @@
 
 #include "kvrp.h"
 #include "kvrp_plan.h"
-#include "kvrp_ptx.h"
 #include "kvrp_q8.h"
 #include "kvrp_attend_q8.h"
 
@@ -72,7 +83,7 @@ __device__ __forceinline__ Seq seq_at(const Params& p, int s, bool* idle = nullp
 
 // A segment: pages [page, end) of (sequence, head group).  Shares are cut by cost: a page counts 1
 // and a unit, (sequence, head group), p.unit_pages more for its queries and results, or the CTAs of a
-// batch's short sequences finish last (24 uneven multi-head sequences: 100 us without, see below).
+// batch's short sequences finish last.
 struct Cursor {
   int s, grp, page, end;
   int from, spent;      // the segment's costs [from, from + spent) of its unit

@@ -9,6 +9,7 @@
 
 #include "kvrp.h"
 #include "kvrp_ptx.h"
+#include "kvrp_ptx_math.h"
 #include "kvrp_q8.h"
 
 namespace kvrp {

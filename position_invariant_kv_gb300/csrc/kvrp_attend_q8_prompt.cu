@@ -24,11 +24,43 @@
 //     weights + 128 of accumulator, twice, are what 512 columns hold.  (With 128 tokens and
 //     the weights in the scores' place each tile waited for both products: 911 TFLOP/s on
 //     4096 rows over 16441 tokens.)
+//
+// Measured: 4096 rows over 16441 tokens, 28 / 4 heads x 128: 687 us, 1231 TFLOP/s, 63% of the measured
+// bf16 peak; 6 questions of 37 to 900 rows behind 500 to 12000 tokens: 220 us, 1015 TFLOP/s.  A tile
+// takes about 2300 cycles, its products alone 1500: the softmax warps wait some 800 of them for
+// products, which share the 128 bytes a cycle of shared memory with the conversion of V (two thirds
+// busy).  Beginning and ending a unit costs about 7 us.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 
 #include "kvrp_attend_q8.h"
+#include "kvrp_plan.h"
 
 namespace kvrp {
+
+kvrp_status encode_q8_pool(CUtensorMap* map, const void* pool, int num_pages, int row_bytes, int head_dim) {
+  // found once: the driver's entry point does not change while the library is loaded
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn) : nullptr;
+  }();
+  if (!encode) return fail(KVRP_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[3] = {(cuuint64_t)row_bytes, 16, (cuuint64_t)num_pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)row_bytes * 16};
+  const cuuint32_t box[3] = {(cuuint32_t)head_dim, 16, 1}, estr[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            // a wider fetch would bring in the next head's rows, which another CTA reads
+                            head_dim == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(KVRP_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d) for an 8-bit pool", (int)r);
+  return KVRP_OK;
+}
+
 namespace attend_q8 {
 
 namespace {
@@ -173,7 +205,7 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // ---- units and shares ------------------------------------------------------------------------
 // Beginning and ending a unit (its queries, the first scores, the results) takes a CTA as long as some
 // tiles do; the shares count that, or the CTAs of a batch's many short units finish last.
-constexpr int kUnitTiles = 6;
+constexpr int kUnitTiles = 6;   // 4: 222 us for the 6 questions above, 6: 220
 
 // A unit's part inside this CTA's share: tiles [j0, j1) of its n_kv.
 struct Unit {

@@ -23,7 +23,6 @@
 
 #include "kvrp.h"
 #include "kvrp_plan.h"
-#include "kvrp_q8.h"
 
 namespace kvrp {
 
@@ -554,20 +553,6 @@ kvrp_status current_device_sms(int* sms, int* smem_optin) {
   if (st != KVRP_OK) return st;
   *sms = di->sms;
   *smem_optin = di->smem_optin;
-  return KVRP_OK;
-}
-
-kvrp_status encode_q8_pool(CUtensorMap* map, const void* pool, int num_pages, int row_bytes, int head_dim) {
-  const cuuint64_t dims[3] = {(cuuint64_t)row_bytes, 16, (cuuint64_t)num_pages};
-  const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)row_bytes * 16};
-  const cuuint32_t box[3] = {(cuuint32_t)head_dim, 16, 1}, estr[3] = {1, 1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                              // a wider fetch would bring in the next head's rows, which another CTA reads
-                              head_dim == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(KVRP_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d) for an 8-bit pool", (int)r);
   return KVRP_OK;
 }
 

@@ -131,6 +131,7 @@ def test_attend_q8_refusals(kvrp):
     assert st(workspace=None) == kvrp.KVRP_ERR_WORKSPACE and st(workspace_bytes=1024) == kvrp.KVRP_ERR_WORKSPACE
     assert kvrp.kv_attend_q8_workspace_size(8, 3, 128, 1) == 0 and kvrp.kv_attend_q8_workspace_size(8, 2, 96, 1) == 0
     assert kvrp.kv_attend_q8_workspace_size(8, 2, 128, 0) == 0
+    assert st(seqs=_Seqs(kvrp, n_rows=1 << 27, max_rows=2)) == uns                # n_rows x group reaches 2^28
     need = kvrp.kv_attend_q8_workspace_size(8, 2, 128, 2)
     assert need > 0
     import torch
