@@ -630,7 +630,9 @@ kvrp_status kv_pack_q8(const void* k_src, const void* v_src, int64_t src_layer_s
   if (!k_src || !v_src || !k_pool || !v_pool || !k_scale || !v_scale) return fail(KVRP_ERR_INVALID_ARG, "%s: NULL argument", fn);
   const int pages = (int)(((int64_t)n_tokens + append::kPage - 1) / append::kPage);
   const int64_t D = (int64_t)n_kv_heads * head_dim;
-  if (num_pages <= 0 || (src_table && src_pages <= 0) || (!block_table && pages > num_pages))
+  constexpr int kMostPages = INT32_MAX / append::kPage;
+  if (num_pages <= 0 || num_pages > kMostPages || (src_table && (src_pages <= 0 || src_pages > kMostPages)) ||
+      (!block_table && pages > num_pages))
     return fail(KVRP_ERR_INVALID_ARG, "%s: num_pages or src_pages out of range", fn);
   const int64_t src_need = src_table ? (int64_t)src_pages * append::kPage * D : (int64_t)n_tokens * D;
   src_layer_stride = src_layer_stride ? src_layer_stride : src_need;

@@ -19,6 +19,7 @@ namespace kvrp {
 namespace q8 {
 
 constexpr int kPage = 16;   // tokens per page (and per block)
+constexpr int kMostTokens = 0x7fffff00;   // of a sequence: a tile more stays an int
 
 #ifdef __CUDACC__
 
@@ -33,7 +34,7 @@ __device__ __forceinline__ bool sequence(const kvrp_seqs& q, int s, int& row0, i
   len = q.seq_lens[s];
   rows = end - row0;
   const bool ok = row0 >= 0 && end >= row0 && end <= q.n_rows && len >= rows &&
-                  (int64_t)len <= (int64_t)q.table_stride * kPage;
+                  len <= kMostTokens && (int64_t)len <= (int64_t)q.table_stride * kPage;
   if (!ok || len == 0) rows = 0;
   return ok || len == 0;
 }

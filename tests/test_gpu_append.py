@@ -258,6 +258,7 @@ def test_idle_places_bad_lengths_and_bad_pages():
     b = Batch(ctx=[3, 20, 40, 7], rows=[1] * 4, hq=4, hkv=2, d=64)
     for lens, table_edit, flags, skipped in (([4, 0, 41, 8], None, 0, [1]), ([4, -2, 41, 8], None, 4, [1]),
                                              ([4, 21, 41, 16 * b.table.shape[1] + 1], None, 4, [3]),
+                                             ([4, 2 ** 31 - 1, 41, 8], None, 4, [1]),
                                              (b.lens, (2, 2, b.pages), 1, [2]), (b.lens, (0, 0, -5), 1, [0])):
         table = b.table.copy()
         if table_edit:

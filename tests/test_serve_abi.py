@@ -97,6 +97,7 @@ def test_pack_refusals(kvrp):
     assert st(k=None) == inv and st(v_pool=None) == inv and st(k_scale=None) == inv
     assert st(n_layers=0) == inv and st(n_tokens=-1) == inv and st(num_pages=0) == inv and st(src_pages=0) == inv
     assert st(block_table=None, num_pages=6) == inv                  # 7 pages do not fit
+    assert st(num_pages=1 << 28) == inv and st(src_pages=1 << 28) == inv
     assert st(head_dim=32) == uns and st(n_kv_heads=0) == uns
     assert st(pool_layer_stride=16) == inv and st(scale_layer_stride=31) == inv and st(src_layer_stride=8) == inv
     assert st(src_layer_stride=7 * 16 * 128 + 4) == ali and st(pool_layer_stride=16 * 16 * 128 + 8) == ali
