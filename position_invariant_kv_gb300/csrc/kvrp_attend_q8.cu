@@ -785,7 +785,7 @@ int sm_count() {
   return std::min(n, kMaxCtas / kMaxCtasPerSm);
 }
 
-size_t meta_bytes(int n_cta) { return ((size_t)n_cta * sizeof(int4) + 255) / 256 * 256; }
+size_t meta_bytes(int n_cta) { return ((size_t)n_cta * 2 * sizeof(int4) + 255) / 256 * 256; }
 size_t workspace_bytes(int n_cta, int cols, int head_dim) {
   return 256 + meta_bytes(n_cta) + (size_t)n_cta * 2 * cols * (head_dim + 4) * sizeof(float);
 }

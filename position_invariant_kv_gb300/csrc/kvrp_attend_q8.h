@@ -37,7 +37,7 @@ struct Params {
   uint32_t* status;
   float* partial;       // [n_cta][2][cols][D + 4]: O, then max, accumulator max, sum; of a unit begun
                         // before this CTA's share, and of one that goes on after it
-  int4* meta;           // [n_cta][2]: the unit whose first, not last, part this CTA holds
+  int4* meta;           // [n_cta] (few rows) or [n_cta][2]: the unit whose first, not last, part this CTA holds
   int Hq, Hkv, g, n_cta, max_rows;
   int cols;             // (head, row) columns of a part: heads of a group x max_rows x g, or kPromptRows
   int hg, n_grp;        // few rows: KV heads a CTA takes together, their groups,

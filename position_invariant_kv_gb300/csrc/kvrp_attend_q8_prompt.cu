@@ -25,8 +25,8 @@
 //     the weights in the scores' place each tile waited for both products: 911 TFLOP/s on
 //     4096 rows over 16441 tokens.)
 //
-// Measured: 4096 rows over 16441 tokens, 28 / 4 heads x 128: 687 us, 1231 TFLOP/s, 63% of the measured
-// bf16 peak; 6 questions of 37 to 900 rows behind 500 to 12000 tokens: 220 us, 1015 TFLOP/s.  A tile
+// Measured: 4096 rows over 16441 tokens, 28 / 4 heads x 128: 683 us, 1238 TFLOP/s, 64% of the measured
+// bf16 peak; 6 questions of 37 to 900 rows behind 500 to 12000 tokens: 215 us, 1038 TFLOP/s.  A tile
 // takes about 2300 cycles, its products alone 1500: the softmax warps wait some 800 of them for
 // products, which share the 128 bytes a cycle of shared memory with the conversion of V (two thirds
 // busy).  Beginning and ending a unit costs about 7 us.
@@ -205,14 +205,14 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // ---- units and shares ------------------------------------------------------------------------
 // Beginning and ending a unit (its queries, the first scores, the results) takes a CTA as long as some
 // tiles do; the shares count that, or the CTAs of a batch's many short units finish last.
-constexpr int kUnitTiles = 6;   // 4: 222 us for the 6 questions above, 6: 220
+constexpr int kUnitTiles = 6;   // 4: 222 us for the 6 questions above, 6: 220 (215 with a later step)
 
 // A unit's part inside this CTA's share: tiles [j0, j1) of its n_kv.
 struct Unit {
   int s, rt, h;             // sequence, row tile, KV head
   int row0, rows, len;      // the sequence
   int n_rt, n_kv, j0, j1;
-  int spent;                // cost of this part
+  int from, spent;          // this part's costs [from, from + spent) of its unit
   int64_t left;             // cost of the share from here on
 };
 template <int N>
@@ -242,6 +242,7 @@ __device__ __forceinline__ void take(Unit& u, int from) {
   const int to = (int)min((int64_t)u.n_kv + kUnitTiles, from + u.left);
   u.j0 = max(0, from - kUnitTiles);
   u.j1 = max(0, to - kUnitTiles);
+  u.from = from;
   u.spent = to - from;
 }
 struct Shared {
@@ -250,6 +251,8 @@ struct Shared {
   float vs[kScaleSlots][kMostPages];                 // of V,
   float vs_top[kScaleSlots];                         // and the largest of V's
   int64_t cost[kWarpsAll];
+  int64_t total, end;     // the cost in all, and where this CTA's share ends
+  int n_cta;
   Unit first;
   int found;
   int abort_flag;
@@ -267,6 +270,11 @@ __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
   const int64_t n_cta = min((int64_t)p.n_cta, (total + kUnitTiles + 1) / (kUnitTiles + 2));
   if ((int)blockIdx.x >= n_cta) return false;
   const int64_t a = total * blockIdx.x / n_cta, b = total * (blockIdx.x + 1) / n_cta;
+  if (threadIdx.x == 0) {
+    sh.total = total;
+    sh.end = b;
+    sh.n_cta = (int)n_cta;
+  }
   int64_t before = 0;
   int s = 0;
   for (int s0 = 0; s0 < n; s0 += kWarpsAll) {   // the sequence that holds tile a
@@ -415,7 +423,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
   Unit u = sh.first;
 
   if (!any) {
-    if (tid == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (tid == 0) p.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   } else if (warp >= 12) {
     fewer_registers<L::kRegsMisc>();
     if (warp == 12) {
@@ -623,7 +631,8 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     int n = 0;                  // tiles of the share
     uint32_t ns = 0;            // of them, this Q tile's
     bool ok = true;
-    int4 meta = make_int4(-1, 0, 0, 0);
+    int4 meta = make_int4(0, 0, 0, 0);   // of a unit that begins here and goes on: parts, KV head, row tile, first row
+    int meta_cols = 0;                   // and (row, query head) pairs of its sequence
     // Where 16-byte chunk x of row r is in part 0 (high) or 1 (low) of this Q tile; between units the
     // two rows of a thread's row are where its results are laid out for whole-row stores.
     auto row_chunk = [&](int part, int r, int x) {
@@ -631,8 +640,12 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     };
     do {
       const bool begins = u.j0 == 0, ends = u.j1 == u.n_kv;
-      if (begins && !ends) meta.x = u.s, meta.y = u.h, meta.w = u.rt;
-      if (!begins) meta.z = ends ? 2 : 1;
+      if (begins && !ends && tid == 0) {
+        // the CTA whose share holds the unit's last tile: the largest j with total j / n_cta below the unit's end
+        const int64_t unit_end = sh.end - u.left - u.from + u.n_kv + kUnitTiles;
+        meta = make_int4((int)((unit_end * sh.n_cta - 1) / sh.total) - (int)blockIdx.x + 1, u.h, u.rt, u.row0);
+        meta_cols = u.rows * p.g;
+      }
       if (t >= active_tiles(p, u)) {
         n += u.j1 - u.j0;
         continue;
@@ -859,7 +872,10 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       }
       tc_fence_before();   // the accumulator is read before the next unit's first product
     } while (ok && next_unit<N>(p, u));
-    if (tid == 0) p.meta[blockIdx.x] = meta;
+    if (tid == 0) {
+      p.meta[2 * blockIdx.x] = meta;
+      p.meta[2 * blockIdx.x + 1] = make_int4(meta_cols, 0, 0, 0);
+    }
   }
   __syncwarp();
   tc_fence_before();
@@ -869,69 +885,81 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
   write_idle(p, D);
 }
 
-// A warp a row of a unit that more than one CTA held: block (i, y) takes rows y * 16 .. of the
-// unit that begins in CTA i.
-constexpr int kCombineWarps = 4, kCombineRows = 16;
+// A warp a row of a unit that more than one CTA held: block (i, y) takes rows y * kCombineRows .. of
+// the unit that begins in CTA i, two rows a warp and two parts of each at a time. That CTA knows from its
+// share where the unit ends and says so, so that nothing is searched here. Four parts at a time cost 5 us
+// more of the 6 questions' 215: most units have two.
+constexpr int kCombineWarps = 4, kCombineRows = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kCombineWarps) prompt_combine_kernel(const __grid_constant__ Params p) {
   constexpr int V = D / 32;   // values a lane
-  __shared__ int last;
+  constexpr int kEach = kCombineRows / kCombineWarps, kBatch = 2;   // rows a warp, parts in flight
   pdl_wait();
   pdl_launch_dependents();
-  const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-  const int4 mt = p.meta[i];
-  if (mt.x < 0) return;
-  int row0, rows, len;
-  sequence(p.seqs, mt.x, row0, rows, len);
-  const int64_t col0 = (int64_t)mt.w * kPromptRows + blockIdx.y * kCombineRows, cols = (int64_t)rows * p.g;
-  if (col0 >= cols) return;
-  if (tid == 0) last = 0x7fffffff;
-  __syncthreads();
-  for (int j0 = i + 1; j0 < p.n_cta; j0 += 32 * kCombineWarps) {   // the CTA that ends the unit
-    const int j = j0 + tid;
-    if (j < p.n_cta && p.meta[j].z == 2) atomicMin(&last, j);
-    __syncthreads();
-    if (last != 0x7fffffff) break;
-    __syncthreads();
+  const int i = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int4 mt = p.meta[2 * i], mt2 = p.meta[2 * i + 1];
+  const int col0 = mt.z * kPromptRows + blockIdx.y * kCombineRows, n = min(mt.x, p.n_cta - i);
+  if (mt.x <= 0 || col0 >= mt2.x) return;
+  float acc[kEach][V], m[kEach], om[kEach], l[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    m[k] = om[k] = -INFINITY;
+    l[k] = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[k][v] = 0.f;
   }
-  const int n = min(last, p.n_cta - 1) - i + 1;
-  for (int k = tid >> 5; k < kCombineRows; k += kCombineWarps) {
-    const int64_t col = col0 + k;
-    if (col >= cols) break;
-    auto entry = [&](int x) {
-      return p.partial + ((int64_t)((i + x) * 2 + (x == 0 ? 1 : 0)) * p.cols + blockIdx.y * kCombineRows + k) * (D + 4);
-    };
-    float m = -INFINITY, om = -INFINITY;
-    for (int x = lane; x < n; x += 32) {
-      const float4 s = *reinterpret_cast<const float4*>(entry(x) + D);
-      m = fmaxf(m, s.x);
-      om = fmaxf(om, s.y);
-    }
+  for (int x0 = 0; x0 < n; x0 += kBatch) {
+    float4 st[kEach][kBatch];
+    float val[kEach][kBatch][V];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      om = fmaxf(om, __shfl_xor_sync(0xffffffffu, om, o));
-    }
-    float acc[V], l = 0.f;
+    for (int k = 0; k < kEach; ++k)
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
-#pragma unroll 4
-    for (int x = 0; x < n; ++x) {
-      const float* e = entry(x);
-      const float4 s = *reinterpret_cast<const float4*>(e + D);
-      const float w = om == -INFINITY ? 0.f : ex2(s.y - om);
-      l += m == -INFINITY ? 0.f : s.z * ex2(s.x - m);
+      for (int b = 0; b < kBatch; ++b) {
+        const int x = x0 + b, row = warp + k * kCombineWarps;
+        const bool held = x < n && col0 + row < mt2.x;
+        const float* e = p.partial +
+                         ((int64_t)((i + x) * 2 + (x == 0 ? 1 : 0)) * p.cols + blockIdx.y * kCombineRows + row) * (D + 4);
+        st[k][b] = held ? *reinterpret_cast<const float4*>(e + D) : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = fmaf(e[lane * V + v], w, acc[v]);
+        for (int v = 0; v < V; ++v) val[k][b][v] = held ? e[lane * V + v] : 0.f;
+      }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      float nm = m[k], no = om[k];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        nm = fmaxf(nm, st[k][b].x);
+        no = fmaxf(no, st[k][b].y);
+      }
+      const float zm = nm == -INFINITY ? 0.f : nm, zo = no == -INFINITY ? 0.f : no;   // 2^-inf = 0, and no inf - inf
+      l[k] *= ex2(m[k] - zm);
+      const float r = ex2(om[k] - zo);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[k][v] *= r;
+      m[k] = nm;
+      om[k] = no;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        l[k] = fmaf(st[k][b].z, ex2(st[k][b].x - zm), l[k]);
+        const float w = ex2(st[k][b].y - zo);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[k][v] = fmaf(val[k][b][v], w, acc[k][v]);
+      }
     }
-    const float r = l == 0.f ? 0.f : ex2(om - m - kShift) / l;
-    const int64_t row = (row0 + col / p.g) * p.Hq + mt.y * p.g + col % p.g;
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int col = col0 + warp + k * kCombineWarps;
+    if (col >= mt2.x) continue;
+    const float r = l[k] == 0.f ? 0.f : ex2(om[k] - m[k] - kShift) / l[k];
+    const int tok = over_group(p, col);
+    const int64_t row = (int64_t)(mt.w + tok) * p.Hq + mt.y * p.g + col - tok * p.g;
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(acc[v] * r, acc[v + 1] * r);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(acc[k][v] * r, acc[k][v + 1] * r);
       *reinterpret_cast<uint32_t*>(p.out + row * D + lane * V + v) = *reinterpret_cast<const uint32_t*>(&b);
     }
-    if (p.lse && lane == 0) p.lse[row] = (m + lg2(l)) * kLn2;
+    if (p.lse && lane == 0) p.lse[row] = (m[k] + lg2(l[k])) * kLn2;
   }
 }
 
