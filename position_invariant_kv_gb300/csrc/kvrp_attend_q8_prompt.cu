@@ -577,7 +577,9 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         if (!ok) break;
         vref = next_vref(vref, sh.vs_top[slot]);
         const int held = u.len - j * N;   // a slot past the sequence may hold anything, NaN included
-        const float scale = vref > 0.f ? 128.f / vref : 0.f;
+        // A scale enters relative to vref before the 2^7 does: 2^7 / vref alone passes fp32's range where all
+        // of a tile's blocks are zeros (scale 2^-126).
+        const float inv = vref > 0.f ? 1.f / vref : 0.f;
         const uint32_t from = smem + L::kOffV + vs * L::kKV;
         uint4 w[kEach];
 #pragma unroll
@@ -599,7 +601,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
           const int tok = tok0 + kHop * i;
-          const __half2 r2 = __float2half2_rn(sh.vs[slot][tok / kPage] * scale);
+          const __half2 r2 = __float2half2_rn(sh.vs[slot][tok / kPage] * inv * 128.f);
           const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
           const uint32_t row = to + (c / 4) * (N * 128) + tok * 128;   // of the 64-column block c / 4
 #pragma unroll

@@ -1,0 +1,104 @@
+"""kv_attend_q8 where its caches, queries and scores leave the ordinary: zero and tiny values,
+tiny queries, value scales far apart, values that are not finite, scores that rise along the
+sequence.  Against the fp64 oracle (oracle/serve.py), element by element, in both kernels.
+
+Bars, derived from the roundings.  A query enters the score product with an error of at most
+2^-17 of its row's largest element, a score is an fp32 sum of products: a score is off by
+delta = 2^-17 scale max|q| sum|k| + 2^-16 scale sum|q k| at most, its weight by 2 delta of
+itself (delta is far below 1), and by 2^-11 more from its f16 rounding, which is at most
+2^-32 of the row's largest weight times value scale below f16's normal range (values are at
+most 448 scales).  Sums are fp32: 2^-11 covers them and the accumulator's corrections, one for
+each of at most 2^9 tiles.  The store adds half a bf16 step.  The log-sum-exp is off by 2 delta
+and 2^-12, and 2^-20 of its size."""
+import numpy as np
+import pytest
+import torch
+
+from oracle.serve import attend_rows, e4m3_round
+from serve_util import bf16, bf16_bits_to_f64, dev, f64, i32, round_to_bf16_bits
+from test_gpu_attend_q8 import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from position_invariant_kv_gb300.build import build
+    build()
+
+
+FLOOR = 2.0 ** -126   # the scale of a block of zeros
+# few rows: one tile of columns, two tiles; many rows: one Q tile, several units and parts of them
+SHAPES = {
+    "few_128": dict(ctx=[0, 14, 333], rows=[3, 4, 4], hq=4, hkv=2, d=128),
+    "few_64": dict(ctx=[13, 700], rows=[2, 4], hq=16, hkv=4, d=64),
+    "few_long": dict(ctx=[6001], rows=[2], hq=7, hkv=1, d=128),
+    "many_128": dict(ctx=[5, 190], rows=[41, 120], hq=7, hkv=1, d=128),
+    "many_64": dict(ctx=[0, 250], rows=[70, 90], hq=8, hkv=2, d=64),
+    "many_long": dict(ctx=[6000], rows=[40], hq=7, hkv=1, d=128),
+    "many_long_64": dict(ctx=[6007], rows=[40], hq=4, hkv=1, d=64),
+}
+each_shape = pytest.mark.parametrize("shape", SHAPES)
+
+
+def send(c):
+    """The case's values, scales and queries onto the device (slots no sequence uses stay NaN)."""
+    used = np.zeros((c.pages, 16), bool)
+    for s, n in enumerate(c.lens):
+        used[c.table[s][np.arange(n) // 16], np.arange(n) % 16] = True
+    for j in range(2):
+        t = torch.from_numpy(c.val[j].astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8)
+        t[torch.from_numpy(~used)] = 0x7F
+        c.pool[j].copy_(t)
+        c.dsc[j].copy_(torch.from_numpy(c.scale[j].astype(np.float32)))
+    c.dq = dev(c.q)
+
+
+def check(c):
+    send(c)
+    c.run()
+    torch.cuda.synchronize()
+    assert int(c.status) == 0
+    got, lse = f64(c.out), f64(c.lse)
+    q, g = bf16_bits_to_f64(c.q), c.hq // c.hkv
+    for s in range(len(c.rows)):
+        a, b = c.starts[s], c.starts[s + 1]
+        k, v = c.sequence(s)
+        with np.errstate(invalid="ignore"):
+            ref, ref_lse, mag = attend_rows(q[a:b], k, v, c.hkv, c.sm)
+        n = c.lens[s]
+        vs = c.scale[1][c.table[s][np.arange(n) // 16]]
+        for i in range(b - a):
+            t = c.lens[s] - (b - a) + i + 1
+            for j in range(c.hq):
+                kk, row = k[:t, j // g], q[a + i, j]
+                assert np.array_equal(np.isnan(got[a + i, j]), np.isnan(ref[i, j])), (s, i, j)
+                assert np.isnan(lse[a + i, j]) == np.isnan(ref_lse[i, j])
+                if np.isnan(ref_lse[i, j]):
+                    continue
+                delta = c.sm * (2.0 ** -17 * np.abs(row).max() * np.abs(kk).sum(1) + 2.0 ** -16 * np.abs(kk) @ np.abs(row)).max()
+                assert delta < 2.0 ** -5
+                x = c.sm * (kk @ row)
+                tiny = t * 2.0 ** -32 * 448 * np.exp(x - ref_lse[i, j] + np.log(vs[:t, j // g])).max()
+                ok = ~np.isnan(ref[i, j])
+                room = 2.0 ** -8 * np.abs(ref[i, j]) + (2 * delta + 2.0 ** -10) * mag[i, j] + tiny + 2.0 ** -133
+                err = np.abs(got[a + i, j] - ref[i, j])
+                assert np.all(err[ok] <= room[ok]), (s, i, j, (err[ok] / room[ok]).max())
+                assert abs(lse[a + i, j] - ref_lse[i, j]) <= 2 * delta + 2.0 ** -12 + 2.0 ** -20 * abs(ref_lse[i, j]), (s, i, j)
+
+
+@each_shape
+@pytest.mark.parametrize("where", ["all", "first", "middle"])
+def test_zero_values(shape, where):
+    """Blocks of zero values, which the library writes with the scale 2^-126: everywhere, in the first
+    token tiles, and over the part of a long context at which some CTAs' shares begin."""
+    c = Case(**SHAPES[shape])
+    for s, n in enumerate(c.lens):
+        pages = -(-n // 16)
+        lo, hi = {"all": (0, pages), "first": (0, min(pages, 8)), "middle": (pages // 6, 5 * pages // 6)}[where]
+        c.val[1][c.table[s][lo:hi]], c.scale[1][c.table[s][lo:hi]] = 0, FLOOR
+    check(c)
+    if where == "all":
+        assert bool((c.out == 0).all())
