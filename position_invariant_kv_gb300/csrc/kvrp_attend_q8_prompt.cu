@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           // Both issuers have done tile n - 4's scores, so both softmax groups have read tile n - 5's, and
           // V's warps are past tile n - 5: nobody needs slot n - 8 any more.
           if (lane < kMostPages) {
-            sh.ks[slot][lane] = fmaxf(fk, 1e-30f);   // above 0, so that a masked score stays -inf
+            sh.ks[slot][lane] = fk;
             sh.vs[slot][lane] = fv;
           }
           float most = fv;   // 0 in the lanes without a page
@@ -734,10 +734,16 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         if (__builtin_expect((j + 1) * N > first_limit, 0)) {
           const int seen = limit - j * N;   // columns below this are visible
 #pragma unroll
-          for (int q = 0; q < L::kP; ++q)
+          for (int q = 0; q < L::kP; ++q) {
+            // A masked score is -inf times its page's factor, which has to be above 0.  A page of which the row
+            // sees nothing, or which is not there, has no say; one that it sees at least fp32's smallest normal
+            // number: with less its scores, products below 2^25, vanish either way.
+            if (16 * q >= seen) f[q] = 1.f;
+            else if (f[q] < kLeastFactor) f[q] = kLeastFactor;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (16 * q + i >= seen) asm volatile("mov.b32 %0, 0xff800000;" : "=r"(r[q][i]));   // -inf
+          }
         }
         float top = -INFINITY;
 #pragma unroll

@@ -102,3 +102,32 @@ def test_zero_values(shape, where):
     check(c)
     if where == "all":
         assert bool((c.out == 0).all())
+
+
+@each_shape
+@pytest.mark.parametrize("size", [-42, -60, -100])
+def test_tiny_queries(shape, size):
+    """Rows far below one, and a row of zeros: the mean of the values."""
+    c = Case(**SHAPES[shape])
+    q = bf16_bits_to_f64(c.q) * np.exp2(size)
+    q[0, 0] = 0
+    q[-1, -1] /= np.exp2(size)
+    c.q = round_to_bf16_bits(q)
+    check(c)
+
+
+@each_shape
+def test_tiny_softmax_scale(shape):
+    c = Case(**SHAPES[shape])
+    c.sm = 1e-30
+    check(c)
+
+
+@each_shape
+@pytest.mark.parametrize("size", [116])
+def test_keys_at_the_scale_floor(shape, size):
+    """Keys in blocks of the smallest scale, under queries so large that the scores do not vanish."""
+    c = Case(**SHAPES[shape])
+    c.scale[0][:] = FLOOR
+    c.q = round_to_bf16_bits(bf16_bits_to_f64(c.q) * np.exp2(size) * (2.0 if size > 0 else 1.0))
+    check(c)
