@@ -443,7 +443,9 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               const int seen = pg + w < cc.end ? limit[nt][b] - (pg + w) * kPage : 0;
-              if (f[w][nt][b] == 0.f) f[w][nt][b] = 1.f;   // no scale: the scores are 0, and -inf stays -inf
+              // -inf times the factor has to stay -inf, also where the page has no say or the product underflows
+              if (seen <= 0) f[w][nt][b] = 1.f;
+              else if (f[w][nt][b] < kLeastFactor) f[w][nt][b] = kLeastFactor;
               if (gid >= seen) make_minus_inf(c[w][nt][b]);
               if (gid + 8 >= seen) make_minus_inf(c[w][nt][2 + b]);
             }

@@ -124,9 +124,10 @@ def test_tiny_softmax_scale(shape):
 
 
 @each_shape
-@pytest.mark.parametrize("size", [116])
+@pytest.mark.parametrize("size", [-30, 116])
 def test_keys_at_the_scale_floor(shape, size):
-    """Keys in blocks of the smallest scale, under queries so large that the scores do not vanish."""
+    """Keys in blocks of the smallest scale, under queries for which the scores vanish and under ones so
+    large that they do not."""
     c = Case(**SHAPES[shape])
     c.scale[0][:] = FLOOR
     c.q = round_to_bf16_bits(bf16_bits_to_f64(c.q) * np.exp2(size) * (2.0 if size > 0 else 1.0))
