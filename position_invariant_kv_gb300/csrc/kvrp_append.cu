@@ -87,12 +87,17 @@ __device__ __forceinline__ bool find_run(const Params& p, int want, Run* out, in
     return true;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (want == 0)   // tells what is out of range past the first pass, which the scan below may leave before
+    for (int s = kThreads + threadIdx.x; s < q.n_seqs; s += kThreads) {
+      int row0, rows, len;
+      if (!sequence(q, s, row0, rows, len)) flag(p.status, KVRP_DEV_BAD_LENGTH);
+    }
   int before = 0;   // runs of the sequences scanned so far
   for (int s0 = 0; s0 < q.n_seqs; s0 += kThreads) {
     const int s = s0 + threadIdx.x;
     int row0 = 0, rows = 0, len = 0, runs = 0;
     if (s < q.n_seqs) {
-      if (!sequence(q, s, row0, rows, len) && want == 0) flag(p.status, KVRP_DEV_BAD_LENGTH);
+      if (!sequence(q, s, row0, rows, len) && want == 0 && s0 == 0) flag(p.status, KVRP_DEV_BAD_LENGTH);
       if (rows > 0) runs = (len - 1) / kPage - (len - rows) / kPage + 1;
     }
     int sum = runs;
