@@ -329,6 +329,18 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
 #pragma unroll 1
   for (int i = 0; i < kStages; ++i) issue();
 
+  // A lane's V fragment of a page: tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9, features gid FPL ..
+  auto token_of = [&](int i) { return 2 * tig + (i & 1) + (i >> 1) * 8; };
+  auto load_v = [&](uint32_t box, int i, uint32_t (&v)[FPL / 4]) {
+    if constexpr (D == 128) {
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(box + box_offset<D>(token_of(i), gid)));
+    } else {
+      asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                   : "=r"(v[0]), "=r"(v[1]) : "r"(box + box_offset<D>(token_of(i), gid >> 1) + (gid & 1) * 8));
+    }
+  };
+
   Cursor cc = plan.at;   // the segment being computed
   Seq cq = plan.seq;
   int c_st = 0;
@@ -402,10 +414,10 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
       __syncwarp();   // every lane's copies of the stage have landed
       if (++c_st == kStages) c_st = 0;
       const uint32_t kat = ring + (uint32_t)st * C::kStage, vat = kat + PG * kBox;
-      // ---- S = K Q^T -----------------------------------------------------------------
-      float c[PG][NT][4], f[PG][NT][2], lvs[PG];   // raw scores; x = c f; log2 of the value scales
       // the pages next to the end: a row sees its own position and before; the share's end cuts a step
       const bool tail = (pg + PG) * kPage > ctx + 1 || pg + PG > cc.end;
+      // ---- S = K Q^T -----------------------------------------------------------------
+      float c[PG][NT][4], f[PG][NT][2], lvs[PG];   // raw scores; x = c f; log2 of the value scales
       bool grow = false;
 #pragma unroll
       for (int w = 0; w < PG; ++w) {
@@ -511,27 +523,59 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
       // ---- O^T += V^T P^T --------------------------------------------------------------
 #pragma unroll
       for (int w = 0; w < PG; ++w) {
-        uint32_t v[4][FPL / 4];   // tokens 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9: features gid FPL ..
+        uint32_t v[4][FPL / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 2 * tig + (i & 1) + (i >> 1) * 8;
-          if constexpr (D == 128) {
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
-                         : "r"(vat + w * kBox + box_offset<D>(t, gid)));
-          } else {
-            asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
-                         : "=r"(v[i][0]), "=r"(v[i][1])
-                         : "r"(vat + w * kBox + box_offset<D>(t, gid >> 1) + (gid & 1) * 8));
-          }
-        }
+        for (int i = 0; i < 4; ++i) load_v(vat + w * kBox, i, v[i]);
         if (tail) {   // a slot past the sequence, or past the share, may hold anything, NaN included
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int t = 2 * tig + (i & 1) + (i >> 1) * 8;
-            if ((pg + w) * kPage + t >= cq.len || pg + w >= cc.end) {
+            if ((pg + w) * kPage + token_of(i) >= cq.len || pg + w >= cc.end) {
 #pragma unroll
               for (int j = 0; j < FPL / 4; ++j) make_zero(v[i][j]);
+            }
+          }
+          // A NaN of a token that not all rows see: weight 0 would not keep it from the others.  It is taken out
+          // of the stage, byte by byte and on few registers, and the accumulators of the rows that do see it
+          // become NaN.  (Looking for it costs a sequence's last pages: 43.5 -> 44.5 us for 4 rows x 32 sequences.)
+          const int t0 = (pg + w) * kPage;
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t nan = 0;
+#pragma unroll
+            for (int j = 0; j < FPL / 4; ++j) nan |= q8::nan_bytes(v[i][j]);
+            odd |= nan && t0 + token_of(i) > ctx;
+          }
+          if (__any_sync(0xffffffffu, odd)) {
+            const int end = pg + w < cc.end ? cq.len : 0;
+#pragma unroll
+            for (int f = 0; f < FPL; ++f) {
+              int at = INT32_MAX;   // the first such token with a NaN in this lane's feature f
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int t = t0 + token_of(i);
+                const uint32_t byte = vat + w * kBox + box_offset<D>(token_of(i), gid * FPL / 16) + (gid * FPL + f) % 16;
+                uint32_t x;
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(byte));
+                if (t > ctx && t < end && (x & 0x7f) == 0x7f) {
+                  at = min(at, t);
+                  asm volatile("st.shared.u8 [%0], %1;" ::"r"(byte), "r"(0) : "memory");
+                }
+              }
+              at = min(at, __shfl_xor_sync(0xffffffffu, at, 1));
+              at = min(at, __shfl_xor_sync(0xffffffffu, at, 2));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                  if (at < limit[nt][b]) o[f / 2][nt][2 * (f % 2) + b] = __int_as_float(0x7fc00000);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              load_v(vat + w * kBox, i, v[i]);
+              if (t0 + token_of(i) >= end)
+#pragma unroll
+                for (int j = 0; j < FPL / 4; ++j) make_zero(v[i][j]);
             }
           }
         }

@@ -56,6 +56,12 @@ def send(c):
     c.dq = dev(c.q)
 
 
+def at(c, s, tokens):
+    """(page, slot) arrays of tokens of sequence s."""
+    tokens = np.asarray(tokens)
+    return c.table[s][tokens // 16], tokens % 16
+
+
 def check(c):
     send(c)
     c.run()
@@ -131,4 +137,28 @@ def test_keys_at_the_scale_floor(shape, size):
     c = Case(**SHAPES[shape])
     c.scale[0][:] = FLOOR
     c.q = round_to_bf16_bits(bf16_bits_to_f64(c.q) * np.exp2(size) * (2.0 if size > 0 else 1.0))
+    check(c)
+
+
+@pytest.mark.parametrize("shape", [n for n in SHAPES if n.startswith("few")])
+@pytest.mark.parametrize("what", ["v", "v_all_heads", "k"])
+def test_nan_in_a_later_row(shape, what):
+    """A value that is not finite reaches the rows that see its token, no others."""
+    c = Case(**SHAPES[shape])
+    for s, n in enumerate(c.lens):
+        rows = c.rows[s]
+        for token, feature in ((n - 1, 3), (n - 1, c.d - 1), (n - rows // 2 - 1, 17), (n - rows // 2 - 1, 3)):
+            page, slot = at(c, s, token)
+            head = slice(None) if what == "v_all_heads" else c.hkv - 1
+            c.val[0 if what == "k" else 1][page, slot, head, feature] = np.nan
+    check(c)
+
+
+@pytest.mark.parametrize("shape", [n for n in SHAPES if n.startswith("few")])
+@pytest.mark.parametrize("token", [0, 100])
+def test_nan_before_all_rows(shape, token):
+    c = Case(**SHAPES[shape])
+    for s, n in enumerate(c.lens):
+        page, slot = at(c, s, min(token, n - 1))
+        c.val[1][page, slot, 0, 5] = np.nan
     check(c)
