@@ -67,6 +67,7 @@ namespace {
 
 constexpr int kRows = 128;                 // rows of a Q tile
 constexpr int kWarpsAll = 16, kThreadsAll = 32 * kWarpsAll;
+constexpr int kWarpsRows = 8, kMostFeatures = 128;   // the softmax warps; head_dim at most
 constexpr int kScaleSlots = 8;             // tiles whose scales are kept
 constexpr int kMostPages = 8;              // pages of a token tile
 constexpr uint32_t kNoRow = 0xffffffffu;   // a row of the tile that no query fills
@@ -91,7 +92,7 @@ struct Prompt {
   static_assert(2 * kRegsRow + kRegsV + kRegsMisc <= 4 * 128, "more registers than the block holds");
   static constexpr int kOffK = 4 * kQ, kOffV = kOffK + kKst * kKV, kOffVc = kOffV + kVst * kKV;
   static constexpr int kSmem = 1024 + kOffVc + kCst * kVc;
-  static_assert(kSmem <= 227 * 1024 - 2048, "shared memory");
+  static_assert(kSmem <= 227 * 1024 - 8192, "shared memory");
 };
 
 // ---- tensor-core pieces ------------------------------------------------------------------
@@ -256,6 +257,8 @@ struct Shared {
   Unit first;
   int found;
   int abort_flag;
+  int later_nan;          // a value taken out of a product because not all rows of its unit see it was NaN
+  int nan_at[kWarpsRows][kMostFeatures];   // then: the first token with one, by features, a softmax warp's unit
   uint32_t tmem;
 };
 template <int N>
@@ -344,12 +347,39 @@ __device__ __forceinline__ int active_tiles(const Params& p, const Unit& u) {   
 }
 // x / g for 0 <= x < 2^28 (the host keeps rows x group below): by a product with 2^32 / g, rounded up.
 __device__ __forceinline__ int over_group(const Params& p, int x) { return (int)((uint64_t)(uint32_t)x * p.g_inverse >> 32); }
+// Tokens below this are seen by all rows of the unit.
+__device__ __forceinline__ int seen_by_all(const Params& p, const Unit& u) {
+  return u.len - u.rows + over_group(p, u.rt * kPromptRows) + 1;
+}
 // The reference of the value scales after a tile: a power of two at least the largest scale,
 // two octaves above it when it moves, so that it moves seldom.
 __device__ __forceinline__ float next_vref(float vref, float top) {
   if (!(top > vref)) return vref;
   const uint32_t e = (__float_as_uint(top) + 0x7fffffu) >> 23;   // 2^ceil(log2 top)
   return __uint_as_float(min(e + 2u, 254u) << 23);
+}
+
+// The first of the tokens [from, to) of sequence s whose value is NaN, for each feature of KV head h (INT32_MAX:
+// none), by a warp.  Reads the values again; a cache without such values never comes here.
+template <int D>
+__device__ __noinline__ void find_later_nan(const Params& p, int s, int h, int from, int to, int* at) {
+  constexpr int kEach = D / 32;
+  const int lane = threadIdx.x & 31;
+  int first[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) first[e] = INT32_MAX;
+  for (int t = to - 1; t >= from; --t) {
+    const int page = p.seqs.block_tables[(int64_t)s * p.seqs.table_stride + t / kPage];
+    if (page < 0 || page >= p.seqs.num_pages) continue;
+    const uint8_t* v = p.v_pool + (((int64_t)page * kPage + t % kPage) * p.Hkv + h) * D + lane * kEach;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if ((v[e] & 0x7f) == 0x7f) first[e] = t;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) at[lane * kEach + e] = first[e];
+  __syncwarp();
 }
 
 template <int D>
@@ -391,6 +421,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       mbar_init(drained(t), 1);
     }
     sh.abort_flag = 0;
+    sh.later_nan = 0;
     mbar_init_fence();
   }
   if (warp == 13) tmem_alloc(smem_u32(&sh.tmem), 512);
@@ -571,6 +602,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     bool ok = true;
     do {
       float vref = 0.f;
+      const int seen_all = seen_by_all(p, u);
       for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
         const int vs = n % L::kVst, vb = n % L::kCst, slot = n % kScaleSlots;
         ok = wait(vfull(vs), (n / L::kVst) & 1);
@@ -593,6 +625,24 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
             make_zero(w[i].z);
             make_zero(w[i].w);
           }
+        }
+        const int from_tok = seen_all - j * N;
+        if (__builtin_expect(from_tok < N, 0)) {
+          // A NaN of a token that not all rows see: weight 0 would not keep it from the others' sums.  It is
+          // taken out, and the softmax warps put it into the rows that do see the token.
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            if (tok0 + kHop * i < from_tok) continue;
+            uint32_t* const x[4] = {&w[i].x, &w[i].y, &w[i].z, &w[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t nan = q8::nan_bytes(*x[e]);
+              odd |= nan != 0;
+              *x[e] &= ~((nan >> 7) * 0xffu);
+            }
+          }
+          if (odd) *static_cast<volatile int*>(&sh.later_nan) = 1;
         }
         mbar_arrive(vempty(vs));
         ok = wait(cempty(vb), ((n / L::kCst) & 1) ^ 1);
@@ -824,6 +874,8 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       const bool whole = begins && ends;
       const float f = l == 0.f ? 0.f : vref * 0x1p-14f / l;
       float* part = p.partial + ((int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * p.cols + t * kRows) * (D + 4);
+      const bool odd = uniform(*static_cast<volatile int*>(&sh.later_nan)) != 0;
+      if (odd) find_later_nan<D>(p, u.s, u.h, max(seen_by_all(p, u), u.j0 * N), min(u.len, u.j1 * N), sh.nan_at[warp]);
       auto stage = [&](int x, uint32_t a, uint32_t b2, uint32_t c2, uint32_t d) {
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row_chunk(x / kHalf, row, x % kHalf)), "r"(a), "r"(b2), "r"(c2), "r"(d) : "memory");
       };
@@ -867,6 +919,17 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           uint4 v;
           asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                        : "r"((from ^ swizzle) + i * kAtOnce * D));
+          if (odd) {   // rows that see a value that was taken out
+            const int lim = __shfl_sync(0xffffffffu, limit, i * kAtOnce + sub);
+            const int* at = sh.nan_at[warp] + (whole ? 8 * x : pass * (D / 2) + 4 * x);
+            uint32_t* const word[4] = {&v.x, &v.y, &v.z, &v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (!whole && at[e] < lim) *word[e] = 0x7fc00000u;
+              if (whole && at[2 * e] < lim) *word[e] |= 0x7fc0u;
+              if (whole && at[2 * e + 1] < lim) *word[e] |= 0x7fc00000u;
+            }
+          }
           if (to_row != kNoRow) {
             if (whole) *reinterpret_cast<uint4*>(to_out + (int64_t)to_row * (2 * D)) = v;
             else *reinterpret_cast<uint4*>(to_part + i * kAtOnce * (D + 4) * 4) = v;

@@ -140,7 +140,7 @@ def test_keys_at_the_scale_floor(shape, size):
     check(c)
 
 
-@pytest.mark.parametrize("shape", [n for n in SHAPES if n.startswith("few")])
+@each_shape
 @pytest.mark.parametrize("what", ["v", "v_all_heads", "k"])
 def test_nan_in_a_later_row(shape, what):
     """A value that is not finite reaches the rows that see its token, no others."""
@@ -154,7 +154,7 @@ def test_nan_in_a_later_row(shape, what):
     check(c)
 
 
-@pytest.mark.parametrize("shape", [n for n in SHAPES if n.startswith("few")])
+@each_shape
 @pytest.mark.parametrize("token", [0, 100])
 def test_nan_before_all_rows(shape, token):
     c = Case(**SHAPES[shape])
