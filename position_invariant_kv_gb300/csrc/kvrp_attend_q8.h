@@ -24,6 +24,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kShift = 7.f;       // weights of the accumulator are exp2(. + 7)
 constexpr float kLazy = 8.f;        // how far a score may pass the running maximum
 constexpr float kLeastFactor = 1.17549435e-38f;   // 2^-126: what a score is multiplied with where some are masked
+constexpr float kZeroBlock = 0x1p-126f;    // a zero block's scale, which a page outside the pool reads as
 constexpr int kMaxCtasPerSm = 2, kMaxCtas = 1024;   // bounds of the grid
 constexpr int kMaxCols = 16;        // rows x group of the decode kernel
 

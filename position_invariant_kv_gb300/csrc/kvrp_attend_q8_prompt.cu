@@ -16,7 +16,9 @@
 //     twice the f16 rate cost what one would, without converting K.
 //   - O += P V by kind::f16: P as f16 from TMEM, V as f16 in shared memory, converted from e4m3
 //     by four warps together with the page's scale relative to a running reference (a power
-//     of two): exact for power-of-two scales within 2^14 of each other.
+//     of two), exact for powers of two within 2^12 of it.  From the first tile on whose scales lie
+//     farther apart, a unit's part has V unscaled and the scales in the weights' exponent, with a
+//     running maximum of x + log2 vs for the accumulator beside that of x for the sum.
 //   - Two 128-row Q tiles a CTA, each with its own softmax warps (a thread a row) and its own
 //     MMA issuer.  TMEM holds for each the accumulator, the scores and, apart from them, the
 //     weights: the next tile's scores are formed while this one's are being turned into
@@ -72,6 +74,9 @@ constexpr int kScaleSlots = 8;             // tiles whose scales are kept
 constexpr int kMostPages = 8;              // pages of a token tile
 constexpr uint32_t kNoRow = 0xffffffffu;   // a row of the tile that no query fills
 constexpr float kVShift = 7.f;             // V enters as v * vs * 2^7 / vref: up to 448 * 128 in f16
+// With a reference, a value scale is at least kNear of it, so that its products with e4m3 values (multiples of 2^-9)
+// and 2^7 are f16's normal numbers; and the part's first reference at least kReach of it.
+constexpr float kNear = 0x1p-12f, kReach = 0x1p-48f;
 
 template <int D>
 struct Prompt {
@@ -88,7 +93,7 @@ struct Prompt {
   static __host__ __device__ constexpr int tmem_o(int t) { return D == 128 ? 256 + t * 128 : 384 + t * 64; }
   // Registers a thread of the softmax (which holds a row of scores), V and other warps: the
   // 4 x 128 that the warp groups were launched with, shared out anew.
-  static constexpr int kRegsRow = D == 128 ? 168 : 184, kRegsV = 88, kRegsMisc = D == 128 ? 88 : 56;
+  static constexpr int kRegsRow = D == 128 ? 168 : 200, kRegsV = D == 128 ? 88 : 64, kRegsMisc = D == 128 ? 88 : 48;
   static_assert(2 * kRegsRow + kRegsV + kRegsMisc <= 4 * 128, "more registers than the block holds");
   static constexpr int kOffK = 4 * kQ, kOffV = kOffK + kKst * kKV, kOffVc = kOffV + kVst * kKV;
   static constexpr int kSmem = 1024 + kOffVc + kCst * kVc;
@@ -250,7 +255,7 @@ struct Shared {
   __align__(8) uint64_t bars[40];
   __align__(16) float ks[kScaleSlots][kMostPages];   // a tile's scales of K,
   float vs[kScaleSlots][kMostPages];                 // of V,
-  float vs_top[kScaleSlots];                         // and the largest of V's
+  float vref[kScaleSlots];                           // and the reference of V's, 0 from where they lie apart
   int64_t cost[kWarpsAll];
   int64_t total, end;     // the cost in all, and where this CTA's share ends
   int n_cta;
@@ -463,12 +468,16 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       bool ok = true;
       do {
         const int pages = (u.len + kPage - 1) / kPage;
+        // The reference of the value scales; none from a tile on whose scales lie too far apart for it, or from where
+        // it is too far from the first one for the accumulator that began relative to that.
+        float vref = 0.f, first_vref = 0.f;
+        bool apart = false;
         for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
           const int ks = n % L::kKst, vs = n % L::kVst, slot = n % kScaleSlots;
           const int pg = j * L::kP + lane;
           const bool mine = lane < L::kP && pg < pages;
           int page = p.seqs.num_pages;   // past the pool: the box reads zeros
-          float fk = 0.f, fv = 0.f;
+          float fk = 0.f, fv = mine ? kZeroBlock : 0.f;
           if (mine) {
             const int e = p.seqs.block_tables[(int64_t)u.s * p.seqs.table_stride + pg];
             if (e >= 0 && e < p.seqs.num_pages) {
@@ -487,10 +496,14 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
             sh.ks[slot][lane] = fk;
             sh.vs[slot][lane] = fv;
           }
-          float most = fv;   // 0 in the lanes without a page
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-          if (lane == 0) sh.vs_top[slot] = most;
+          // positive numbers are in the order of their bits
+          const uint32_t least = __reduce_min_sync(0xffffffffu, mine ? __float_as_uint(fv) : 0x7f7fffffu);
+          const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fv));
+          const float next = next_vref(vref, __uint_as_float(most));
+          if (j == u.j0) first_vref = next;
+          apart |= __uint_as_float(least) < next * kNear || first_vref < next * kReach;
+          vref = next;
+          if (lane == 0) sh.vref[slot] = apart ? 0.f : next;
           const uint32_t bytes = (uint32_t)min(L::kP, pages - j * L::kP) * kPage * D;
           __syncwarp();
           if (lane == 0) mbar_expect_tx(kfull(ks), bytes);
@@ -601,13 +614,12 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     int n = 0;
     bool ok = true;
     do {
-      float vref = 0.f;
       const int seen_all = seen_by_all(p, u);
       for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
         const int vs = n % L::kVst, vb = n % L::kCst, slot = n % kScaleSlots;
         ok = wait(vfull(vs), (n / L::kVst) & 1);
         if (!ok) break;
-        vref = next_vref(vref, sh.vs_top[slot]);
+        const float vref = sh.vref[slot];
         const int held = u.len - j * N;   // a slot past the sequence may hold anything, NaN included
         // A scale enters relative to vref before the 2^7 does: 2^7 / vref alone passes fp32's range where all
         // of a tile's blocks are zeros (scale 2^-126).
@@ -651,7 +663,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
           const int tok = tok0 + kHop * i;
-          const __half2 r2 = __float2half2_rn(sh.vs[slot][tok / kPage] * inv * 128.f);
+          const __half2 r2 = __float2half2_rn(vref > 0.f ? sh.vs[slot][tok / kPage] * inv * 128.f : 128.f);
           const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
           const uint32_t row = to + (c / 4) * (N * 128) + tok * 128;   // of the 64-column block c / 4
 #pragma unroll
@@ -689,6 +701,17 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     // two rows of a thread's row are where its results are laid out for whole-row stores.
     auto row_chunk = [&](int part, int r, int x) {
       return smem + (2 * t + part) * L::kQ + r * D + (D == 128 ? ((x ^ (r & 7)) << 4) : ((x ^ ((r >> 1) & 3)) << 4));
+    };
+    auto scale_accumulator = [&](float fix) {
+#pragma unroll
+      for (int b = 0; b < D / 16; ++b) {
+        uint32_t o[16];
+        tmem_ld16(O + 16 * b, o);
+        tmem_wait_ld(o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+        tmem_st16(O + 16 * b, o);
+      }
     };
     do {
       const bool begins = u.j0 == 0, ends = u.j1 == u.n_kv;
@@ -766,7 +789,9 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         mbar_arrive(qfull(t));
       }
       float m = -INFINITY, l = 0.f, vref = 0.f;
-      for (int j = u.j0; j < u.j1; ++j, ++n, ++ns) {
+      bool apart = false;
+      int j = u.j0;
+      for (; j < u.j1; ++j, ++n, ++ns) {
         ok = wait(sfull(t), ns & 1);
         if (!ok) break;
         tc_fence_after();
@@ -776,9 +801,11 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         float f[L::kP];
 #pragma unroll
         for (int q = 0; q < L::kP; ++q) f[q] = sh.ks[n % kScaleSlots][q] * c;
-        const float nvref = next_vref(vref, sh.vs_top[n % kScaleSlots]);
+        const float nvref = sh.vref[n % kScaleSlots];
+        apart = !(nvref > 0.f);
 #pragma unroll
         for (int q = 0; q < L::kP; ++q) tmem_wait_ld(r[q]);
+        if (__builtin_expect(apart, 0)) break;
         tc_fence_before();
         mbar_arrive(sread(t));
         if (__builtin_expect((j + 1) * N > first_limit, 0)) {
@@ -820,15 +847,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
             ok = wait(ofull(t), (ns - 1) & 1);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int b = 0; b < D / 16; ++b) {
-              uint32_t o[16];
-              tmem_ld16(O + 16 * b, o);
-              tmem_wait_ld(o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
-              tmem_st16(O + 16 * b, o);
-            }
+            scale_accumulator(fix);
           }
           if (!ok) break;
         }
@@ -861,18 +880,84 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         const float2 sum = unpair2(sum2);
         l += sum.x + sum.y;
       }
+      float om = m + lg2(vref);   // the accumulator holds sums of 2^(x - om + 14) times v
+      if (__builtin_expect(apart, 0)) {
+        // The part's remaining tiles, from one whose scales lie apart: the accumulator's weights are
+        // 2^(x + log2 vs - om + 7).  Rare, so by pages, from TMEM as often as the scores are needed.
+        if (m == -INFINITY) om = -INFINITY;
+#pragma unroll 1
+        while (ok) {
+          const int slot = n % kScaleSlots, seen = limit - j * N;
+          const auto scores = [&](int q, uint32_t (&x)[16]) {
+            tmem_ld16(S + 16 * q, x);
+            tmem_wait_ld(x);
+            const float f = sh.ks[slot][q] * c;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = 16 * q + i < seen ? __float_as_uint(__uint_as_float(x[i]) * f) : 0xff800000u;
+          };
+          float top = -INFINITY, high = -INFINITY;
+#pragma unroll 1
+          for (int q = 0; q < L::kP; ++q) {
+            uint32_t x[16];
+            scores(q, x);
+            float a = __uint_as_float(x[0]);
+#pragma unroll
+            for (int i = 1; i < 16; ++i) a = fmaxf(a, __uint_as_float(x[i]));
+            top = fmaxf(top, a);
+            high = fmaxf(high, a + lg2(sh.vs[slot][q]));
+          }
+          if (top > m + kLazy) {
+            l *= ex2(m - top);
+            m = top;
+          }
+          float fix = 1.f;
+          if (high > om + kLazy) {
+            fix = ex2(om - high);
+            om = high;
+          }
+          if (j > u.j0) {
+            ok = wait(ofull(t), (ns - 1) & 1);   // the places of the weights are free, the accumulator is at rest
+            if (!ok) break;
+            tc_fence_after();
+            if (__any_sync(0xffffffffu, fix != 1.f)) scale_accumulator(fix);
+          }
+          const float zm = m == -INFINITY ? 0.f : m, zo = om == -INFINITY ? 0.f : om;
+#pragma unroll 1
+          for (int q = 0; q < L::kP; ++q) {
+            uint32_t x[16], w[8];
+            scores(q, x);
+            const float base = kShift + lg2(sh.vs[slot][q]) - zo;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float a = __uint_as_float(x[2 * i]), b = __uint_as_float(x[2 * i + 1]);
+              l += ex2(a - zm + kShift) + ex2(b - zm + kShift);
+              w[i] = pack_f16(ex2(a + base), ex2(b + base));
+            }
+            tmem_st8(P + 8 * q, w);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(sread(t));
+          mbar_arrive(pfull(t, 0));
+          mbar_arrive(pfull(t, 1));
+          ++n, ++ns;
+          if (++j == u.j1) break;
+          ok = wait(sfull(t), ns & 1);
+          tc_fence_after();
+        }
+      }
       if (!ok) break;
       // ---- the part's result -----------------------------------------------------------------
       ok = wait(ofull(t), (ns - 1) & 1);
       if (!ok) break;
       tc_fence_after();
       l *= 0x1p-7f;   // 2^-kShift
-      const float om = m + lg2(vref) - kVShift;   // the accumulator holds sums of 2^(x - om + 7) times v
+      om -= kVShift;
       // Rows are laid out in shared memory, in the Q tile that the finished unit no longer needs, and
       // leave by whole rows (32 rows' 16 bytes an instruction took 2 us a unit): kRowChunks chunks a pass.
       constexpr int kRowChunks = D / 8, kHalf = D / 16;   // 16-byte chunks of the two parts, of one
       const bool whole = begins && ends;
-      const float f = l == 0.f ? 0.f : vref * 0x1p-14f / l;
+      const float f = l == 0.f ? 0.f : ex2(om - m - kShift) / l;
       float* part = p.partial + ((int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * p.cols + t * kRows) * (D + 4);
       const bool odd = uniform(*static_cast<volatile int*>(&sh.later_nan)) != 0;
       if (odd) find_later_nan<D>(p, u.s, u.h, max(seen_by_all(p, u), u.j0 * N), min(u.len, u.j1 * N), sh.nan_at[warp]);

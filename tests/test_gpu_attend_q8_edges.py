@@ -162,3 +162,39 @@ def test_nan_before_all_rows(shape, token):
         page, slot = at(c, s, min(token, n - 1))
         c.val[1][page, slot, 0, 5] = np.nan
     check(c)
+
+
+def along(c, s, steps):
+    """Keys of sequence s and all queries nearly along one direction: the scores of token t rise by steps[t] (natural units)."""
+    rng = np.random.default_rng(3)
+    u = np.sign(rng.standard_normal(c.d))
+    n = c.lens[s]
+    k = np.asarray(steps)[:, None, None] * u * (0.25 / (c.sm * c.d)) + 0.05 * rng.standard_normal((n, c.hkv, c.d))
+    page, slot = at(c, s, np.arange(n))
+    for p in np.unique(page):
+        mine = page == p
+        top = np.abs(k[mine]).max((0, 2))
+        c.scale[0][p] = np.exp2(np.ceil(np.log2(top / 448)))
+    c.val[0][page, slot] = e4m3_round(k / c.scale[0][page][:, :, None])
+    a, b = c.starts[s], c.starts[s + 1]
+    c.q[a:b] = bf16(rng, (b - a, c.hq, c.d), 0.1)
+    c.q[a:b] = round_to_bf16_bits(bf16_bits_to_f64(c.q[a:b]) + 4 * u)
+
+
+@each_shape
+def test_any_value_scales(shape):
+    check(Case(**SHAPES[shape], v_spread=30, pow2=False))
+
+
+@each_shape
+@pytest.mark.parametrize("gap", [0, 20, 60])
+@pytest.mark.parametrize("low,high", [(-40, 0), (-100, 20)])
+def test_weight_on_pages_of_small_value_scales(shape, gap, low, high):
+    """Every other run of pages holds values `high - low` octaves larger, under scores `gap` lower."""
+    c = Case(**SHAPES[shape])
+    for s, n in enumerate(c.lens):
+        small = np.arange(n) // 16 % 8 >= 4
+        along(c, s, gap * small.astype(float))
+        page, _ = at(c, s, np.arange(n))
+        c.scale[1][page] *= np.exp2(np.where(small, low, high))[:, None]
+    check(c)
