@@ -666,12 +666,12 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
           const int c = nt * 8 + 2 * tig + b;
           if (c >= cols) continue;
           if (begins && ends) {
-            const float r = l[nt][b] == 0.f ? 0.f : ex2(om[nt][b] - m[nt][b] - kShift) / l[nt][b];
+            const float2 r = result_factors(m[nt][b], om[nt][b], l[nt][b]);
             const int64_t row = (int64_t)(cq.row0 + c / p.g) * p.Hq + head * p.g + c % p.g;
             uint32_t w[FPL / 2];
 #pragma unroll
             for (int mt = 0; mt < KT; ++mt) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(o[mt][nt][b] * r, o[mt][nt][2 + b] * r);
+              const __nv_bfloat162 v = __floats2bfloat162_rn(o[mt][nt][b] * r.x * r.y, o[mt][nt][2 + b] * r.x * r.y);
               w[mt] = *reinterpret_cast<const uint32_t*>(&v);
             }
             uint4* to = reinterpret_cast<uint4*>(p.out + row * D + gid * FPL);
@@ -803,9 +803,10 @@ __global__ void __launch_bounds__(kCombineThreads, 5) combine_kernel(const __gri
       }
     }
     if (!live) continue;
-    const float r = l == 0.f ? 0.f : ex2(om - m - kShift) / l;
+    const float2 r = result_factors(m, om, l);
+    acc = make_float4(acc.x * r.x * r.y, acc.y * r.x * r.y, acc.z * r.x * r.y, acc.w * r.x * r.y);
     const int64_t row = (int64_t)(mt.w + c / p.g) * p.Hq + (mt.y * p.hg + hd) * p.g + c % p.g;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * r, acc.y * r), hi = __floats2bfloat162_rn(acc.z * r, acc.w * r);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
     *reinterpret_cast<uint2*>(p.out + row * D + 4 * f) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     if (p.lse && f == 0) p.lse[row] = (m + lg2(l)) * kLn2;

@@ -78,6 +78,14 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint32
   }
 }
 
+// What an accumulator is multiplied with in the end, 2^(om - m - 7) / l, in two factors: one alone leaves fp32's range
+// where value scales are near its ends.
+__device__ __forceinline__ float2 result_factors(float m, float om, float l) {
+  if (l == 0.f) return make_float2(0.f, 0.f);
+  const float d = om - m - kShift, half = fmaxf(0.5f * d, -100.f);   // d is -inf where all scales are 0
+  return make_float2(ex2(half), ex2(d - half) / l);
+}
+
 __device__ __forceinline__ void write_idle(const Params& p, int D) {
   // idle places of the batch (length 0): zeros, and no tokens' log-sum-exp
   for (int s = blockIdx.x; s < p.seqs.n_seqs; s += gridDim.x) {

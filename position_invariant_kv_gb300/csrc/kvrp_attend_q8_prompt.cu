@@ -957,7 +957,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       // leave by whole rows (32 rows' 16 bytes an instruction took 2 us a unit): kRowChunks chunks a pass.
       constexpr int kRowChunks = D / 8, kHalf = D / 16;   // 16-byte chunks of the two parts, of one
       const bool whole = begins && ends;
-      const float f = l == 0.f ? 0.f : ex2(om - m - kShift) / l;
+      const float2 f = result_factors(m, om, l);
       float* part = p.partial + ((int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * p.cols + t * kRows) * (D + 4);
       const bool odd = uniform(*static_cast<volatile int*>(&sh.later_nan)) != 0;
       if (odd) find_later_nan<D>(p, u.s, u.h, max(seen_by_all(p, u), u.j0 * N), min(u.len, u.j1 * N), sh.nan_at[warp]);
@@ -974,7 +974,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
             tmem_wait_ld(r);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[2 * i]) * f, __uint_as_float(r[2 * i + 1]) * f);
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[2 * i]) * f.x * f.y, __uint_as_float(r[2 * i + 1]) * f.x * f.y);
               w[i] = *reinterpret_cast<const uint32_t*>(&v);
             }
 #pragma unroll
@@ -1107,12 +1107,12 @@ __global__ void __launch_bounds__(32 * kCombineWarps) prompt_combine_kernel(cons
   for (int k = 0; k < kEach; ++k) {
     const int col = col0 + warp + k * kCombineWarps;
     if (col >= mt2.x) continue;
-    const float r = l[k] == 0.f ? 0.f : ex2(om[k] - m[k] - kShift) / l[k];
+    const float2 r = result_factors(m[k], om[k], l[k]);
     const int tok = over_group(p, col);
     const int64_t row = (int64_t)(mt.w + tok) * p.Hq + mt.y * p.g + col - tok * p.g;
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(acc[k][v] * r, acc[k][v + 1] * r);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(acc[k][v] * r.x * r.y, acc[k][v + 1] * r.x * r.y);
       *reinterpret_cast<uint32_t*>(p.out + row * D + lane * V + v) = *reinterpret_cast<const uint32_t*>(&b);
     }
     if (p.lse && lane == 0) p.lse[row] = (m[k] + lg2(l[k])) * kLn2;

@@ -198,3 +198,11 @@ def test_weight_on_pages_of_small_value_scales(shape, gap, low, high):
         page, _ = at(c, s, np.arange(n))
         c.scale[1][page] *= np.exp2(np.where(small, low, high))[:, None]
     check(c)
+
+
+@each_shape
+def test_tiny_values(shape):
+    """Values near fp32's smallest normal numbers."""
+    c = Case(**SHAPES[shape])
+    c.scale[1][:] = 2.0 ** -125
+    check(c)
