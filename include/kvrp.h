@@ -587,8 +587,8 @@ kvrp_status kv_attend_q8(
 /*
  * kvrp_test_set_wait_limit -- for tests of the failure path only.  Sets the
  * limit, in SM clock cycles, of the relocation kernel's pipeline waits in the
- * plans built from now on by any thread (0 restores the default of about one
- * second).  With a limit of a few hundred cycles the waits give up almost at
+ * plans built from now on by any thread, and of kv_attend_q8's kernel for many
+ * rows in the calls from now on (0 restores the default of about one second).  With a limit of a few hundred cycles the waits give up almost at
  * once: the launch then ORs KVRP_DEV_TIMEOUT into *d_status, lets its copies
  * and tensor-core work drain, frees its TMEM and returns, leaving the output
  * incomplete.  It never hangs the GPU, whatever the limit.

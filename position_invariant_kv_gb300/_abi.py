@@ -396,8 +396,9 @@ def kv_relocate_batch_mla(chunks, *, n_layers: int, kv_lora_dim: int, rope_dim: 
 
 
 def kvrp_test_set_wait_limit(cycles: int) -> None:
-    """Testing hook: the relocation kernel's pipeline wait limit in cycles for
-    plans built from now on (0 = the default, about one second)."""
+    """Testing hook: the pipeline wait limit in cycles of the relocation kernel, for
+    plans built from now on, and of kv_attend_q8's kernel for many rows (0 = the
+    default, about one second)."""
     lib().kvrp_test_set_wait_limit(int(cycles))
 
 

@@ -910,6 +910,7 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   p.unit_pages = std::max(1, 2048 / (hg * head_dim));   // about 2 us of a CTA's share of the bandwidth
   p.rounds = hg == 1 ? 4 : hg == 2 ? 3 : hg == 4 ? 2 : 0;
   p.scale = softmax_scale * 1.4426950408889634f;
+  p.wait_cycles = test_wait_limit() ? (long long)test_wait_limit() : ptx::kTimeoutCycles;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
   p.meta = reinterpret_cast<int4*>(base);
   p.partial = reinterpret_cast<float*>(base + attend_q8::meta_bytes(p.n_cta));

@@ -47,6 +47,7 @@ struct Params {
   int unit_pages;       // a unit's cost beside its pages
   uint64_t g_inverse;   // 2^32 / g, rounded up
   float scale;          // softmax_scale * log2(e)
+  long long wait_cycles;   // many rows: limit of the pipeline's waits
 };
 
 // The kernel for many rows: its columns (rows a partial result holds) and its launch,

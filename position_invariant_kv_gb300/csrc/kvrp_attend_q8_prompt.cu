@@ -168,6 +168,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
 // Two f16 values to e4m3 (NaN stays NaN; nothing here is above 448).
 __device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t v) {
   uint16_t r;
@@ -443,15 +453,16 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
   const uint32_t tmem = sh.tmem;
   volatile int* abort_p = &sh.abort_flag;
   auto wait = [&](uint32_t bar, uint32_t parity) {   // bounded; the same answer in the whole warp
-    bool ok = mbar_try_wait(bar, parity);
+    bool ok = mbar_test_wait(bar, parity);
     if (!__all_sync(0xffffffffu, ok)) {
       const long long t0 = clock64();
       while (!ok && !*abort_p) {
-        ok = mbar_try_wait(bar, parity);
-        if (!ok && clock64() - t0 > kTimeoutCycles) {
+        if (clock64() - t0 > p.wait_cycles) {
           *abort_p = 1;
           flag(p.status, KVRP_DEV_TIMEOUT);
+          break;
         }
+        ok = mbar_try_wait(bar, parity);
       }
     }
     return __all_sync(0xffffffffu, ok) != 0;

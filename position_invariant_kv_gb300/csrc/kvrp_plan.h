@@ -178,7 +178,7 @@ constexpr size_t kNoAllocScratchBytes = plan_bytes_bound(kNoAllocMaxChunks);
 size_t noalloc_scratch_bytes();
 cudaError_t noalloc_scratch(void** ptr);
 
-// Wait limit (cycles) written into every relocation plan; 0 keeps the default.
+// Wait limit (cycles) written into every relocation plan and kv_attend_q8 launch; 0 keeps the default.
 // Set only through kvrp_test_set_wait_limit, by tests of the failure path.
 uint32_t test_wait_limit();
 
