@@ -182,6 +182,17 @@ def along(c, s, steps):
 
 
 @each_shape
+@pytest.mark.parametrize("form", ["rise", "saw", "fall"])
+def test_scores_that_rise(shape, form):
+    """The running maximum moves many times: the sum and the accumulator are scaled down with it."""
+    c = Case(**SHAPES[shape])
+    for s, n in enumerate(c.lens):
+        t = np.arange(n) / n
+        along(c, s, {"rise": 60 * t, "saw": 40 * t + 20 * (np.arange(n) // 16 % 3), "fall": 60 * (1 - t)}[form])
+    check(c)
+
+
+@each_shape
 def test_any_value_scales(shape):
     check(Case(**SHAPES[shape], v_spread=30, pow2=False))
 
