@@ -546,13 +546,21 @@ kvrp_status run(const char* fn, bool q8, const void* q, const void* k, const voi
   const int64_t runs = !seqs->row_start ? seqs->n_seqs
                                         : std::min<int64_t>(seqs->n_rows, seqs->n_rows / kPage + 2 * (int64_t)seqs->n_seqs);
   // A run's heads are shared out among CTAs while the GPU has room for more (three CTAs an SM): a
-  // decode step is a few runs, and its time is one warp's chain of loads.  A prompt a little above
-  // one filling of the GPU (560 runs for 456 places) takes two CTAs a run as well, 35.6 us against
-  // 37.8 with one; below one filling and from two on the second table of angles costs more than the
-  // evener end gives (432 runs, 96 heads: 57.9 us with one, 59.7 with two).
+  // decode step is a few runs, and its time is one warp's chain of loads.  Above one filling a run takes
+  // two CTAs where the last filling would be at most half full, and so ends half a filling earlier, one
+  // elsewhere: the second table of angles costs more than an evener end gives.  Measured with one / two a
+  // run, us (28 + 2 x 4 heads with norms, 32 + 2 x 32 without; 456 places; * is the rule's):
+  //   runs / places        1.1         1.3         1.6         1.9         2.2         2.7         3.3         3.8
+  //   bf16, 28 + 8    36.5/31.9*  37.8/35.4*  40.9*/42.3  44.4*/47.4  56.7/54.5*  62.3*/65.3  77.2/77.9*  83.8*/88.5
+  //   bf16, 32 + 64   76.3/66.7*  77.2/74.1*  93.5*/91.6  110*/103    125/120*    147*/146    180/176*    207*/202
+  //   8 bits, 28 + 8  46.3/40.6*  48.6/43.5*  51.8*/53.5  55.0*/59.1  72.5/68.5*  79.0*/82.7  99.7/98.5*  106*/112
+  //   8 bits, 32 + 64 88.1/74.2*  94.7/81.0*  100*/102    113*/116    141/134*    164*/162    197/194*    220*/222
   const int64_t places = 3 * (int64_t)sms;
   const int rounds = (n_q_heads - p.h0 + 2 * n_kv_heads + kWarps - 1) / kWarps;
-  const int64_t wanted = runs > places && runs < 2 * places ? 2 : places / runs;
+  // of a ragged batch, whose sequences mostly begin and end inside a page
+  const int64_t likely = !seqs->row_start ? runs : std::min<int64_t>(runs, seqs->n_rows / kPage + seqs->n_seqs);
+  const bool half = (2 * likely + places - 1) / places < 2 * ((likely + places - 1) / places);
+  const int64_t wanted = likely <= places ? places / likely : half ? 2 : 1;
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(rounds, wanted));
   if (runs * p.splits > INT32_MAX) return fail(KVRP_ERR_UNSUPPORTED, "%s: too many rows", fn);
 
