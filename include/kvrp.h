@@ -477,7 +477,8 @@ typedef struct kvrp_seqs {
  *     q', k' = R(position) (w * x / sqrt(mean(x^2) + norm_eps)),  v' = v
  * in fp32, rounded once to bf16.  R is rotate-half RoPE or, with mrope_section,
  * M-RoPE; the angle position * theta^(-2i/head_dim) is formed mod 2 pi in
- * 64-bit fixed point (error below 2^-30 turns over the int32 range of positions).
+ * 64-bit fixed point, from a frequency of a double's precision: off by at most
+ * 2^-56 turns a position, 2^-25 turns at the ends of the int32 range (theta >= 1).
  *   q, k, v      device bf16, row r at base + r * stride elements, heads
  *                contiguous [n_heads][head_dim] inside a row (so a fused
  *                projection [q | k | v] passes three pointers and one stride).
@@ -563,17 +564,22 @@ kvrp_status kv_pack_q8(
  *                token sets are merged.
  *   workspace    device scratch of kv_attend_q8_workspace_size(...) bytes; its
  *                contents need not survive between calls; calls that can overlap
- *                need one each.  max_rows is kvrp_seqs.max_rows (1 without row_start).
+ *                need one each.  max_rows is kvrp_seqs.max_rows (1 without row_start,
+ *                n_rows where that is 0); few and many rows need different sizes,
+ *                neither always the larger.
  * An idle sequence (length 0) gets zeros and a log-sum-exp of -inf.  A sequence
  * with a bad length, or more rows than max_rows, is flagged and its rows are left as
  * they were.  A bad table entry sets KVRP_DEV_BAD_PAGE and reads as a page of
- * zeros.  Slots past a sequence's length are never used, whatever they hold.
+ * zeros.  Slots past a sequence's length are never used, whatever they hold; a
+ * value that is NaN reaches the rows that see its token and no others.
  * rows x group up to 16 take a kernel for few rows, more one that fills tensor-core
  * tiles with rows; n_rows x n_q_heads must stay below 2^32, n_rows x group below 2^28
  * (UNSUPPORTED).  KVRP_DEV_TIMEOUT is OR-ed in if an internal pipeline wait gave up
- * (the output is then undefined).  The output does not depend on how the work is split
- * over the GPU beyond fp32 rounding, and the same call gives the same bits.  Asynchronous on `stream`; may
- * be captured into a graph and replayed as lengths and tables change.
+ * (the output is then undefined).  The same call gives the same bits.  How the work is
+ * split over the GPU's SMs moves the output by rounding alone: of the softmax weights to
+ * f16 (2^-11 of each at most) and of sums in fp32.  With many rows, value scales more than
+ * 2^12 apart cost time (about 2.3 times that of others).  Asynchronous on `stream`; may be
+ * captured into a graph and replayed as lengths and tables change.
  */
 size_t kv_attend_q8_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_rows);
 

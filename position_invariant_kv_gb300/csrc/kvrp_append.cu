@@ -20,7 +20,7 @@
 //     flight.  The 8-bit form loads the next head's rows as it is done with this one's; in the
 //     bf16 form that measured slower (40.7 against 35.6 us) and it loads a head at a time.
 //   Measured: 8 sequences, 8719 rows of 28 + 2 x 4 heads x 128 with norms and M-RoPE, 160 MB, 35.6 us
-//   (4.5 TB/s, 67% of a copy); 6790 rows of 32 + 2 x 32 heads into 8 bits, 278 MB, 57.9 us (72%);
+//   (4.5 TB/s, 67% of a copy); 6790 rows of 32 + 2 x 32 heads into 8 bits, 278 MB, 58.1 us (71%);
 //   one row of each of 16 sequences 3.0 us, of 64 into 8 bits 4.5 us (launch and latency).
 //
 // pack_kernel.  One warp a block: 16 rows of one head of one layer in registers, amax (two bf16

@@ -33,15 +33,17 @@
 //     (for the accumulator, whose weights are exp2(x + log2 vs - max)).  The second keeps
 //     the f16 weights in range however far the pages' value scales lie apart.
 //   - Maxima move only when a score passes them by 2^8 (one vote a step instead of six
-//     shuffles); weights then stay below 2^15, inside f16.
+//     shuffles); weights then stay below 2^15, inside f16.  They are summed in fp32 before they are
+//     rounded to it, 2^-11 of each at most: the output, rounded to bf16, is 1.7e-3 from the 64-bit
+//     result with them as with fp32 weights, and a low part would double the second product.
 // combine_kernel: merges the partial results of units that more than one CTA shared.
 //
-// Measured: 16 sequences x 16384 tokens, 28 / 4 heads x 128 (269 MB): 55.7 us, 4.8 TB/s, 72% of a
+// Measured: 16 sequences x 16384 tokens, 28 / 4 heads x 128 (269 MB): 56.2 us, 4.8 TB/s, 71% of a
 // copy.  From the first data to the last page the reads run at the memory's rate (about 34 us); 6 us
 // go before them (the shares, the first table entries, the first pages), SMs end up to 5 us apart,
 // merging and combining take 6.  24 uneven multi-head sequences (566 MB): 99 us, 85%.  4 rows x 4
-// heads x 64 over 32 sequences (118 MB): 43.8 us, 40%: 8 warps an SM, each bound by the latency of its
-// own chain of products and powers.  One sequence of 1000 tokens: 11 us, two launches and about ten
+// heads x 64 over 32 sequences (118 MB): 44.5 us, 40%: 8 warps an SM, each bound by the latency of its
+// own chain of products and powers.  One sequence of 1000 tokens: 12 us, two launches and about ten
 // dependent trips to memory.
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -11,14 +11,17 @@
 //     the combine.
 //   - S = Q K^T by tcgen05 kind::f8f6f4: K goes from memory to the tensor cores as stored.
 //     q is split into two e4m3 parts, high and low, after its row was divided by a power of
-//     two: bf16's 8 significant bits are 4 + 4, so the parts are q exactly down to 2^-10 of
-//     the row's largest element and off by at most 2^-18 of it below.  Two products at
+//     two: bf16's 8 significant bits are 4 + 4, so the parts are q exactly down to 2^-9 of
+//     the row's largest element and off by at most 2^-17 of it below.  Two products at
 //     twice the f16 rate cost what one would, without converting K.
 //   - O += P V by kind::f16: P as f16 from TMEM, V as f16 in shared memory, converted from e4m3
 //     by four warps together with the page's scale relative to a running reference (a power
 //     of two), exact for powers of two within 2^12 of it.  From the first tile on whose scales lie
 //     farther apart, a unit's part has V unscaled and the scales in the weights' exponent, with a
-//     running maximum of x + log2 vs for the accumulator beside that of x for the sum.
+//     running maximum of x + log2 vs for the accumulator beside that of x for the sum.  The weights
+//     are rounded to f16, 2^-11 of each at most, and summed before that in fp32: the output, rounded to
+//     bf16, is 1.7e-3 from the 64-bit result with them as with fp32 weights, and a second, low part
+//     would double the second product.
 //   - Two 128-row Q tiles a CTA, each with its own softmax warps (a thread a row) and its own
 //     MMA issuer.  TMEM holds for each the accumulator, the scores and, apart from them, the
 //     weights: the next tile's scores are formed while this one's are being turned into
@@ -27,11 +30,14 @@
 //     the weights in the scores' place each tile waited for both products: 911 TFLOP/s on
 //     4096 rows over 16441 tokens.)
 //
-// Measured: 4096 rows over 16441 tokens, 28 / 4 heads x 128: 683 us, 1238 TFLOP/s, 64% of the measured
-// bf16 peak; 6 questions of 37 to 900 rows behind 500 to 12000 tokens: 215 us, 1038 TFLOP/s.  A tile
-// takes about 2300 cycles, its products alone 1500: the softmax warps wait some 800 of them for
-// products, which share the 128 bytes a cycle of shared memory with the conversion of V (two thirds
-// busy).  Beginning and ending a unit costs about 7 us.
+// Measured: 4096 rows over 16441 tokens, 28 / 4 heads x 128: 688 us, 1229 TFLOP/s, 63% of the measured
+// bf16 peak; 6 questions of 37 to 900 rows behind 500 to 12000 tokens: 215 us, 1038 TFLOP/s.  The same
+// with 32 / 8 heads x 64: 667 and 215 us, 724 and 591 TFLOP/s.  With value scales spread over 2^30: 1626
+// and 468 us (head_dim 128).  A tile takes about 2300 cycles, its products alone 1500: the softmax warps
+// wait some 800 of them for products, which share the 128 bytes a cycle of shared memory with the
+// conversion of V (two thirds busy).  What is in the way of the next scores costs at once: instructions
+// between a tile's scores and their release, and in the warp that loads (70 more a tile: 60 us of 690).
+// Beginning and ending a unit costs about 7 us.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -92,7 +98,9 @@ struct Prompt {
   static __host__ __device__ constexpr int tmem_p(int t) { return D == 128 ? t * 128 + 80 : 256 + t * 64; }
   static __host__ __device__ constexpr int tmem_o(int t) { return D == 128 ? 256 + t * 128 : 384 + t * 64; }
   // Registers a thread of the softmax (which holds a row of scores), V and other warps: the
-  // 4 x 128 that the warp groups were launched with, shared out anew.
+  // 4 x 128 that the warp groups were launched with, shared out anew.  head_dim 64, 128 scores a row:
+  // 184 / 88 / 56 spill 600 bytes a thread and take 757 us for 4096 rows over 16441 tokens, 192 / 80 / 48
+  // 704, 200 / 64 / 48 (384 bytes) 657, 200 / 56 / 56 662.
   static constexpr int kRegsRow = D == 128 ? 168 : 200, kRegsV = D == 128 ? 88 : 64, kRegsMisc = D == 128 ? 88 : 48;
   static_assert(2 * kRegsRow + kRegsV + kRegsMisc <= 4 * 128, "more registers than the block holds");
   static constexpr int kOffK = 4 * kQ, kOffV = kOffK + kKst * kKV, kOffVc = kOffV + kVst * kKV;
