@@ -38,11 +38,11 @@
 //     result with them as with fp32 weights, and a low part would double the second product.
 // combine_kernel: merges the partial results of units that more than one CTA shared.
 //
-// Measured: 16 sequences x 16384 tokens, 28 / 4 heads x 128 (269 MB): 56.2 us, 4.8 TB/s, 71% of a
+// Measured: 16 sequences x 16384 tokens, 28 / 4 heads x 128 (269 MB): 55.1 us, 4.9 TB/s, 73% of a
 // copy.  From the first data to the last page the reads run at the memory's rate (about 34 us); 6 us
 // go before them (the shares, the first table entries, the first pages), SMs end up to 5 us apart,
-// merging and combining take 6.  24 uneven multi-head sequences (566 MB): 99 us, 85%.  4 rows x 4
-// heads x 64 over 32 sequences (118 MB): 44.5 us, 40%: 8 warps an SM, each bound by the latency of its
+// merging and combining take 6.  24 uneven multi-head sequences (566 MB): 97 us, 87%.  4 rows x 4
+// heads x 64 over 32 sequences (118 MB): 44.6 us, 40%: 8 warps an SM, each bound by the latency of its
 // own chain of products and powers.  One sequence of 1000 tokens: 12 us, two launches and about ten
 // dependent trips to memory.
 #include <cuda.h>
@@ -538,7 +538,9 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
           }
           // A NaN of a token that not all rows see: weight 0 would not keep it from the others.  It is taken out
           // of the stage, byte by byte and on few registers, and the accumulators of the rows that do see it
-          // become NaN.  (Looking for it costs a sequence's last pages: 43.5 -> 44.5 us for 4 rows x 32 sequences.)
+          // become NaN.  (Looking for it costs a sequence's last pages: 43.5 -> 44.5 us for 4 rows x 32 sequences.
+          // One row a sequence has no such tokens: with one tile of columns leaving the vote out takes 11.5 us
+          // instead of 11.8 for a short sequence; with two the other code that it leads to takes 45.2 instead of 44.5.)
           const int t0 = (pg + w) * kPage;
           bool odd = false;
 #pragma unroll
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
             for (int j = 0; j < FPL / 4; ++j) nan |= q8::nan_bytes(v[i][j]);
             odd |= nan && t0 + token_of(i) > ctx;
           }
-          if (__any_sync(0xffffffffu, odd)) {
+          if ((NT == 2 || cq.rows > 1) && __any_sync(0xffffffffu, odd)) {
             const int end = pg + w < cc.end ? cq.len : 0;
 #pragma unroll
             for (int f = 0; f < FPL; ++f) {
