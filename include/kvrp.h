@@ -78,6 +78,9 @@ typedef enum kvrp_status {
 #define KVRP_DEV_BAD_PAGE 0x1u
 #define KVRP_DEV_TIMEOUT 0x2u
 #define KVRP_DEV_BAD_LENGTH 0x4u   /* kvrp_seqs: a sequence's rows or length out of range */
+#define KVRP_DEV_NO_PAGES 0x8u     /* kv_step_tables: too few free pages for a sequence */
+#define KVRP_DEV_BAD_TOKEN 0x10u   /* kv_verify_drafts: a drafted token outside the vocabulary,
+                                      or a row of probabilities without weight */
 
 /* One destination pool (one tensor). */
 typedef struct kvrp_dst {
@@ -591,6 +594,109 @@ kvrp_status kv_attend_q8(
     uint32_t* d_status, kvrp_stream_t stream);
 
 /*
+ * A context that all sequences of a batch begin with (reused chunks, a system
+ * prompt), held once in the pages of the pools: token t at page
+ * block_table[t / 16], slot t % 16.  Both arrays are on the device.
+ *   block_table   int32 [n_pages].
+ *   length        int32 [1]: its tokens, rounded down to whole pages (the rest of
+ *                 an open page belongs to each sequence alone); at most 16 n_pages.
+ */
+typedef struct kvrp_prefix {
+  const int32_t* block_table;
+  const int32_t* length;
+  int32_t n_pages;
+} kvrp_prefix;
+
+/*
+ * kv_step_tables -- the batch of a step, built on the device: writes the arrays
+ * that `seqs` points to (row_start, seq_lens, block_tables; row_start may not be
+ * NULL here) from each sequence's tokens and rows, so that a captured step goes
+ * on by itself while lengths, accepted drafts and sequences come and go.
+ *   kept_lens    int32 [n_seqs]: tokens of the cache that stay (kv_verify_drafts'
+ *                kept_lens; 0 for a place that falls free).  May be seqs->seq_lens.
+ *   new_rows     int32 [n_seqs]: rows to append behind them.
+ *   prefix       optional: the first pages of every sequence, owned by none.  Its
+ *                length may change only while no sequence holds pages.
+ *   held_pages   int32 [n_seqs]: pages that the sequence's table holds, the
+ *                prefix's included; 0 for one that begins (its table then starts
+ *                with the prefix's pages).  held_out: the same after the call.
+ *   free_pages   int32 [num_pages]: a ring of free pages, of which
+ *   free_state   int32 [2] = {head, count} says free_pages[(head + i) mod num_pages],
+ *                i < count, are free.  free_state_out: the same after the call.
+ *   positions    optional int32 [n_rows]: the position of each row.
+ *   slots        optional int64 [n_rows]: page * 16 + slot of each row.
+ * held_out and free_state_out may be their inputs; the other arrays are distinct.
+ * A sequence needs ceil((kept + new) / 16) pages.  In the order of the batch,
+ * sequences take what they lack from the ring's head on; what one has too much
+ * goes back behind the free ones and can be taken from the next call on.  Table
+ * entries past those needed keep what they held.
+ *   row_start    the running sum of new_rows (at most n_rows).
+ *   seq_lens     kept + new; 0 (an idle place, whose rows the other calls leave out)
+ *                for a sequence that cannot be served.  It keeps its pages and table;
+ *                its rows get position 0 and slot -1, as do the rows behind the last
+ *                sequence.
+ * *d_status: KVRP_DEV_NO_PAGES, if a sequence and those before it ask for more
+ * pages than are free (all those behind it that ask for any are left out too);
+ * KVRP_DEV_BAD_LENGTH, for a sequence with a negative count, kept tokens that it
+ * has no pages for, fewer kept tokens than the prefix, rows past n_rows, or more
+ * tokens than its table has entries for, for all sequences where free_state or the
+ * prefix's length is out of range, and where more pages come back than the ring
+ * holds (they are lost); KVRP_DEV_BAD_PAGE, where a page written or given back is
+ * outside [0, num_pages) (it goes where it belongs all the same; a row on it gets
+ * slot -1).  n_seqs x table_stride must stay below 2^31 (UNSUPPORTED).
+ * Asynchronous on `stream`; may be captured into a graph.
+ */
+kvrp_status kv_step_tables(
+    const int32_t* kept_lens, const int32_t* new_rows, const kvrp_seqs* seqs, const kvrp_prefix* prefix,
+    const int32_t* held_pages, int32_t* held_out,
+    int32_t* free_pages, const int32_t* free_state, int32_t* free_state_out,
+    int32_t* positions, int64_t* slots, uint32_t* d_status, kvrp_stream_t stream);
+
+/*
+ * kv_verify_drafts -- which drafted tokens of a step stay, and the token after
+ * the last one that does.  Sequence s owns the rows of kvrp_seqs: its first row is
+ * its last token, each row after that a draft; row r of `target` (and `draft`) holds
+ * the probabilities of the token that follows row r's.  The drafts are taken in turn:
+ *   draft tokens[r + 1] stays while   u_accept[r] * draft[r][token] < target[r][token]
+ * and at the first row a whose draft does not, or that has none, a token is drawn:
+ *   weight of i = the positive part of w(target[a][i]) - w(draft[a][i]) where a draft
+ *                 was turned down, and w(target[a][i]) where there was none or no
+ *                 positive part is left;   w(x) = floor(2^40 x), x in [0, 1]
+ *   token       = the first i at which the weights' running sum passes
+ *                 floor(floor(2^32 u_sample[s]) * (their sum) / 2^32)
+ * so that with independent uniform numbers the tokens are distributed as the target's
+ * own.  Weights and sums are whole numbers: the token does not depend on how the sum
+ * is split up.  The comparison is exact too (64-bit products of the 32-bit values).
+ *   target, draft   device, row r at base + r * stride elements (0: vocab), of
+ *                 prob_type KVRP_F32 or KVRP_BF16.  Values below 0 and NaN weigh
+ *                 nothing, values above 1 as 1.  A sequence's last row of `draft` is not
+ *                 read.  draft NULL: the drafts are certain (looked up, not drawn), that
+ *                 is draft[r][i] = 1 at the drafted token and 0 elsewhere.
+ *   tokens        device int32 [n_rows]; u_accept, u_sample   device fp32 [n_rows],
+ *                 [n_seqs], in [0, 1).
+ *   out_tokens    device int32 [n_rows]: from each sequence's first row on the drafts that
+ *                 stay, the drawn token, then -1.
+ *   accepted      optional device int32 [n_seqs]: how many drafts stay.
+ *   kept_lens     optional device int32 [n_seqs]: seq_lens without the rows turned down
+ *                 (the cache then holds all tokens but the drawn one).  May be
+ *                 seqs->seq_lens.
+ * An idle sequence (length 0) gets -1 in its rows, and 0; one without rows 0, and its
+ * length.  A sequence with a bad length is flagged (KVRP_DEV_BAD_LENGTH) and its
+ * outputs stay as they were.  KVRP_DEV_BAD_TOKEN: a drafted token outside [0, vocab)
+ * (it is turned down), or a row without weight (the token is -1).  block_tables and
+ * num_pages of `seqs` are not used beyond its checks.  vocab up to 2^22.  Pointers 4-byte
+ * aligned (bf16 probabilities 2); rows that begin on 16 bytes are read fastest.
+ * Asynchronous on `stream`; may be captured into a graph.
+ */
+#define KVRP_F32 0
+#define KVRP_BF16 1
+
+kvrp_status kv_verify_drafts(
+    const void* target, int64_t target_stride, const void* draft, int64_t draft_stride, int32_t prob_type,
+    int32_t vocab, const kvrp_seqs* seqs, const int32_t* tokens, const float* u_accept, const float* u_sample,
+    int32_t* out_tokens, int32_t* accepted, int32_t* kept_lens, uint32_t* d_status, kvrp_stream_t stream);
+
+/*
  * kvrp_test_set_wait_limit -- for tests of the failure path only.  Sets the
  * limit, in SM clock cycles, of the relocation kernel's pipeline waits in the
  * plans built from now on by any thread, and of kv_attend_q8's kernel for many
@@ -623,10 +729,11 @@ const char* kvrp_status_string(kvrp_status status);
 const char* kvrp_last_error(void);
 
 /* Kernel launches that this host thread's last relocation call (kv_relocate_*),
- * attention call (kv_attend_*), append or pack enqueued.  Relocation: the relocation
+ * attention call (kv_attend_*), append, pack, step tables or verification enqueued.  Relocation: the relocation
  * kernel, plus for a batch the small copy launches that carry its launch plan to
  * the device (31 KB of plan each).  Attention: the block and combine kernels (2;
- * the combine alone when no chunk has tokens).  Append and pack: 1.  0 when the
+ * the combine alone when no chunk has tokens).  Append, pack and draft verification: 1.
+ * Step tables: 1, or 2 for many rows.  0 when the
  * call returned an error or had nothing to move. */
 int32_t kvrp_last_launch_count(void);
 

@@ -18,6 +18,8 @@ CUDA kernel.  Names mirror the C ABI in include/kvrp.h:
     kv_append_q8             the same into the 8-bit cache (e4m3, a scale for each page and head)
     kv_pack_q8               bf16 pages (a relocated chunk) into the 8-bit cache
     kv_attend_q8             causal attention of the new rows over the 8-bit cache
+    kv_step_tables           the batch of a step on the device: tables, lengths, positions, slots
+    kv_verify_drafts         drafted tokens against the target's probabilities, and the next token
 
 Tensors may be passed as torch CUDA tensors (their data_ptr is used) or as raw
 device addresses (int).  Streams default to torch's current stream.  A status
@@ -27,7 +29,8 @@ package fails when libkvrp.so has not been built.
 from __future__ import annotations
 
 from ._abi import (  # noqa: F401
-    KVRP_DEV_BAD_LENGTH, KVRP_DEV_BAD_PAGE, KVRP_DEV_TIMEOUT, KVRP_OK, KVRP_ERR_INVALID_ARG, KVRP_ERR_ALIGNMENT,
+    KVRP_DEV_BAD_LENGTH, KVRP_DEV_BAD_PAGE, KVRP_DEV_BAD_TOKEN, KVRP_DEV_NO_PAGES, KVRP_DEV_TIMEOUT, KVRP_OK,
+    KVRP_ERR_INVALID_ARG, KVRP_ERR_ALIGNMENT,
     KVRP_ERR_UNSUPPORTED, KVRP_ERR_CUDA, KVRP_ERR_WORKSPACE,
     Dst, Chunk, KvrpError, lib, lib_path,
     kv_relocate_patch, kv_relocate_patch_mrope, kv_relocate_patch_mla, kv_relocate_batch, kv_relocate_batch_workspace_size,
@@ -38,5 +41,6 @@ from ._abi import (  # noqa: F401
     kv_patch_form, kv_patch_form_orbit, kv_patch_form_workspace_size,
     kv_attend_relocated, kv_attend_relocated_workspace_size, AttnChunk, attn_chunk_array, KVRP_ATTN_MAX_CHUNKS,
     KVRP_ROPE_NONE, KVRP_ROPE_HEADS, KVRP_ROPE_MLA_TAIL,
+    KVRP_BF16, KVRP_F32, Prefix, kv_step_tables, kv_verify_drafts,
     Seqs, kv_append, kv_append_q8, kv_pack_q8, kv_attend_q8, kv_attend_q8_workspace_size,
 )

@@ -18,6 +18,10 @@ KVRP_ERR_WORKSPACE = 5
 KVRP_DEV_BAD_PAGE = 0x1
 KVRP_DEV_TIMEOUT = 0x2
 KVRP_DEV_BAD_LENGTH = 0x4
+KVRP_DEV_NO_PAGES = 0x8
+KVRP_DEV_BAD_TOKEN = 0x10
+KVRP_F32 = 0
+KVRP_BF16 = 1
 
 EXPORTED_SYMBOLS = (
     "kv_relocate_patch", "kv_relocate_patch_mrope", "kv_relocate_patch_mla", "kv_relocate_batch",
@@ -25,6 +29,7 @@ EXPORTED_SYMBOLS = (
     "kv_relocate_batch_mla", "kvrp_test_set_wait_limit", "kvrp_test_attend_split", "kv_patch_form_workspace_size",
     "kv_patch_form", "kv_patch_form_orbit", "kv_attend_relocated_workspace_size", "kv_attend_relocated",
     "kv_append", "kv_append_q8", "kv_pack_q8", "kv_attend_q8_workspace_size", "kv_attend_q8",
+    "kv_step_tables", "kv_verify_drafts",
     "kvrp_status_string",
     "kvrp_last_error", "kvrp_last_launch_count", "kvrp_version",
 )
@@ -66,6 +71,10 @@ class kvrp_seqs(C.Structure):
     _fields_ = [("row_start", C.c_void_p), ("seq_lens", C.c_void_p), ("block_tables", C.c_void_p),
                 ("n_seqs", C.c_int32), ("n_rows", C.c_int32), ("table_stride", C.c_int32),
                 ("num_pages", C.c_int32), ("max_rows", C.c_int32)]
+
+
+class kvrp_prefix(C.Structure):
+    _fields_ = [("block_table", C.c_void_p), ("length", C.c_void_p), ("n_pages", C.c_int32)]
 
 
 def _load_library():
@@ -136,6 +145,14 @@ def _load_library():
         C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.POINTER(kvrp_seqs), C.c_int32, C.c_int32,
         C.c_int32, C.c_void_p, C.c_void_p, C.c_float, C.c_double, C.c_void_p, C.POINTER(C.c_int32), C.c_void_p,
         C.c_void_p, C.c_void_p]
+    L.kv_step_tables.restype = st
+    L.kv_step_tables.argtypes = [
+        C.c_void_p, C.c_void_p, C.POINTER(kvrp_seqs), C.POINTER(kvrp_prefix), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+        C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]
+    L.kv_verify_drafts.restype = st
+    L.kv_verify_drafts.argtypes = [
+        C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int32, C.c_int32, C.POINTER(kvrp_seqs), C.c_void_p, C.c_void_p,
+        C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]
     L.kv_append.restype = st
     L.kv_append.argtypes = append_args + [C.c_void_p, C.c_void_p]
     L.kv_append_q8.restype = st
@@ -541,6 +558,20 @@ class Seqs:
         self.ref = C.byref(self.c)
 
 
+class Prefix:
+    """Shared tokens that all sequences of a batch begin with (fields as in struct kvrp_prefix):
+    device int32 tensors block_table [n_pages] and length [1], whose contents may change between
+    calls."""
+
+    def __init__(self, block_table, length):
+        for name, t in (("block_table", block_table), ("length", length)):
+            if t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous() or (t is length and t.numel() != 1):
+                raise ValueError(f"{name}: a contiguous int32 tensor{' of one entry' if t is length else ''} is needed")
+        self.arrays = (block_table, length)   # keeps the device memory alive
+        self.c = kvrp_prefix(_ptr(block_table) if block_table.numel() else None, _ptr(length), int(block_table.numel()))
+        self.ref = C.byref(self.c)
+
+
 _SECTIONS = {}
 
 
@@ -601,3 +632,23 @@ def kv_attend_q8(q, seqs: Seqs, *, n_q_heads: int, n_kv_heads: int, head_dim: in
         _ptr(q), q_stride, seqs.ref, n_q_heads, n_kv_heads, head_dim, softmax_scale, _ptr(k_pool), _ptr(v_pool),
         _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes, _ptr(d_status),
         _stream(stream)))
+
+
+def kv_step_tables(kept_lens, new_rows, seqs: Seqs, *, held_pages, free_pages, free_state, held_out=None, free_state_out=None,
+                   prefix: Optional[Prefix] = None, positions=None, slots=None, d_status=None, stream=None) -> None:
+    """Row starts, lengths, block tables (written into the arrays of seqs), positions and slots of a step, from each
+    sequence's kept tokens and new rows.  held_out and free_state_out default to held_pages and free_state."""
+    _check(lib().kv_step_tables(
+        _ptr(kept_lens), _ptr(new_rows), seqs.ref, prefix.ref if prefix is not None else None, _ptr(held_pages),
+        _ptr(held_pages if held_out is None else held_out), _ptr(free_pages), _ptr(free_state),
+        _ptr(free_state if free_state_out is None else free_state_out), _ptr(positions), _ptr(slots), _ptr(d_status),
+        _stream(stream)))
+
+
+def kv_verify_drafts(target, seqs: Seqs, *, vocab: int, tokens, u_accept, u_sample, out_tokens, draft=None,
+                     prob_type: int = KVRP_F32, accepted=None, kept_lens=None, target_stride: int = 0, draft_stride: int = 0,
+                     d_status=None, stream=None) -> None:
+    """Which drafted tokens stay against the target's probabilities, and the token after the last one that does."""
+    _check(lib().kv_verify_drafts(
+        _ptr(target), target_stride, _ptr(draft), draft_stride, prob_type, vocab, seqs.ref, _ptr(tokens), _ptr(u_accept),
+        _ptr(u_sample), _ptr(out_tokens), _ptr(accepted), _ptr(kept_lens), _ptr(d_status), _stream(stream)))

@@ -19,6 +19,7 @@ SOURCES = [os.path.join(HERE, "csrc", "kvrp_kernel.cu"), os.path.join(HERE, "csr
            os.path.join(HERE, "csrc", "kvrp_attend.cu"), os.path.join(HERE, "csrc", "kvrp_append.cu"),
            os.path.join(HERE, "csrc", "kvrp_attend_q8.cu"),
            os.path.join(HERE, "csrc", "kvrp_attend_q8_prompt.cu"),
+           os.path.join(HERE, "csrc", "kvrp_tables.cu"), os.path.join(HERE, "csrc", "kvrp_verify.cu"),
            os.path.join(HERE, "csrc", "kvrp_host.cpp")]
 HEADERS = [os.path.join(ROOT, "include", "kvrp.h"), os.path.join(HERE, "csrc", "kvrp_plan.h"),
            os.path.join(HERE, "csrc", "kvrp_ptx.h"), os.path.join(HERE, "csrc", "kvrp_q8.h"),

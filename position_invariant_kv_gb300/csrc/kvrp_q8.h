@@ -83,6 +83,7 @@ kvrp_status encode_q8_pool(CUtensorMap* map, const void* pool, int num_pages, in
 
 // Host checks that the entry points over a ragged batch (kvrp_seqs) share.
 kvrp_status check_seqs(const char* fn, const kvrp_seqs* s);
+kvrp_status check_prefix(const char* fn, const kvrp_prefix* x);
 kvrp_status check_heads(const char* fn, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim);
 
 }  // namespace kvrp
