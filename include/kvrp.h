@@ -608,6 +608,31 @@ typedef struct kvrp_prefix {
 } kvrp_prefix;
 
 /*
+ * kv_attend_shared_q8 -- kv_attend_q8 for a batch whose sequences all begin with
+ * the prefix's tokens: those are read once for the whole batch instead of once a
+ * sequence.  The same result up to rounding, the same arguments, and
+ *   prefix       the shared tokens, in pages of the same pools.  Table entries of
+ *                the sequences for these pages are not read.
+ *   workspace    kv_attend_shared_q8_workspace_size(...) bytes, max_rows and n_rows
+ *                those of the call (see kv_attend_q8 on max_rows).
+ * The first row of a sequence has to lie behind the prefix: one that does not, or a
+ * prefix longer than its table, or row_start out of order, is KVRP_DEV_BAD_LENGTH, and
+ * the rows concerned stay as they were.  A prefix of no tokens, and batches of one
+ * sequence, are fine.  Several prefixes: one call each, over the sequences of seqs'
+ * arrays that share it (row_start may begin above 0).  Everything else, NaN, bad pages,
+ * idle sequences and lse among it, is as in kv_attend_q8.
+ */
+size_t kv_attend_shared_q8_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_rows,
+                                          int32_t n_rows);
+
+kvrp_status kv_attend_shared_q8(
+    const void* q, int64_t q_stride, const kvrp_seqs* seqs, const kvrp_prefix* prefix,
+    int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, float softmax_scale,
+    const void* k_pool, const void* v_pool, const float* k_scale, const float* v_scale,
+    void* out, float* lse, void* workspace, size_t workspace_bytes,
+    uint32_t* d_status, kvrp_stream_t stream);
+
+/*
  * kv_step_tables -- the batch of a step, built on the device: writes the arrays
  * that `seqs` points to (row_start, seq_lens, block_tables; row_start may not be
  * NULL here) from each sequence's tokens and rows, so that a captured step goes

@@ -18,6 +18,7 @@ CUDA kernel.  Names mirror the C ABI in include/kvrp.h:
     kv_append_q8             the same into the 8-bit cache (e4m3, a scale for each page and head)
     kv_pack_q8               bf16 pages (a relocated chunk) into the 8-bit cache
     kv_attend_q8             causal attention of the new rows over the 8-bit cache
+    kv_attend_shared_q8      the same for a batch that begins with the same tokens, read once
     kv_step_tables           the batch of a step on the device: tables, lengths, positions, slots
     kv_verify_drafts         drafted tokens against the target's probabilities, and the next token
 
@@ -41,6 +42,7 @@ from ._abi import (  # noqa: F401
     kv_patch_form, kv_patch_form_orbit, kv_patch_form_workspace_size,
     kv_attend_relocated, kv_attend_relocated_workspace_size, AttnChunk, attn_chunk_array, KVRP_ATTN_MAX_CHUNKS,
     KVRP_ROPE_NONE, KVRP_ROPE_HEADS, KVRP_ROPE_MLA_TAIL,
-    KVRP_BF16, KVRP_F32, Prefix, kv_step_tables, kv_verify_drafts,
+    KVRP_BF16, KVRP_F32, Prefix, kv_attend_shared_q8, kv_attend_shared_q8_workspace_size,
+    kv_step_tables, kv_verify_drafts,
     Seqs, kv_append, kv_append_q8, kv_pack_q8, kv_attend_q8, kv_attend_q8_workspace_size,
 )

@@ -29,7 +29,7 @@ EXPORTED_SYMBOLS = (
     "kv_relocate_batch_mla", "kvrp_test_set_wait_limit", "kvrp_test_attend_split", "kv_patch_form_workspace_size",
     "kv_patch_form", "kv_patch_form_orbit", "kv_attend_relocated_workspace_size", "kv_attend_relocated",
     "kv_append", "kv_append_q8", "kv_pack_q8", "kv_attend_q8_workspace_size", "kv_attend_q8",
-    "kv_step_tables", "kv_verify_drafts",
+    "kv_attend_shared_q8_workspace_size", "kv_attend_shared_q8", "kv_step_tables", "kv_verify_drafts",
     "kvrp_status_string",
     "kvrp_last_error", "kvrp_last_launch_count", "kvrp_version",
 )
@@ -145,6 +145,12 @@ def _load_library():
         C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.POINTER(kvrp_seqs), C.c_int32, C.c_int32,
         C.c_int32, C.c_void_p, C.c_void_p, C.c_float, C.c_double, C.c_void_p, C.POINTER(C.c_int32), C.c_void_p,
         C.c_void_p, C.c_void_p]
+    L.kv_attend_shared_q8_workspace_size.restype = C.c_size_t
+    L.kv_attend_shared_q8_workspace_size.argtypes = [C.c_int32] * 5
+    L.kv_attend_shared_q8.restype = st
+    L.kv_attend_shared_q8.argtypes = [
+        C.c_void_p, C.c_int64, C.POINTER(kvrp_seqs), C.POINTER(kvrp_prefix), C.c_int32, C.c_int32, C.c_int32, C.c_float,
+        C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]
     L.kv_step_tables.restype = st
     L.kv_step_tables.argtypes = [
         C.c_void_p, C.c_void_p, C.POINTER(kvrp_seqs), C.POINTER(kvrp_prefix), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
@@ -632,6 +638,24 @@ def kv_attend_q8(q, seqs: Seqs, *, n_q_heads: int, n_kv_heads: int, head_dim: in
         _ptr(q), q_stride, seqs.ref, n_q_heads, n_kv_heads, head_dim, softmax_scale, _ptr(k_pool), _ptr(v_pool),
         _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes, _ptr(d_status),
         _stream(stream)))
+
+
+def kv_attend_shared_q8_workspace_size(n_q_heads: int, n_kv_heads: int, head_dim: int, max_rows: int, n_rows: int) -> int:
+    """Scratch bytes of kv_attend_shared_q8 (depends on the current device's SM count)."""
+    return int(lib().kv_attend_shared_q8_workspace_size(int(n_q_heads), int(n_kv_heads), int(head_dim), int(max_rows),
+                                                        int(n_rows)))
+
+
+def kv_attend_shared_q8(q, seqs: Seqs, prefix: Prefix, *, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                        softmax_scale: float, k_pool, v_pool, k_scale, v_scale, out, workspace, lse=None, q_stride: int = 0,
+                        workspace_bytes: Optional[int] = None, d_status=None, stream=None) -> None:
+    """kv_attend_q8 of a batch whose sequences begin with the same tokens, which are read once for all."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib().kv_attend_shared_q8(
+        _ptr(q), q_stride, seqs.ref, prefix.ref if prefix is not None else None, n_q_heads, n_kv_heads, head_dim,
+        softmax_scale, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace_bytes, _ptr(d_status), _stream(stream)))
 
 
 def kv_step_tables(kept_lens, new_rows, seqs: Seqs, *, held_pages, free_pages, free_state, held_out=None, free_state_out=None,

@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libkvrp.so")
 SOURCES = [os.path.join(HERE, "csrc", "kvrp_kernel.cu"), os.path.join(HERE, "csrc", "kvrp_patch_form.cu"),
            os.path.join(HERE, "csrc", "kvrp_attend.cu"), os.path.join(HERE, "csrc", "kvrp_append.cu"),
            os.path.join(HERE, "csrc", "kvrp_attend_q8.cu"),
-           os.path.join(HERE, "csrc", "kvrp_attend_q8_prompt.cu"),
+           os.path.join(HERE, "csrc", "kvrp_attend_q8_prompt.cu"), os.path.join(HERE, "csrc", "kvrp_attend_shared.cu"),
            os.path.join(HERE, "csrc", "kvrp_tables.cu"), os.path.join(HERE, "csrc", "kvrp_verify.cu"),
            os.path.join(HERE, "csrc", "kvrp_host.cpp")]
 HEADERS = [os.path.join(ROOT, "include", "kvrp.h"), os.path.join(HERE, "csrc", "kvrp_plan.h"),

@@ -74,9 +74,10 @@ struct Seq {
 __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
   return (uint64_t)(a | b) < (1ull << 31) ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
+template <Part kPart>
 __device__ __forceinline__ Seq seq_at(const Params& p, int s, bool* idle = nullptr, bool tell = false) {
   Seq r;
-  const bool ok = sequence(p.seqs, s, r.row0, r.rows, r.len) && r.rows <= p.max_rows;
+  const bool ok = part_sequence<kPart>(p, s, r.row0, r.rows, r.len) && r.rows <= p.max_rows;
   r.pages = ok && r.rows > 0 ? (r.len + kPage - 1) / kPage : 0;
   if (tell && !ok) flag(p.status, KVRP_DEV_BAD_LENGTH);
   if (idle && r.len == 0) *idle = true;
@@ -115,12 +116,13 @@ struct PlanSmem {
 // This CTA's share of the list of (sequence, head group, page).  A share is at least kLeast
 // pages a stream, so that a small batch is not cut into parts that cost more to join than to read.
 constexpr int kLeast = 2;
+template <Part kPart>
 __device__ __forceinline__ bool find_share(const Params& p, Plan* out, PlanSmem& sh) {
   const int n = p.seqs.n_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool idle = false;
   auto cost = [&](const Seq& q) { return q.pages > 0 ? q.pages + p.unit_pages : 0; };   // of one head group
   int64_t later = 0;   // the sequences past the first kThreads
-  for (int s = kThreads + tid; s < n; s += kThreads) later += cost(seq_at(p, s, &idle, blockIdx.x == 0));
+  for (int s = kThreads + tid; s < n; s += kThreads) later += cost(seq_at<kPart>(p, s, &idle, blockIdx.x == 0));
   if (n > kThreads) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) later += __shfl_xor_sync(0xffffffffu, later, o);
@@ -134,7 +136,7 @@ __device__ __forceinline__ bool find_share(const Params& p, Plan* out, PlanSmem&
   for (int s0 = 0; s0 < n; s0 += kThreads) {   // prefix sums, kThreads sequences at a time
     const int s = s0 + tid;
     Seq q = {0, 0, 0, 0};
-    if (s < n) q = s0 == 0 ? seq_at(p, s, &idle, blockIdx.x == 0) : seq_at(p, s);
+    if (s < n) q = s0 == 0 ? seq_at<kPart>(p, s, &idle, blockIdx.x == 0) : seq_at<kPart>(p, s);
     const int mine = cost(q);
     int64_t sum = mine;
 #pragma unroll
@@ -177,12 +179,13 @@ __device__ __forceinline__ bool find_share(const Params& p, Plan* out, PlanSmem&
   return out->at.end > out->at.page;   // else the share ends before its unit's first page
 }
 // The next segment of the share; false at its end.
+template <Part kPart>
 __device__ __forceinline__ bool next_segment(const Params& p, Cursor& c, Seq& q) {
   c.left -= c.spent;
   if (c.left <= 0) return false;
   if (++c.grp == p.n_grp) {
     c.grp = 0;
-    do q = seq_at(p, ++c.s);
+    do q = seq_at<kPart>(p, ++c.s);
     while (q.pages == 0);
   }
   take(p, c, q.pages, 0);
@@ -226,7 +229,7 @@ struct Decode {
   static constexpr int kSmem = kRing + kMergeSlots * kMerge * 4;
 };
 
-template <int D, int NT>   // head_dim; tiles of 8 (row, head) columns
+template <int D, int NT, Part kPart>   // head_dim; tiles of 8 (row, head) columns; kAll or kRest
 __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kernel(const __grid_constant__ Params p) {
   using C = Decode<D, NT>;
   constexpr int KT = D / 16;                 // 16-deep steps over the features; 16-feature tiles of O^T
@@ -242,9 +245,13 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
   pdl_wait();
   pdl_launch_dependents();
   Plan plan;
-  if (!find_share(p, &plan, plan_smem)) {
-    if (tid == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (plan.idle) write_idle(p, D);
+  __shared__ int table0;   // the first page of a sequence that its rows attend over
+  if (kPart == kRest && tid == 0) table0 = max(load_view(p).tokens, 0) / kPage;
+  if (!find_share<kPart>(p, &plan, plan_smem)) {
+    if constexpr (kPart == kAll) {
+      if (tid == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (plan.idle) write_idle(p, D);
+    }
     return;
   }
   // this warp's head of the group, and its stream: pages stream, stream + streams, ... of a segment
@@ -264,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
   int i_st = 0;
   bool more = true;
   auto settle = [&]() {   // to the next segment that has a step for this stream
-    while (i_left == 0 && (more = next_segment(p, ic, iq))) {
+    while (i_left == 0 && (more = next_segment<kPart>(p, ic, iq))) {
       i_first = i_q = 0;
       i_left = steps_of(0, ic.end);
       b_at = 32;
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
         const int q = i_q + lane, pg = i_first + (stream + q / PG * p.streams) * PG + q % PG;
         b_page = -1;      // none
         if (pg < ic.end) {
-          b_page = p.seqs.block_tables[(int64_t)ic.s * p.seqs.table_stride + pg];
+          b_page = p.seqs.block_tables[(int64_t)ic.s * p.seqs.table_stride + (kPart == kRest ? table0 : 0) + pg];
           if (b_page < 0 || b_page >= p.seqs.num_pages) {
             b_page = p.seqs.num_pages;   // read as zeros
             flag(p.status, KVRP_DEV_BAD_PAGE);
@@ -662,6 +669,9 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
       const int j = (int)div64(last * plan.n_cta - 1, plan.total);
       meta = make_int4(cq.rows, cc.grp, j - (int)blockIdx.x + 1, cq.row0);
     }
+    if constexpr (kPart == kRest) {
+      if (begins && tid == 0) p.found[(int64_t)cq.row0 * p.n_grp + cc.grp] = make_int2(blockIdx.x, ends ? 0 : meta.z);
+    }
     if (stream == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -669,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
         for (int b = 0; b < 2; ++b) {
           const int c = nt * 8 + 2 * tig + b;
           if (c >= cols) continue;
-          if (begins && ends) {
+          if (kPart == kAll && begins && ends) {
             const float2 r = result_factors(m[nt][b], om[nt][b], l[nt][b]);
             const int64_t row = (int64_t)(cq.row0 + c / p.g) * p.Hq + head * p.g + c % p.g;
             uint32_t w[FPL / 2];
@@ -684,6 +694,8 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
             if (p.lse && gid == 0) p.lse[row] = (m[nt][b] + lg2(l[nt][b])) * kLn2;
           } else {
             float* to = p.partial + ((int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * p.cols + hd * p.max_rows * p.g + c) * (D + 4);
+            if (kPart == kRest && begins && ends)
+              to = p.dense + ((int64_t)(cq.row0 + c / p.g) * p.Hq + head * p.g + c % p.g) * (D + 4);
             float4* of = reinterpret_cast<float4*>(to + gid * FPL);
 #pragma unroll
             for (int i = 0; i < FPL / 4; ++i)
@@ -692,10 +704,12 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
           }
         }
     }
-    if (!next_segment(p, cc, cq)) break;
+    if (!next_segment<kPart>(p, cc, cq)) break;
   }
-  if (tid == 0) p.meta[blockIdx.x] = meta;
-  if (plan.idle) write_idle(p, D);
+  if constexpr (kPart == kAll) {
+    if (tid == 0) p.meta[blockIdx.x] = meta;
+    if (plan.idle) write_idle(p, D);
+  }
 }
 
 // ---- combine ---------------------------------------------------------------------------
@@ -841,10 +855,89 @@ size_t workspace_bytes(int n_cta, int cols, int head_dim) {
   return 256 + meta_bytes(n_cta) + (size_t)n_cta * 2 * cols * (head_dim + 4) * sizeof(float);
 }
 
+void set_few(Params& p, int sms, int head_dim) {
+  p.hg = head_group(p.Hkv);
+  p.n_grp = p.Hkv / p.hg;
+  p.streams = kWarps / p.hg;
+  p.cols = p.hg * p.max_rows * p.g;
+  p.unit_pages = std::max(1, 2048 / (p.hg * head_dim));   // about 2 us of a CTA's share of the bandwidth
+  p.rounds = p.hg == 1 ? 4 : p.hg == 2 ? 3 : p.hg == 4 ? 2 : 0;
+  p.n_cta = std::min(kMaxCtas, (p.max_rows * p.g > 8 ? Decode<128, 2>::kCtas : kMaxCtasPerSm) * sms);
+}
+
+cudaError_t launch_few(const Params& p, int head_dim, cudaStream_t stream, Part part) {
+  const bool two = p.max_rows * p.g > 8;
+  auto kernel = head_dim == 64 ? (two ? decode_kernel<64, 2, kAll> : decode_kernel<64, 1, kAll>)
+                               : (two ? decode_kernel<128, 2, kAll> : decode_kernel<128, 1, kAll>);
+  if (part == kRest)
+    kernel = head_dim == 64 ? (two ? decode_kernel<64, 2, kRest> : decode_kernel<64, 1, kRest>)
+                            : (two ? decode_kernel<128, 2, kRest> : decode_kernel<128, 1, kRest>);
+  const int smem = head_dim == 64 ? (two ? Decode<64, 2>::kSmem : Decode<64, 1>::kSmem)
+                                  : (two ? Decode<128, 2>::kSmem : Decode<128, 1>::kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(p.n_cta);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 }  // namespace attend_q8
 }  // namespace kvrp
 
 using namespace kvrp;
+
+kvrp_status attend_q8::check_call(const char* fn, const void* q, int64_t& q_stride, const kvrp_seqs* seqs, int32_t n_q_heads,
+                                  int32_t n_kv_heads, int32_t head_dim, float softmax_scale, const void* k_pool,
+                                  const void* v_pool, const float* k_scale, const float* v_scale, void* out, float* lse,
+                                  uint32_t* d_status, Params& p) {
+  kvrp_status st = check_seqs(fn, seqs);
+  if (st != KVRP_OK) return st;
+  st = check_heads(fn, n_q_heads, n_kv_heads, head_dim);
+  if (st != KVRP_OK) return st;
+  if (!q || !k_pool || !v_pool || !k_scale || !v_scale || !out) return fail(KVRP_ERR_INVALID_ARG, "%s: NULL argument", fn);
+  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
+    return fail(KVRP_ERR_INVALID_ARG, "%s: softmax_scale must be > 0", fn);
+  const int64_t q_row = (int64_t)n_q_heads * head_dim;
+  q_stride = q_stride ? q_stride : q_row;
+  if (q_stride < q_row) return fail(KVRP_ERR_INVALID_ARG, "%s: a row stride is shorter than the row", fn);
+  if (q_stride % 8 || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
+    return fail(KVRP_ERR_ALIGNMENT, "%s: pointers must be 16-byte aligned, strides multiples of 8", fn);
+  for (const void* x : {(const void*)k_scale, (const void*)v_scale, (const void*)lse, (const void*)d_status})
+    if (reinterpret_cast<uintptr_t>(x) % 4) return fail(KVRP_ERR_ALIGNMENT, "%s: a 4-byte array is not aligned", fn);
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride = q_stride;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.k_pool = static_cast<const uint8_t*>(k_pool);
+  p.v_pool = static_cast<const uint8_t*>(v_pool);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.seqs = *seqs;
+  p.status = d_status;
+  p.Hq = n_q_heads;
+  p.Hkv = n_kv_heads;
+  p.g = n_q_heads / n_kv_heads;
+  p.g_inverse = ((1ull << 32) + p.g - 1) / p.g;
+  p.max_rows = !seqs->row_start ? 1 : seqs->max_rows ? seqs->max_rows : seqs->n_rows;
+  p.scale = softmax_scale * 1.4426950408889634f;
+  p.wait_cycles = test_wait_limit() ? (long long)test_wait_limit() : ptx::kTimeoutCycles;
+  return KVRP_OK;
+}
+
+kvrp_status attend_q8::check_rows(const char* fn, const Params& p) {
+  if ((int64_t)p.seqs.n_rows * p.Hq >= 1ll << 32 || (int64_t)p.seqs.n_rows * p.g >= (1 << 28) - kPromptRows)
+    return fail(KVRP_ERR_UNSUPPORTED, "%s: n_rows x n_q_heads must stay below 2^32, n_rows x group below 2^28", fn);
+  return KVRP_OK;
+}
 
 extern "C" {
 
@@ -862,62 +955,25 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
                          uint32_t* d_status, kvrp_stream_t stream) {
   const char* fn = "kv_attend_q8";
   g_last_launches = 0;
-  kvrp_status st = check_seqs(fn, seqs);
+  attend_q8::Params p;
+  kvrp_status st = attend_q8::check_call(fn, q, q_stride, seqs, n_q_heads, n_kv_heads, head_dim, softmax_scale, k_pool, v_pool,
+                                         k_scale, v_scale, out, lse, d_status, p);
   if (st != KVRP_OK) return st;
-  st = check_heads(fn, n_q_heads, n_kv_heads, head_dim);
-  if (st != KVRP_OK) return st;
-  if (!q || !k_pool || !v_pool || !k_scale || !v_scale || !out) return fail(KVRP_ERR_INVALID_ARG, "%s: NULL argument", fn);
-  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
-    return fail(KVRP_ERR_INVALID_ARG, "%s: softmax_scale must be > 0", fn);
-  const int64_t q_row = (int64_t)n_q_heads * head_dim;
-  q_stride = q_stride ? q_stride : q_row;
-  if (q_stride < q_row) return fail(KVRP_ERR_INVALID_ARG, "%s: a row stride is shorter than the row", fn);
-  if (q_stride % 8 || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
-    return fail(KVRP_ERR_ALIGNMENT, "%s: pointers must be 16-byte aligned, strides multiples of 8", fn);
-  for (const void* x : {(const void*)k_scale, (const void*)v_scale, (const void*)lse, (const void*)d_status})
-    if (reinterpret_cast<uintptr_t>(x) % 4) return fail(KVRP_ERR_ALIGNMENT, "%s: a 4-byte array is not aligned", fn);
   if (seqs->n_rows == 0) return KVRP_OK;
-  const int max_rows = !seqs->row_start ? 1 : seqs->max_rows ? seqs->max_rows : seqs->n_rows;
-  const size_t need = kv_attend_q8_workspace_size(n_q_heads, n_kv_heads, head_dim, max_rows);
+  const size_t need = kv_attend_q8_workspace_size(n_q_heads, n_kv_heads, head_dim, p.max_rows);
   if (!workspace || workspace_bytes < need) return fail(KVRP_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
-  const int g = n_q_heads / n_kv_heads;
-  const bool few = (int64_t)max_rows * g <= attend_q8::kMaxCols;
-  if ((int64_t)seqs->n_rows * n_q_heads >= 1ll << 32 || (int64_t)seqs->n_rows * g >= (1 << 28) - attend_q8::kPromptRows)
-    return fail(KVRP_ERR_UNSUPPORTED, "%s: n_rows x n_q_heads must stay below 2^32, n_rows x group below 2^28", fn);
-  const int hg = attend_q8::head_group(n_kv_heads);
+  st = attend_q8::check_rows(fn, p);
+  if (st != KVRP_OK) return st;
   int sms = 0, smem_optin = 0;
   st = current_device_sms(&sms, &smem_optin);
   if (st != KVRP_OK) return st;
-
-  attend_q8::Params p;
-  std::memset(&p, 0, sizeof(p));
-  p.q = static_cast<const uint16_t*>(q);
-  p.q_stride = q_stride;
-  p.out = static_cast<uint16_t*>(out);
-  p.lse = lse;
-  p.k_pool = static_cast<const uint8_t*>(k_pool);
-  p.v_pool = static_cast<const uint8_t*>(v_pool);
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
-  p.seqs = *seqs;
-  p.status = d_status;
-  p.Hq = n_q_heads;
-  p.Hkv = n_kv_heads;
-  p.g = g;
-  p.g_inverse = ((1ull << 32) + g - 1) / g;
-  p.n_cta = std::min(attend_q8::kMaxCtas, few ? attend_q8::kMaxCtasPerSm * sms : sms);
-  p.cols = few ? hg * max_rows * g : attend_q8::kPromptRows;
-  p.max_rows = max_rows;
-  p.hg = hg;
-  p.n_grp = n_kv_heads / hg;
-  p.streams = attend_q8::kWarps / hg;
-  p.unit_pages = std::max(1, 2048 / (hg * head_dim));   // about 2 us of a CTA's share of the bandwidth
-  p.rounds = hg == 1 ? 4 : hg == 2 ? 3 : hg == 4 ? 2 : 0;
-  p.scale = softmax_scale * 1.4426950408889634f;
-  p.wait_cycles = test_wait_limit() ? (long long)test_wait_limit() : ptx::kTimeoutCycles;
+  const bool few = (int64_t)p.max_rows * p.g <= attend_q8::kMaxCols;
+  p.n_cta = std::min(attend_q8::kMaxCtas, sms);
+  p.cols = attend_q8::kPromptRows;
+  if (few) attend_q8::set_few(p, sms, head_dim);
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
   p.meta = reinterpret_cast<int4*>(base);
-  p.partial = reinterpret_cast<float*>(base + attend_q8::meta_bytes(p.n_cta));
+  p.partial = reinterpret_cast<float*>(base + attend_q8::meta_bytes(std::min(attend_q8::kMaxCtas, few ? attend_q8::kMaxCtasPerSm * sms : sms)));
   if (!few) {
     CUtensorMap kmap, vmap;
     st = encode_q8_pool(&kmap, k_pool, seqs->num_pages, n_kv_heads * head_dim, head_dim);
@@ -928,13 +984,7 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
     g_last_launches = 2;
     return KVRP_OK;
   }
-  const bool two = max_rows * g > 8;
-  if (two) p.n_cta = std::min(p.n_cta, attend_q8::Decode<128, 2>::kCtas * sms);
-  auto kernel = head_dim == 64 ? (two ? attend_q8::decode_kernel<64, 2> : attend_q8::decode_kernel<64, 1>)
-                               : (two ? attend_q8::decode_kernel<128, 2> : attend_q8::decode_kernel<128, 1>);
-  const int smem = head_dim == 64 ? (two ? attend_q8::Decode<64, 2>::kSmem : attend_q8::Decode<64, 1>::kSmem)
-                                  : (two ? attend_q8::Decode<128, 2>::kSmem : attend_q8::Decode<128, 1>::kSmem);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = attend_q8::launch_few(p, head_dim, stream, attend_q8::kAll);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -942,16 +992,10 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(p.n_cta);
-  cfg.blockDim = dim3(attend_q8::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, p);
-  if (e == cudaSuccess) {
-    cfg.gridDim = dim3(5 * sms);
-    cfg.blockDim = dim3(attend_q8::kCombineThreads);
-    cfg.dynamicSmemBytes = 0;
+  cfg.gridDim = dim3(5 * sms);
+  cfg.blockDim = dim3(attend_q8::kCombineThreads);
+  if (e == cudaSuccess)
     e = cudaLaunchKernelEx(&cfg, head_dim == 64 ? attend_q8::combine_kernel<64> : attend_q8::combine_kernel<128>, p);
-  }
   if (e != cudaSuccess) return fail(KVRP_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
   g_last_launches = 2;
   return KVRP_OK;

@@ -48,12 +48,41 @@ struct Params {
   uint64_t g_inverse;   // 2^32 / g, rounded up
   float scale;          // softmax_scale * log2(e)
   long long wait_cycles;   // many rows: limit of the pipeline's waits
+  // kv_attend_shared_q8 only: the tokens that all sequences begin with, and its passes' results
+  const int32_t *prefix_table, *prefix_length;
+  int prefix_pages;
+  float* dense;         // [n_rows][Hq][D + 4]: like `partial`, of a unit that one CTA held
+  int2* found;          // [n_rows][n_grp], few rows: by a sequence's first row the CTA that begins a unit, and its
+                        // parts (0: it is dense)
 };
+
+// Which tokens a kernel's rows attend over: all of their sequence's (kv_attend_q8); the shared ones, for all rows
+// of the batch as if they were one sequence's, each row seeing all; or those behind the shared ones.
+enum Part { kAll, kShared, kRest };
 
 // The kernel for many rows: its columns (rows a partial result holds) and its launch,
 // p.n_cta blocks.
 constexpr int kPromptRows = 256;
-cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap, const Params& p, int head_dim, cudaStream_t stream);
+// Tokens of its tiles: what TMEM holds.
+__host__ __device__ constexpr int prompt_tokens(int head_dim) { return head_dim == 128 ? 80 : 128; }
+// Beginning and ending a unit (its queries, the first scores, the results) takes a CTA as long as some
+// tiles do; the shares count that, or the CTAs of a batch's many short units finish last.
+constexpr int kUnitTiles = 6;   // 4: 222 us for 6 questions of 37 to 900 rows, 6: 220 (215 with a later step)
+// The fewest CTAs' worth of a batch: a share is at least a unit's tiles and two more.
+__host__ __device__ constexpr int64_t prompt_ctas(int64_t total) { return (total + kUnitTiles + 1) / (kUnitTiles + 2); }
+cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap, const Params& p, int head_dim, cudaStream_t stream,
+                          Part part = kAll);
+// The kernel for few rows, p.n_cta blocks.
+cudaError_t launch_few(const Params& p, int head_dim, cudaStream_t stream, Part part);
+void set_few(Params& p, int sms, int head_dim);   // p's fields for it
+// The host checks of both calls, and what they fill in of the parameters.
+kvrp_status check_call(const char* fn, const void* q, int64_t& q_stride, const kvrp_seqs* seqs, int32_t n_q_heads,
+                       int32_t n_kv_heads, int32_t head_dim, float softmax_scale, const void* k_pool, const void* v_pool,
+                       const float* k_scale, const float* v_scale, void* out, float* lse, uint32_t* d_status, Params& p);
+kvrp_status check_rows(const char* fn, const Params& p);
+size_t meta_bytes(int n_cta);
+int head_group(int n_kv_heads);
+int sm_count();
 
 #ifdef __CUDACC__
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -85,6 +114,40 @@ __device__ __forceinline__ float2 result_factors(float m, float om, float l) {
   if (l == 0.f) return make_float2(0.f, 0.f);
   const float d = om - m - kShift, half = fmaxf(0.5f * d, -100.f);   // d is -inf where all scales are 0
   return make_float2(ex2(half), ex2(d - half) / l);
+}
+
+// The shared tokens of kv_attend_shared_q8, in whole pages, and the batch's rows; tokens -1: out of range.
+struct View {
+  int tokens, first, end;
+};
+__device__ __forceinline__ View load_view(const Params& p) {
+  View v;
+  v.first = p.seqs.row_start ? p.seqs.row_start[0] : 0;
+  v.end = p.seqs.row_start ? p.seqs.row_start[p.seqs.n_seqs] : p.seqs.n_rows;
+  const int length = *p.prefix_length;
+  const bool ok = length >= 0 && length / kPage <= p.prefix_pages && v.first >= 0 && v.end >= v.first && v.end <= p.seqs.n_rows;
+  v.tokens = ok ? length / kPage * kPage : -1;
+  return v;
+}
+// sequence() for a part: rows, and the tokens that they see at most of it.
+template <Part kPart>
+__device__ __forceinline__ bool part_sequence(const Params& p, int s, int& row0, int& rows, int& len) {
+  if constexpr (kPart == kAll) return sequence(p.seqs, s, row0, rows, len);
+  const View v = load_view(p);
+  if constexpr (kPart == kShared) {
+    row0 = v.first;
+    rows = v.tokens > 0 ? v.end - v.first : 0;
+    len = max(v.tokens, 0);
+    return true;
+  }
+  // A sequence that is not behind the shared tokens, or whose rows are not among the batch's, is bad.
+  bool ok = sequence(p.seqs, s, row0, rows, len);
+  if (ok && rows > 0) {
+    ok = v.tokens >= 0 && len - rows >= v.tokens && row0 >= v.first && row0 + rows <= v.end;
+    if (ok) len -= v.tokens;
+    else rows = 0;
+  }
+  return ok;
 }
 
 __device__ __forceinline__ void write_idle(const Params& p, int D) {

@@ -86,7 +86,7 @@ constexpr float kNear = 0x1p-12f, kReach = 0x1p-48f;
 
 template <int D>
 struct Prompt {
-  static constexpr int kN = D == 128 ? 80 : 128;   // tokens of a tile
+  static constexpr int kN = prompt_tokens(D);      // tokens of a tile
   static constexpr int kP = kN / kPage;            // its pages
   static constexpr int kP0 = (kP + 1) / 2;         // the pages whose weights are handed over first
   static constexpr int kQ = kRows * D;             // bytes of one e4m3 part of a Q tile
@@ -227,10 +227,6 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---- units and shares ------------------------------------------------------------------------
-// Beginning and ending a unit (its queries, the first scores, the results) takes a CTA as long as some
-// tiles do; the shares count that, or the CTAs of a batch's many short units finish last.
-constexpr int kUnitTiles = 6;   // 4: 222 us for the 6 questions above, 6: 220 (215 with a later step)
-
 // A unit's part inside this CTA's share: tiles [j0, j1) of its n_kv.
 struct Unit {
   int s, rt, h;             // sequence, row tile, KV head
@@ -239,24 +235,26 @@ struct Unit {
   int from, spent;          // this part's costs [from, from + spent) of its unit
   int64_t left;             // cost of the share from here on
 };
-template <int N>
+template <int N, Part kPart>
 __device__ __forceinline__ int tiles_of(int row0_col, int g, int rows, int len) {   // token tiles of a row tile
+  if constexpr (kPart == kShared) return (len + N - 1) / N;
   const int last = min(rows - 1, (row0_col + kPromptRows - 1) / g);                 // its last token among the rows
   return (len - rows + last + N) / N;
 }
+template <Part kPart>
 __device__ __forceinline__ bool load_seq(const Params& p, int s, Unit& u, bool tell = false) {
-  const bool ok = sequence(p.seqs, s, u.row0, u.rows, u.len) && u.rows <= p.max_rows;
+  const bool ok = part_sequence<kPart>(p, s, u.row0, u.rows, u.len) && (kPart == kShared || u.rows <= p.max_rows);
   if (tell && !ok) flag(p.status, KVRP_DEV_BAD_LENGTH);
   u.n_rt = ok ? (int)(((int64_t)u.rows * p.g + kPromptRows - 1) / kPromptRows) : 0;
   return u.n_rt > 0;
 }
 // The cost of sequence s over all its row tiles, by one warp (one head's worth).
-template <int N>
+template <int N, Part kPart>
 __device__ __forceinline__ int64_t seq_cost(const Params& p, int s, bool tell) {
   Unit u;
   int64_t sum = 0;
-  if (load_seq(p, s, u, tell && (threadIdx.x & 31) == 0))
-    for (int rt = threadIdx.x & 31; rt < u.n_rt; rt += 32) sum += kUnitTiles + tiles_of<N>(rt * kPromptRows, p.g, u.rows, u.len);
+  if (load_seq<kPart>(p, s, u, tell && (threadIdx.x & 31) == 0))
+    for (int rt = threadIdx.x & 31; rt < u.n_rt; rt += 32) sum += kUnitTiles + tiles_of<N, kPart>(rt * kPromptRows, p.g, u.rows, u.len);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
@@ -284,16 +282,16 @@ struct Shared {
   int nan_at[kWarpsRows][kMostFeatures];   // then: the first token with one, by features, a softmax warp's unit
   uint32_t tmem;
 };
-template <int N>
+template <int N, Part kPart>
 __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.seqs.n_seqs;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = kPart == kShared ? 1 : p.seqs.n_seqs;
   int64_t mine = 0;
-  for (int s = warp; s < n; s += kWarpsAll) mine += seq_cost<N>(p, s, blockIdx.x == 0) * p.Hkv;
+  for (int s = warp; s < n; s += kWarpsAll) mine += seq_cost<N, kPart>(p, s, blockIdx.x == 0) * p.Hkv;
   if (lane == 0) sh.cost[warp] = mine;
   __syncthreads();
   int64_t total = 0;
   for (int w = 0; w < kWarpsAll; ++w) total += sh.cost[w];
-  const int64_t n_cta = min((int64_t)p.n_cta, (total + kUnitTiles + 1) / (kUnitTiles + 2));
+  const int64_t n_cta = min((int64_t)p.n_cta, prompt_ctas(total));
   if ((int)blockIdx.x >= n_cta) return false;
   const int64_t a = total * blockIdx.x / n_cta, b = total * (blockIdx.x + 1) / n_cta;
   if (threadIdx.x == 0) {
@@ -305,7 +303,7 @@ __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
   int s = 0;
   for (int s0 = 0; s0 < n; s0 += kWarpsAll) {   // the sequence that holds tile a
     __syncthreads();
-    const int64_t c = s0 + warp < n ? seq_cost<N>(p, s0 + warp, false) * p.Hkv : 0;
+    const int64_t c = s0 + warp < n ? seq_cost<N, kPart>(p, s0 + warp, false) * p.Hkv : 0;
     if (lane == 0) sh.cost[warp] = c;
     __syncthreads();
     bool here = false;
@@ -319,11 +317,11 @@ __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
   // the unit inside it, by warp 0: 32 row tiles at a time
   if (warp == 0) {
     Unit u;
-    load_seq(p, s, u);
+    load_seq<kPart>(p, s, u);
     int64_t at = a - before;   // tiles into the sequence
     for (int r0 = 0; r0 < u.n_rt; r0 += 32) {
       const int rt = r0 + lane;
-      const int t = rt < u.n_rt ? tiles_of<N>(rt * kPromptRows, p.g, u.rows, u.len) : -kUnitTiles;
+      const int t = rt < u.n_rt ? tiles_of<N, kPart>(rt * kPromptRows, p.g, u.rows, u.len) : -kUnitTiles;
       const int cost = t + kUnitTiles;
       int64_t sum = (int64_t)cost * p.Hkv;
 #pragma unroll
@@ -349,7 +347,7 @@ __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
   return sh.first.j1 > sh.first.j0 || sh.first.left > sh.first.spent;
 }
 // The share's next unit; false at its end.
-template <int N>
+template <int N, Part kPart>
 __device__ __forceinline__ bool next_unit(const Params& p, Unit& u) {
   u.left -= u.spent;
   if (u.left <= 0) return false;
@@ -358,9 +356,9 @@ __device__ __forceinline__ bool next_unit(const Params& p, Unit& u) {
     if (++u.rt == u.n_rt) {
       u.rt = 0;
       do ++u.s;
-      while (!load_seq(p, u.s, u));
+      while (!load_seq<kPart>(p, u.s, u));
     }
-    u.n_kv = tiles_of<N>(u.rt * kPromptRows, p.g, u.rows, u.len);
+    u.n_kv = tiles_of<N, kPart>(u.rt * kPromptRows, p.g, u.rows, u.len);
   }
   take(u, 0);
   return u.j1 > 0;
@@ -371,7 +369,9 @@ __device__ __forceinline__ int active_tiles(const Params& p, const Unit& u) {   
 // x / g for 0 <= x < 2^28 (the host keeps rows x group below): by a product with 2^32 / g, rounded up.
 __device__ __forceinline__ int over_group(const Params& p, int x) { return (int)((uint64_t)(uint32_t)x * p.g_inverse >> 32); }
 // Tokens below this are seen by all rows of the unit.
+template <Part kPart>
 __device__ __forceinline__ int seen_by_all(const Params& p, const Unit& u) {
+  if constexpr (kPart == kShared) return u.len;
   return u.len - u.rows + over_group(p, u.rt * kPromptRows) + 1;
 }
 // The reference of the value scales after a tile: a power of two at least the largest scale,
@@ -382,17 +382,17 @@ __device__ __forceinline__ float next_vref(float vref, float top) {
   return __uint_as_float(min(e + 2u, 254u) << 23);
 }
 
-// The first of the tokens [from, to) of sequence s whose value is NaN, for each feature of KV head h (INT32_MAX:
+// The first of the tokens [from, to) of a table whose value is NaN, for each feature of KV head h (INT32_MAX:
 // none), by a warp.  Reads the values again; a cache without such values never comes here.
 template <int D>
-__device__ __noinline__ void find_later_nan(const Params& p, int s, int h, int from, int to, int* at) {
+__device__ __noinline__ void find_later_nan(const Params& p, const int32_t* table, int h, int from, int to, int* at) {
   constexpr int kEach = D / 32;
   const int lane = threadIdx.x & 31;
   int first[kEach];
 #pragma unroll
   for (int e = 0; e < kEach; ++e) first[e] = INT32_MAX;
   for (int t = to - 1; t >= from; --t) {
-    const int page = p.seqs.block_tables[(int64_t)s * p.seqs.table_stride + t / kPage];
+    const int page = table[t / kPage];
     if (page < 0 || page >= p.seqs.num_pages) continue;
     const uint8_t* v = p.v_pool + (((int64_t)page * kPage + t % kPage) * p.Hkv + h) * D + lane * kEach;
 #pragma unroll
@@ -405,7 +405,16 @@ __device__ __noinline__ void find_later_nan(const Params& p, int s, int h, int f
   __syncwarp();
 }
 
-template <int D>
+// The pages of a sequence's tokens in this part.
+template <Part kPart>
+__device__ __forceinline__ const int32_t* table_of(const Params& p, int s) {
+  if constexpr (kPart == kShared) return p.prefix_table;
+  const int32_t* table = p.seqs.block_tables + (int64_t)s * p.seqs.table_stride;
+  if constexpr (kPart == kRest) table += load_view(p).tokens / kPage;   // a sequence with rows here: tokens >= 0
+  return table;
+}
+
+template <int D, Part kPart>
 __global__ void __launch_bounds__(kThreadsAll, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ Params p) {
@@ -454,7 +463,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
   }
   pdl_wait();
   pdl_launch_dependents();
-  const bool any = find_share<N>(p, sh);
+  const bool any = find_share<N, kPart>(p, sh);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -478,7 +487,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
   Unit u = sh.first;
 
   if (!any) {
-    if (tid == 0) p.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (kPart != kShared && tid == 0) p.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   } else if (warp >= 12) {
     fewer_registers<L::kRegsMisc>();
     if (warp == 12) {
@@ -487,6 +496,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       bool ok = true;
       do {
         const int pages = (u.len + kPage - 1) / kPage;
+        const int32_t* table = table_of<kPart>(p, u.s);
         // The reference of the value scales; none from a tile on whose scales lie too far apart for it, or from where
         // it is too far from the first one for the accumulator that began relative to that.
         float vref = 0.f, first_vref = 0.f;
@@ -498,7 +508,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           int page = p.seqs.num_pages;   // past the pool: the box reads zeros
           float fk = 0.f, fv = mine ? kZeroBlock : 0.f;
           if (mine) {
-            const int e = p.seqs.block_tables[(int64_t)u.s * p.seqs.table_stride + pg];
+            const int e = table[pg];
             if (e >= 0 && e < p.seqs.num_pages) {
               page = e;
               fk = p.k_scale[(int64_t)e * p.Hkv + u.h];
@@ -536,7 +546,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           if (mine) tma_load_3d(smem + L::kOffV + vs * L::kKV + lane * kPage * D, &vmap, vfull(vs), u.h * D, 0, page);
           ++nv;
         }
-      } while (ok && next_unit<N>(p, u));
+      } while (ok && next_unit<N, kPart>(p, u));
       if (!ok && lane == 0) {   // every issued copy lands before the CTA exits
         for (int i = max(0, nk - L::kKst); i < nk; ++i) drain_wait(kfull(i % L::kKst), (i / L::kKst) & 1, p.status);
         for (int i = max(0, nv - L::kVst); i < nv; ++i) drain_wait(vfull(i % L::kVst), (i / L::kVst) & 1, p.status);
@@ -613,7 +623,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           tc_fence_after();
           values(n, L::kP0, L::kP, 1);
         }
-      } while (ok && next_unit<N>(p, u));
+      } while (ok && next_unit<N, kPart>(p, u));
       if (!ok && elect_one()) {   // let the tensor cores finish before TMEM is freed
         mma_commit(drained(t));
         drain_wait(drained(t), 0, p.status);
@@ -633,7 +643,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     int n = 0;
     bool ok = true;
     do {
-      const int seen_all = seen_by_all(p, u);
+      const int seen_all = seen_by_all<kPart>(p, u);
       for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
         const int vs = n % L::kVst, vb = n % L::kCst, slot = n % kScaleSlots;
         ok = wait(vfull(vs), (n / L::kVst) & 1);
@@ -704,7 +714,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         fence_proxy_async_smem();
         mbar_arrive(cfull(vb));
       }
-    } while (ok && next_unit<N>(p, u));
+    } while (ok && next_unit<N, kPart>(p, u));
   } else {
     more_registers<L::kRegsRow>();
     // ---- softmax: a thread a row ----------------------------------------------------------------
@@ -747,8 +757,8 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       const int col = u.rt * kPromptRows + t * kRows + row;   // (token, query head) pair: below 2^31, n_rows x group is
       const bool live = col < u.rows * p.g;
       const int tok = over_group(p, col);
-      const int limit = live ? u.len - u.rows + tok + 1 : 0;               // tokens the row sees
-      const int first_limit = u.len - u.rows + over_group(p, u.rt * kPromptRows + t * kRows) + 1;
+      const int limit = !live ? 0 : kPart == kShared ? u.len : u.len - u.rows + tok + 1;   // tokens the row sees
+      const int first_limit = kPart == kShared ? u.len : u.len - u.rows + over_group(p, u.rt * kPromptRows + t * kRows) + 1;
       const uint32_t out_row = live ? (uint32_t)(u.row0 + tok) * p.Hq + u.h * p.g + (col - tok * p.g) : kNoRow;
       // ---- q / 2^(e - 7) = high + low, both e4m3 -------------------------------------------------
       // A warp its 32 rows, D / 16 lanes a row, so that a load takes whole rows (a row a thread took
@@ -975,11 +985,12 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       // Rows are laid out in shared memory, in the Q tile that the finished unit no longer needs, and
       // leave by whole rows (32 rows' 16 bytes an instruction took 2 us a unit): kRowChunks chunks a pass.
       constexpr int kRowChunks = D / 8, kHalf = D / 16;   // 16-byte chunks of the two parts, of one
-      const bool whole = begins && ends;
+      const bool whole = kPart == kAll && begins && ends;   // rows that are done
+      const bool dense = kPart != kAll && begins && ends;   // or that are to be joined with the other part's
       const float2 f = result_factors(m, om, l);
       float* part = p.partial + ((int64_t)(blockIdx.x * 2 + (begins ? 1 : 0)) * p.cols + t * kRows) * (D + 4);
       const bool odd = uniform(*static_cast<volatile int*>(&sh.later_nan)) != 0;
-      if (odd) find_later_nan<D>(p, u.s, u.h, max(seen_by_all(p, u), u.j0 * N), min(u.len, u.j1 * N), sh.nan_at[warp]);
+      if (odd) find_later_nan<D>(p, table_of<kPart>(p, u.s), u.h, max(seen_by_all<kPart>(p, u), u.j0 * N), min(u.len, u.j1 * N), sh.nan_at[warp]);
       auto stage = [&](int x, uint32_t a, uint32_t b2, uint32_t c2, uint32_t d) {
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(row_chunk(x / kHalf, row, x % kHalf)), "r"(a), "r"(b2), "r"(c2), "r"(d) : "memory");
       };
@@ -1036,18 +1047,19 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           }
           if (to_row != kNoRow) {
             if (whole) *reinterpret_cast<uint4*>(to_out + (int64_t)to_row * (2 * D)) = v;
+            else if (dense) *reinterpret_cast<uint4*>(p.dense + (int64_t)to_row * (D + 4) + pass * (D / 2) + 4 * x) = v;
             else *reinterpret_cast<uint4*>(to_part + i * kAtOnce * (D + 4) * 4) = v;
           }
         }
         __syncwarp();
       }
       if (live) {
-        if (!whole) *reinterpret_cast<float4*>(part + (int64_t)row * (D + 4) + D) = make_float4(m, om, l, 0.f);
+        if (!whole) *reinterpret_cast<float4*>((dense ? p.dense + (int64_t)out_row * (D + 4) : part + (int64_t)row * (D + 4)) + D) = make_float4(m, om, l, 0.f);
         else if (p.lse) p.lse[out_row] = (m + lg2(l)) * kLn2;
       }
       tc_fence_before();   // the accumulator is read before the next unit's first product
-    } while (ok && next_unit<N>(p, u));
-    if (tid == 0) {
+    } while (ok && next_unit<N, kPart>(p, u));
+    if (kPart != kShared && tid == 0) {
       p.meta[2 * blockIdx.x] = meta;
       p.meta[2 * blockIdx.x + 1] = make_int4(meta_cols, 0, 0, 0);
     }
@@ -1057,7 +1069,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 13) tmem_dealloc(tmem, 512);
-  write_idle(p, D);
+  if constexpr (kPart == kAll) write_idle(p, D);
 }
 
 // A warp a row of a unit that more than one CTA held: block (i, y) takes rows y * kCombineRows .. of
@@ -1065,7 +1077,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
 // share where the unit ends and says so, so that nothing is searched here. Four parts at a time cost 5 us
 // more of the 6 questions' 215: most units have two.
 constexpr int kCombineWarps = 4, kCombineRows = 8;
-template <int D>
+template <int D, Part kPart>
 __global__ void __launch_bounds__(32 * kCombineWarps) prompt_combine_kernel(const __grid_constant__ Params p) {
   constexpr int V = D / 32;   // values a lane
   constexpr int kEach = kCombineRows / kCombineWarps, kBatch = 2;   // rows a warp, parts in flight
@@ -1128,21 +1140,28 @@ __global__ void __launch_bounds__(32 * kCombineWarps) prompt_combine_kernel(cons
   for (int k = 0; k < kEach; ++k) {
     const int col = col0 + warp + k * kCombineWarps;
     if (col >= mt2.x) continue;
-    const float2 r = result_factors(m[k], om[k], l[k]);
     const int tok = over_group(p, col);
     const int64_t row = (int64_t)(mt.w + tok) * p.Hq + mt.y * p.g + col - tok * p.g;
+    if constexpr (kPart == kRest) {
+      float* to = p.dense + row * (D + 4);
 #pragma unroll
-    for (int v = 0; v < V; v += 2) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(acc[k][v] * r.x * r.y, acc[k][v + 1] * r.x * r.y);
-      *reinterpret_cast<uint32_t*>(p.out + row * D + lane * V + v) = *reinterpret_cast<const uint32_t*>(&b);
+      for (int v = 0; v < V; v += 2) *reinterpret_cast<float2*>(to + lane * V + v) = make_float2(acc[k][v], acc[k][v + 1]);
+      if (lane == 0) *reinterpret_cast<float4*>(to + D) = make_float4(m[k], om[k], l[k], 0.f);
+    } else {
+      const float2 r = result_factors(m[k], om[k], l[k]);
+#pragma unroll
+      for (int v = 0; v < V; v += 2) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(acc[k][v] * r.x * r.y, acc[k][v + 1] * r.x * r.y);
+        *reinterpret_cast<uint32_t*>(p.out + row * D + lane * V + v) = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      if (p.lse && lane == 0) p.lse[row] = (m[k] + lg2(l[k])) * kLn2;
     }
-    if (p.lse && lane == 0) p.lse[row] = (m[k] + lg2(l[k])) * kLn2;
   }
 }
 
-template <int D>
+template <int D, Part kPart>
 cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Params& p, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Prompt<D>::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, kPart>, cudaFuncAttributeMaxDynamicSharedMemorySize, Prompt<D>::kSmem);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1153,18 +1172,23 @@ cudaError_t launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const Param
   cfg.gridDim = dim3(p.n_cta);
   cfg.blockDim = dim3(kThreadsAll);
   cfg.dynamicSmemBytes = Prompt<D>::kSmem;
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, prompt_kernel<D>, kmap, vmap, p);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, prompt_kernel<D, kPart>, kmap, vmap, p);
+  if (kPart == kShared) return e;   // its parts are joined with the other's
   cfg.gridDim = dim3(p.n_cta, kPromptRows / kCombineRows);
   cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.dynamicSmemBytes = 0;
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, prompt_combine_kernel<D>, p);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, prompt_combine_kernel<D, kPart>, p);
   return e;
 }
 
 }  // namespace
 
-cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap, const Params& p, int head_dim, cudaStream_t stream) {
-  return head_dim == 64 ? launch<64>(kmap, vmap, p, stream) : launch<128>(kmap, vmap, p, stream);
+cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap, const Params& p, int head_dim, cudaStream_t stream,
+                          Part part) {
+  const auto f = part == kAll ? (head_dim == 64 ? launch<64, kAll> : launch<128, kAll>)
+               : part == kShared ? (head_dim == 64 ? launch<64, kShared> : launch<128, kShared>)
+                                 : (head_dim == 64 ? launch<64, kRest> : launch<128, kRest>);
+  return f(kmap, vmap, p, stream);
 }
 
 }  // namespace attend_q8

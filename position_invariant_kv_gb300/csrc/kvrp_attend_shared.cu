@@ -1,0 +1,270 @@
+// Attention over the 8-bit paged cache of a batch whose sequences begin with the same tokens
+// (kv_attend_shared_q8).
+//
+//   out = (e^a O_a + e^b O_b) / (e^a + e^b):  O_a, a the attention and log-sum-exp over the shared tokens,
+//   O_b, b over a sequence's own tokens behind them (causal).
+//
+// Three passes, none of which reads anything twice:
+//   - the shared tokens, for all rows of the batch as if they were one sequence's: the tensor-core kernel
+//     for prompts (kvrp_attend_q8_prompt.cu) with every row seeing every token.  K and V of the shared pages are
+//     read once for each 256 (row, query head) pairs of a KV head instead of once a sequence, and few rows
+//     a sequence become full tiles.
+//   - the sequences' own tokens: the kernel that kv_attend_q8 takes for as many rows, from the shared
+//     pages' end on.
+//   - join_kernel merges both passes' partial results, in fp32, and rounds once.  A unit of the first pass
+//     that several CTAs shared is found by arithmetic (all its units cost the same); one of the second
+//     by a record that the CTA that begins it leaves.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "kvrp.h"
+#include "kvrp_attend_q8.h"
+#include "kvrp_plan.h"
+#include "kvrp_q8.h"
+
+namespace kvrp {
+namespace attend_q8 {
+
+namespace {
+
+struct Join {
+  Params p;                   // of the second pass
+  const float *shared, *shared_dense;   // the first one's partial and dense results, its CTAs at most
+  int shared_ctas;
+  bool few;
+};
+
+constexpr int kJoinThreads = 128;
+
+// A row and kItems of its query heads a block; D / 4 threads hold an item's features, four each.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Join j) {
+  constexpr int kLanes = D / 4, kItems = kJoinThreads / kLanes, N = prompt_tokens(D), kStep = D + 4;
+  const Params& p = j.p;
+  const int chunks = (p.Hq + kItems - 1) / kItems;
+  const int row = blockIdx.x / chunks, head = blockIdx.x % chunks * kItems + threadIdx.x / kLanes, f = threadIdx.x % kLanes;
+  pdl_wait();
+  pdl_launch_dependents();
+  const View view = load_view(p);
+  if (view.tokens < 0) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) flag(p.status, KVRP_DEV_BAD_LENGTH);
+    return;
+  }
+  int s = row;   // the row's sequence: the last whose first row is not behind it
+  if (p.seqs.row_start) {
+    if (row < view.first || row >= view.end) return;
+    int lo = 0, hi = p.seqs.n_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.seqs.row_start[mid] <= row) lo = mid;
+      else hi = mid;
+    }
+    s = lo;
+  }
+  int row0, rows, len;
+  const bool ok = part_sequence<kRest>(p, s, row0, rows, len);
+  if (head >= p.Hq) return;
+  const int64_t at = (int64_t)row * p.Hq + head;
+  if (ok && len == 0) {   // an idle place of the batch
+    const int end = p.seqs.row_start ? p.seqs.row_start[s + 1] : s + 1;
+    if (row < row0 || row >= end) return;
+    *reinterpret_cast<uint2*>(p.out + at * D + 4 * f) = make_uint2(0, 0);
+    if (p.lse && f == 0) p.lse[at] = -INFINITY;
+    return;
+  }
+  if (!ok || rows > p.max_rows || row < row0 || row >= row0 + rows) return;   // flagged by the second pass
+
+  const int h = head / p.g, jq = head - h * p.g;
+  // the shared tokens' parts
+  int first = 0, n_shared = 0;
+  int64_t y = 0;
+  if (view.tokens > 0) {
+    const int64_t col = (int64_t)(row - view.first) * p.g + jq, cost = (view.tokens + N - 1) / N + kUnitTiles;
+    const int64_t tiles = ((int64_t)(view.end - view.first) * p.g + kPromptRows - 1) / kPromptRows;
+    const int64_t unit = col / kPromptRows * p.Hkv + h, total = tiles * p.Hkv * cost;
+    const int64_t n_cta = min((int64_t)j.shared_ctas, prompt_ctas(total));
+    // the CTA of cost x is the largest c with total c / n_cta not above it
+    first = (int)(((unit * cost + kUnitTiles + 1) * n_cta - 1) / total);
+    n_shared = (int)(((unit + 1) * cost * n_cta - 1) / total) - first + 1;
+    y = col % kPromptRows;
+  }
+  // the own tokens'
+  int2 own = make_int2(0, 0);
+  int64_t own_y = 0;
+  if (j.few) {
+    own = p.found[(int64_t)row0 * p.n_grp + h / p.hg];
+    own_y = (h % p.hg) * p.max_rows * p.g + (row - row0) * p.g + jq;
+  }
+  const int n = n_shared + max(own.y, 1);
+  const auto entry = [&](int x) -> const float* {
+    if (x < n_shared) return n_shared == 1 ? j.shared_dense + at * kStep
+                                           : j.shared + ((int64_t)((first + x) * 2 + (x == 0 ? 1 : 0)) * kPromptRows + y) * kStep;
+    x -= n_shared;
+    return own.y == 0 ? p.dense + at * kStep : p.partial + ((int64_t)((own.x + x) * 2 + (x == 0 ? 1 : 0)) * p.cols + own_y) * kStep;
+  };
+  float m = -INFINITY, om = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kBatch = 8;   // parts in flight
+  for (int x0 = 0; x0 < n; x0 += kBatch) {
+    float4 st[kBatch], v[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      st[b] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+      v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x0 + b < n) {
+        const float* e = entry(x0 + b);
+        st[b] = *reinterpret_cast<const float4*>(e + D);
+        v[b] = reinterpret_cast<const float4*>(e)[f];
+      }
+    }
+    float nm = m, no = om;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      nm = fmaxf(nm, st[b].x);
+      no = fmaxf(no, st[b].y);
+    }
+    const float zm = nm == -INFINITY ? 0.f : nm, zo = no == -INFINITY ? 0.f : no;   // 2^-inf = 0, and no inf - inf
+    l *= ex2(m - zm);
+    const float r = ex2(om - zo);
+    acc = make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
+    m = nm;
+    om = no;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      l = fmaf(st[b].z, ex2(st[b].x - zm), l);
+      const float w = ex2(st[b].y - zo);
+      acc.x = fmaf(v[b].x, w, acc.x);
+      acc.y = fmaf(v[b].y, w, acc.y);
+      acc.z = fmaf(v[b].z, w, acc.z);
+      acc.w = fmaf(v[b].w, w, acc.w);
+    }
+  }
+  const float2 r = result_factors(m, om, l);
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * r.x * r.y, acc.y * r.x * r.y),
+                       b = __floats2bfloat162_rn(acc.z * r.x * r.y, acc.w * r.x * r.y);
+  *reinterpret_cast<uint2*>(p.out + at * D + 4 * f) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  if (p.lse && f == 0) p.lse[at] = (m + lg2(l)) * kLn2;
+}
+
+// Where things are in the workspace, in bytes.
+struct Layout {
+  size_t meta, found, shared, shared_dense, partial, dense, end;
+};
+Layout layout(int Hq, int Hkv, int D, int64_t max_rows, int64_t n_rows, int sms) {
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const int g = Hq / Hkv, hg = head_group(Hkv);
+  const bool few = max_rows * g <= kMaxCols;
+  const size_t entry = (D + 4) * sizeof(float), rows = (size_t)n_rows * Hq * entry;
+  Layout l;
+  l.meta = 256;   // what aligning the caller's pointer takes
+  l.found = l.meta + (few ? 0 : meta_bytes(sms));
+  l.shared = l.found + (few ? up((size_t)n_rows * (Hkv / hg) * sizeof(int2)) : 0);
+  l.shared_dense = l.shared + up((size_t)sms * 2 * kPromptRows * entry);
+  l.partial = l.shared_dense + up(rows);
+  l.dense = l.partial + (few ? up((size_t)kMaxCtasPerSm * sms * 2 * hg * max_rows * g * entry)
+                             : up((size_t)sms * 2 * kPromptRows * entry));
+  l.end = l.dense + up(rows);
+  return l;
+}
+
+}  // namespace
+
+}  // namespace attend_q8
+}  // namespace kvrp
+
+using namespace kvrp;
+
+extern "C" {
+
+size_t kv_attend_shared_q8_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_rows,
+                                          int32_t n_rows) {
+  if (check_heads("kv_attend_shared_q8_workspace_size", n_q_heads, n_kv_heads, head_dim) != KVRP_OK || max_rows <= 0 ||
+      n_rows < max_rows)
+    return 0;
+  return attend_q8::layout(n_q_heads, n_kv_heads, head_dim, max_rows, n_rows, attend_q8::sm_count()).end;
+}
+
+kvrp_status kv_attend_shared_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs, const kvrp_prefix* prefix,
+                                int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, float softmax_scale,
+                                const void* k_pool, const void* v_pool, const float* k_scale, const float* v_scale, void* out,
+                                float* lse, void* workspace, size_t workspace_bytes, uint32_t* d_status, kvrp_stream_t stream) {
+  const char* fn = "kv_attend_shared_q8";
+  g_last_launches = 0;
+  attend_q8::Params p;
+  kvrp_status st = attend_q8::check_call(fn, q, q_stride, seqs, n_q_heads, n_kv_heads, head_dim, softmax_scale, k_pool, v_pool,
+                                         k_scale, v_scale, out, lse, d_status, p);
+  if (st != KVRP_OK) return st;
+  if (!prefix) return fail(KVRP_ERR_INVALID_ARG, "%s: NULL prefix", fn);
+  st = check_prefix(fn, prefix);
+  if (st != KVRP_OK) return st;
+  if (seqs->n_rows == 0) return KVRP_OK;
+  const size_t need = kv_attend_shared_q8_workspace_size(n_q_heads, n_kv_heads, head_dim, p.max_rows, seqs->n_rows);
+  if (!workspace || workspace_bytes < need) return fail(KVRP_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
+  st = attend_q8::check_rows(fn, p);
+  if (st != KVRP_OK) return st;
+  int sms = 0, smem_optin = 0;
+  st = current_device_sms(&sms, &smem_optin);
+  if (st != KVRP_OK) return st;
+  sms = attend_q8::sm_count();   // at most what the workspace is laid out for
+  const bool few = (int64_t)p.max_rows * p.g <= attend_q8::kMaxCols;
+  const attend_q8::Layout at = attend_q8::layout(n_q_heads, n_kv_heads, head_dim, p.max_rows, seqs->n_rows, sms);
+  uint8_t* base = reinterpret_cast<uint8_t*>(reinterpret_cast<uintptr_t>(workspace) & ~uintptr_t(255));
+  p.prefix_table = prefix->block_table;
+  p.prefix_length = prefix->length;
+  p.prefix_pages = prefix->n_pages;
+  p.n_cta = sms;
+  p.cols = attend_q8::kPromptRows;
+
+  CUtensorMap kmap, vmap;
+  st = encode_q8_pool(&kmap, k_pool, seqs->num_pages, n_kv_heads * head_dim, head_dim);
+  if (st == KVRP_OK) st = encode_q8_pool(&vmap, v_pool, seqs->num_pages, n_kv_heads * head_dim, head_dim);
+  if (st != KVRP_OK) return st;
+  attend_q8::Params shared = p;
+  shared.partial = reinterpret_cast<float*>(base + at.shared);
+  shared.dense = reinterpret_cast<float*>(base + at.shared_dense);
+  cudaError_t e = cudaSuccess;
+  int launches = 0;
+  if (prefix->n_pages > 0) {
+    e = attend_q8::launch_prompt(kmap, vmap, shared, head_dim, stream, attend_q8::kShared);
+    ++launches;
+  }
+  p.meta = reinterpret_cast<int4*>(base + at.meta);
+  p.found = reinterpret_cast<int2*>(base + at.found);
+  p.partial = reinterpret_cast<float*>(base + at.partial);
+  p.dense = reinterpret_cast<float*>(base + at.dense);
+  if (few) attend_q8::set_few(p, sms, head_dim);
+  if (e == cudaSuccess)
+    e = few ? attend_q8::launch_few(p, head_dim, stream, attend_q8::kRest)
+            : attend_q8::launch_prompt(kmap, vmap, p, head_dim, stream, attend_q8::kRest);
+  launches += few ? 1 : 2;
+
+  attend_q8::Join j;
+  j.p = p;
+  j.shared = shared.partial;
+  j.shared_dense = shared.dense;
+  j.shared_ctas = shared.n_cta;
+  j.few = few;
+  const int items = attend_q8::kJoinThreads / (head_dim / 4);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)((int64_t)seqs->n_rows * ((n_q_heads + items - 1) / items)));
+  cfg.blockDim = dim3(attend_q8::kJoinThreads);
+  if (e == cudaSuccess)
+    e = cudaLaunchKernelEx(&cfg, head_dim == 64 ? attend_q8::join_kernel<64> : attend_q8::join_kernel<128>, j);
+  if (e != cudaSuccess) return fail(KVRP_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  g_last_launches = launches + 1;
+  return KVRP_OK;
+}
+
+}  // extern "C"

@@ -50,8 +50,23 @@ struct Params {
 
 __device__ __forceinline__ float value(float x) { return x; }
 __device__ __forceinline__ float value(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
-// floor(2^40 x) of x in [0, 1]; 0 of NaN and of less.
-__device__ __forceinline__ uint64_t whole(float x) { return __float2ull_rz(fminf(fmaxf(x, 0.f), 1.f) * 0x1p40f); }
+// floor(2^40 x), x in [0, 1], as 2^20 high + low, both below 2^23 and so in the low bits of a sum with 2^23
+// that is rounded down; `bits` are those sums' own, kBits above high and low.  Every step is exact.  (The
+// conversion to 64 bits runs at a fraction of these four operations' rate: 256 rows of 262144 took 226 us.)
+constexpr uint32_t kBits = 0x4b000000u;   // 2^23
+struct Whole {
+  uint32_t high, low;
+  __device__ __forceinline__ explicit Whole(float x) {
+    const float h = __fmaf_rd(x, 0x1p20f, 0x1p23f);
+    const float rest = __fmaf_rn(x, 0x1p20f, 0x1p23f - h);
+    high = __float_as_uint(h);
+    low = __float_as_uint(__fmaf_rd(rest, 0x1p20f, 0x1p23f));
+  }
+};
+__device__ __forceinline__ uint64_t whole(float x) {
+  const Whole w(x);
+  return ((uint64_t)(w.high - kBits) << 20) + (w.low - kBits);
+}
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -107,43 +122,66 @@ __device__ __forceinline__ void load(const T* row, int first, int vocab, bool fi
 enum Kind { kTarget, kPositivePart, kWithout };   // weights: p; max(0, p - q); p but for one token
 template <typename T>
 struct Weights {
+  static constexpr int kE = Row<T>::kE;
   Row<T> p, q;
   int vocab, token;
   bool q_fits;
   template <Kind K>
-  __device__ __forceinline__ void raw(int v, T (&a)[16 / sizeof(T)], T (&b)[16 / sizeof(T)]) const {
-    const int first = v * Row<T>::kE - p.skip;
+  __device__ __forceinline__ void raw(int v, T (&a)[kE], T (&b)[kE]) const {
+    const int first = v * kE - p.skip;
     load<T>(p.at, first, vocab, true, a);
     if (K == kPositivePart) load<T>(q.at, first, vocab, q_fits, b);
   }
   template <Kind K>
   __device__ __forceinline__ uint64_t weight(int v, int i, T a, T b) const {
-    const uint64_t w = whole(value(a));
-    if (K == kWithout) return v * Row<T>::kE - p.skip + i == token ? 0 : w;
-    if (K == kTarget) return w;
-    const uint64_t less = whole(value(b));
-    return w > less ? w - less : 0;
+    const float x = __saturatef(value(a));   // [0, 1], and 0 of NaN
+    if (K == kWithout) return v * kE - p.skip + i == token ? 0 : whole(x);
+    if (K == kTarget) return whole(x);
+    return whole(x) - whole(fminf(x, __saturatef(value(b))));   // where q is not below p, p - p
   }
+  // Of vectors [begin, end), this lane's share.  With K = kWithout the token counts: taken off once, below.
   template <Kind K>
-  __device__ __forceinline__ uint64_t sum(int begin, int end) const {   // of vectors [begin, end), this lane's share
-    constexpr int kE = Row<T>::kE, kDepth = 4;
+  __device__ __forceinline__ uint64_t sum(int begin, int end) const {
+    constexpr int kDepth = 4;
     const int lane = threadIdx.x & 31;
     uint64_t s = 0;
+    const auto add = [&](const T (&a)[kE], const T (&b)[kE], uint32_t& high, uint32_t& low) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        const float x = __saturatef(value(a[i]));
+        const Whole w(x);
+        if (K == kPositivePart) {
+          const Whole less(fminf(x, __saturatef(value(b[i]))));
+          high += w.high - less.high;
+          low += w.low - less.low;
+        } else {
+          high += w.high - kBits;
+          low += w.low - kBits;
+        }
+      }
+    };
+    // at most 32 values at a time: |high|, |low| stay below 2^25; low may be negative
+    const auto flush = [&](uint32_t high, uint32_t low) { s += ((uint64_t)high << 20) + (uint64_t)(int64_t)(int32_t)low; };
     int v = begin + lane;
     for (; v + 32 * (kDepth - 1) < end; v += 32 * kDepth) {
       T a[kDepth][kE], b[kDepth][kE];
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) raw<K>(v + 32 * d, a[d], b[d]);
+      uint32_t high = 0, low = 0;
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d)
-#pragma unroll
-        for (int i = 0; i < kE; ++i) s += weight<K>(v + 32 * d, i, a[d][i], b[d][i]);
+      for (int d = 0; d < kDepth; ++d) add(a[d], b[d], high, low);
+      flush(high, low);
     }
     for (; v < end; v += 32) {
       T a[kE], b[kE];
       raw<K>(v, a, b);
-#pragma unroll
-      for (int i = 0; i < kE; ++i) s += weight<K>(v, i, a[i], b[i]);
+      uint32_t high = 0, low = 0;
+      add(a, b, high, low);
+      flush(high, low);
+    }
+    if (K == kWithout && token >= 0 && token < vocab) {
+      const int at = (token + p.skip) / kE;
+      if (at >= begin && at < end && (at - begin) % 32 == lane) s -= whole(__saturatef(value(p.at[token])));
     }
     return s;
   }
@@ -194,7 +232,7 @@ __device__ __forceinline__ void find(const Weights<T>& w, Smem& sh, int begin, i
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ Params p) {
   __shared__ Smem sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, s = blockIdx.y;
   const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
@@ -349,9 +387,11 @@ extern "C" kvrp_status kv_verify_drafts(const void* target, int64_t target_strid
   p.status = d_status;
   p.vocab = vocab;
 
-  // CTAs a sequence: as many as fill the GPU, of at least 2048 values each
-  int ctas = 1;
-  while (ctas < verify::kMostCtas && ctas * seqs->n_seqs < 2 * sms && vocab >= ctas * 4096) ctas *= 2;
+  // CTAs a sequence, of at least 4096 values each: what one filling of the GPU holds, two an SM, or the
+  // second filling costs as much as the first (64 sequences of 130003: 15.7 us with 4, 22.5 with 6,
+  // 20.6 with 8); for more sequences than that two, whose uneven ends hide each other (256 of 262144:
+  // 81.5 us with 1, 76.8 with 2, 85.9 with 8).
+  const int ctas = std::max(1, std::min({verify::kMostCtas, std::max(2, 2 * sms / seqs->n_seqs), vocab / 4096}));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -75,6 +75,43 @@ def test_verify_refusals(kvrp):  # noqa: F811
         assert st() == kvrp.KVRP_ERR_CUDA and st(draft=None, accepted=None, kept_lens=None) == kvrp.KVRP_ERR_CUDA
 
 
+def test_attend_shared_refusals(kvrp):  # noqa: F811
+    inv, ali, uns = kvrp.KVRP_ERR_INVALID_ARG, kvrp.KVRP_ERR_ALIGNMENT, kvrp.KVRP_ERR_UNSUPPORTED
+
+    def st(seqs=None, prefix=0, **over):
+        args = dict(q=0x10000, n_q_heads=8, n_kv_heads=2, head_dim=128, softmax_scale=0.1, k_pool=0x20000, v_pool=0x30000,
+                    k_scale=0x40000, v_scale=0x50000, out=0x60000, lse=0x70000, workspace=0x100000, workspace_bytes=1 << 40,
+                    stream=0)
+        args.update(over)
+        q = args.pop("q")
+        with pytest.raises(kvrp.KvrpError) as e:
+            kvrp.kv_attend_shared_q8(q, seqs or _Seqs(kvrp, max_rows=2), _Prefix(kvrp) if prefix == 0 else prefix, **args)
+        assert kvrp.kvrp_last_launch_count() == 0
+        return e.value.status
+
+    for over, code in BAD_SEQS:
+        assert st(seqs=_Seqs(kvrp, **over)) == getattr(kvrp, "KVRP_ERR_" + code), over
+    for over, code in BAD_PREFIX:
+        assert st(prefix=_Prefix(kvrp, **over)) == getattr(kvrp, "KVRP_ERR_" + code), over
+    assert st(prefix=None) == inv
+    for name in ("q", "out", "k_pool", "v_pool", "k_scale", "v_scale"):
+        assert st(**{name: None}) == inv, name
+    assert st(softmax_scale=0.0) == inv and st(softmax_scale=float("inf")) == inv and st(q_stride=1016) == inv
+    assert st(head_dim=96) == uns and st(n_q_heads=7) == uns and st(n_q_heads=34) == uns
+    assert st(q=0x10008) == ali and st(v_pool=0x30008) == ali and st(out=0x60004) == ali and st(lse=0x70002) == ali
+    assert st(q_stride=1028) == ali and st(d_status=0x70001) == ali
+    size = kvrp.kv_attend_shared_q8_workspace_size
+    for rows in (2, 10):
+        need = size(8, 2, 128, rows, 10)
+        assert need > 0 and st(seqs=_Seqs(kvrp, max_rows=rows), workspace_bytes=need - 1) == kvrp.KVRP_ERR_WORKSPACE
+    assert st(workspace=None) == kvrp.KVRP_ERR_WORKSPACE
+    assert size(8, 3, 128, 1, 1) == 0 and size(8, 2, 96, 1, 1) == 0 and size(8, 2, 128, 0, 1) == 0 and size(8, 2, 128, 3, 2) == 0
+    assert st(seqs=_Seqs(kvrp, n_rows=1 << 27, max_rows=2), workspace_bytes=1 << 50) == uns
+    import torch
+    if not torch.cuda.is_available():
+        assert st(seqs=_Seqs(kvrp, max_rows=2), workspace_bytes=size(8, 2, 128, 2, 10)) == kvrp.KVRP_ERR_CUDA
+
+
 def test_prefix_object_checks(kvrp):  # noqa: F811
     import torch
     table, length = torch.zeros(5, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
