@@ -242,7 +242,12 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
   const uint32_t ring = smem_u32(raw_smem) + (uint32_t)warp * kStages * C::kStage;
   float* merge = reinterpret_cast<float*>(raw_smem + C::kRing);
   float2* my_scales = scales + warp * kStages * PG;
-  pdl_wait();
+  // Behind the shared tokens' pass: its blocks have all waited for what came before this call when they let this
+  // kernel's in, so what is read here is there, and what is written here nobody else reads or writes any more.  This
+  // kernel takes the places that the pass's blocks leave one after another, and waits for it at its end instead, as
+  // its own end tells the join that both are done.
+  const bool behind = kPart == kRest && p.behind;
+  if (!behind) pdl_wait();
   pdl_launch_dependents();
   Plan plan;
   __shared__ int table0;   // the first page of a sequence that its rows attend over
@@ -252,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
       if (tid == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
       if (plan.idle) write_idle(p, D);
     }
+    if (behind) pdl_wait();
     return;
   }
   // this warp's head of the group, and its stream: pages stream, stream + streams, ... of a segment
@@ -710,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
     if (tid == 0) p.meta[blockIdx.x] = meta;
     if (plan.idle) write_idle(p, D);
   }
+  if (behind) pdl_wait();
 }
 
 // ---- combine ---------------------------------------------------------------------------

@@ -51,6 +51,7 @@ struct Params {
   // kv_attend_shared_q8 only: the tokens that all sequences begin with, and its passes' results
   const int32_t *prefix_table, *prefix_length;
   int prefix_pages;
+  bool behind;          // few rows: launched behind the shared tokens' pass, on which nothing here depends
   float* dense;         // [n_rows][Hq][D + 4]: like `partial`, of a unit that one CTA held
   int2* found;          // [n_rows][n_grp], few rows: by a sequence's first row the CTA that begins a unit, and its
                         // parts (0: it is dense)

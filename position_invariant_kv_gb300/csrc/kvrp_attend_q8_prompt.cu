@@ -282,9 +282,35 @@ struct Shared {
   int nan_at[kWarpsRows][kMostFeatures];   // then: the first token with one, by features, a softmax warp's unit
   uint32_t tmem;
 };
+// The same where all units cost the same (the shared tokens): by arithmetic, in one thread.
+template <int N>
+__device__ __forceinline__ bool find_even_share(const Params& p, Shared& sh) {
+  if (threadIdx.x == 0) {
+    Unit u;
+    u.j0 = u.j1 = 0;
+    u.left = u.spent = 0;
+    if (load_seq<kShared>(p, 0, u)) {
+      u.s = 0;
+      u.n_kv = tiles_of<N, kShared>(0, p.g, u.rows, u.len);
+      const int cost = u.n_kv + kUnitTiles;
+      const int64_t total = (int64_t)u.n_rt * p.Hkv * cost, n_cta = min((int64_t)p.n_cta, prompt_ctas(total));
+      if (blockIdx.x < n_cta) {
+        const int64_t a = total * blockIdx.x / n_cta, b = total * (blockIdx.x + 1) / n_cta, unit = a / cost;
+        u.rt = (int)(unit / p.Hkv);
+        u.h = (int)(unit - (int64_t)u.rt * p.Hkv);
+        u.left = b - a;
+        take(u, (int)(a - unit * cost));
+      }
+    }
+    sh.first = u;
+  }
+  __syncthreads();
+  return sh.first.j1 > sh.first.j0 || sh.first.left > sh.first.spent;
+}
 template <int N, Part kPart>
 __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = kPart == kShared ? 1 : p.seqs.n_seqs;
+  if constexpr (kPart == kShared) return find_even_share<N>(p, sh);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.seqs.n_seqs;
   int64_t mine = 0;
   for (int s = warp; s < n; s += kWarpsAll) mine += seq_cost<N, kPart>(p, s, blockIdx.x == 0) * p.Hkv;
   if (lane == 0) sh.cost[warp] = mine;
@@ -744,7 +770,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     };
     do {
       const bool begins = u.j0 == 0, ends = u.j1 == u.n_kv;
-      if (begins && !ends && tid == 0) {
+      if (kPart != kShared && begins && !ends && tid == 0) {
         // the CTA whose share holds the unit's last tile: the largest j with total j / n_cta below the unit's end
         const int64_t unit_end = sh.end - u.left - u.from + u.n_kv + kUnitTiles;
         meta = make_int4((int)((unit_end * sh.n_cta - 1) / sh.total) - (int)blockIdx.x + 1, u.h, u.rt, u.row0);

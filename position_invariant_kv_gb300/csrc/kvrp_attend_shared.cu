@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   };
   float m = -INFINITY, om = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kBatch = 8;   // parts in flight
+  constexpr int kBatch = 16;   // parts in flight
   for (int x0 = 0; x0 < n; x0 += kBatch) {
     float4 st[kBatch], v[kBatch];
 #pragma unroll
@@ -238,6 +238,7 @@ kvrp_status kv_attend_shared_q8(const void* q, int64_t q_stride, const kvrp_seqs
   p.found = reinterpret_cast<int2*>(base + at.found);
   p.partial = reinterpret_cast<float*>(base + at.partial);
   p.dense = reinterpret_cast<float*>(base + at.dense);
+  p.behind = few && launches > 0;
   if (few) attend_q8::set_few(p, sms, head_dim);
   if (e == cudaSuccess)
     e = few ? attend_q8::launch_few(p, head_dim, stream, attend_q8::kRest)
