@@ -518,6 +518,9 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     fewer_registers<L::kRegsMisc>();
     if (warp == 12) {
       // ---- TMA: a lane a page ---------------------------------------------------------------
+      // Table entries and scales of kAhead tiles are read at a time, a lane a page, and those of the next kAhead
+      // meanwhile: two dependent trips to memory a tile were what every tile took (1.33 us, whatever its rows).
+      constexpr int kAhead = 32 / L::kP;
       int n = 0, nk = 0, nv = 0;   // the tile, K and V tiles issued
       bool ok = true;
       do {
@@ -527,28 +530,44 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         // it is too far from the first one for the accumulator that began relative to that.
         float vref = 0.f, first_vref = 0.f;
         bool apart = false;
+        // page j kP + lane of the batch that begins with tile j: its place in the pools, past them where there is none
+        const auto entry = [&](int j) {
+          const int pg = j * L::kP + lane;
+          if (lane >= kAhead * L::kP || pg >= min(pages, u.j1 * L::kP)) return -1;
+          const int e = table[pg];
+          if (e >= 0 && e < p.seqs.num_pages) return e;
+          flag(p.status, KVRP_DEV_BAD_PAGE);
+          return p.seqs.num_pages;
+        };
+        const auto scale = [&](const float* scales, int e, float none) {
+          return e < 0 ? 0.f : e < p.seqs.num_pages ? scales[(int64_t)e * p.Hkv + u.h] : none;
+        };
+        int b_page = -1, next_page = entry(u.j0), at = kAhead - 1;
+        float b_k = 0.f, b_v = 0.f, next_k = scale(p.k_scale, next_page, 0.f), next_v = scale(p.v_scale, next_page, kZeroBlock);
         for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
           const int ks = n % L::kKst, vs = n % L::kVst, slot = n % kScaleSlots;
-          const int pg = j * L::kP + lane;
-          const bool mine = lane < L::kP && pg < pages;
-          int page = p.seqs.num_pages;   // past the pool: the box reads zeros
-          float fk = 0.f, fv = mine ? kZeroBlock : 0.f;
-          if (mine) {
-            const int e = table[pg];
-            if (e >= 0 && e < p.seqs.num_pages) {
-              page = e;
-              fk = p.k_scale[(int64_t)e * p.Hkv + u.h];
-              fv = p.v_scale[(int64_t)e * p.Hkv + u.h];
-            } else {
-              flag(p.status, KVRP_DEV_BAD_PAGE);
-            }
+          if (++at == kAhead) {
+            at = 0;
+            b_page = next_page;
+            b_k = next_k;
+            b_v = next_v;
+            next_page = entry(j + kAhead);
+          } else if (at == 1) {
+            next_k = scale(p.k_scale, next_page, 0.f);
+            next_v = scale(p.v_scale, next_page, kZeroBlock);
           }
+          const int from = (at * L::kP + lane) & 31;
+          const int page = __shfl_sync(0xffffffffu, b_page, from);
+          const bool mine = lane < L::kP && page >= 0;   // a page past the pool: the box reads zeros
+          const float fk = __shfl_sync(0xffffffffu, b_k, from);
+          float fv = __shfl_sync(0xffffffffu, b_v, from);
+          if (!mine) fv = 0.f;
           ok = wait(kempty(ks), ((n / L::kKst) & 1) ^ 1);   // the first pass finds the stage free
           if (!ok) break;
           // Both issuers have done tile n - 4's scores, so both softmax groups have read tile n - 5's, and
           // V's warps are past tile n - 5: nobody needs slot n - 8 any more.
           if (lane < kMostPages) {
-            sh.ks[slot][lane] = fk;
+            sh.ks[slot][lane] = mine ? fk : 0.f;
             sh.vs[slot][lane] = fv;
           }
           // positive numbers are in the order of their bits
