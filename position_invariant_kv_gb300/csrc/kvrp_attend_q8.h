@@ -71,6 +71,52 @@ __host__ __device__ constexpr int prompt_tokens(int head_dim) { return head_dim 
 constexpr int kUnitTiles = 6;   // 4: 222 us for 6 questions of 37 to 900 rows, 6: 220 (215 with a later step)
 // The fewest CTAs' worth of a batch: a share is at least a unit's tiles and two more.
 __host__ __device__ constexpr int64_t prompt_ctas(int64_t total) { return (total + kUnitTiles + 1) / (kUnitTiles + 2); }
+// The units of the shared tokens' pass, tiles of kPromptRows (row, query head) pairs for each KV head, all over the same
+// tokens, and the CTAs that take them.  In general the costs of all units are cut into equal shares, of which some end
+// inside one unit and go on in the next, beginning it as well.  Where the tokens are so few that such shares are
+// mostly beginnings, every unit is cut into `parts`, one a CTA, of three tiles or more, on two thirds of the SMs at most:
+// the others begin the own tokens' pass, and more parts take the join longer (5 sequences over 4000 shared
+// tokens and 300 own, 8 heads: 21.8 us, with all SMs 25.0, in shares 23.9; 3 over 1008, 4 KV heads: 17.9, in shares 21.5).
+// Where parts would not be a third shorter than shares, shares are faster (4 over 16000: 25.3 us, in parts 29.6).
+struct EvenUnits {
+  int n_kv;             // token tiles of a unit
+  int parts;            // 0: shares
+  int64_t units, cost, total;   // shares: a unit's cost, all units'
+  int64_t n_cta;
+  __host__ __device__ EvenUnits(int64_t pairs, int heads, int tokens, int head_dim, int most_cta) {
+    const int n = prompt_tokens(head_dim);
+    n_kv = (tokens + n - 1) / n;
+    units = n_kv == 0 ? 0 : (pairs + kPromptRows - 1) / kPromptRows * heads;
+    cost = n_kv + kUnitTiles;
+    total = units * cost;
+    parts = 0;
+    n_cta = 0;
+    if (units == 0) return;
+    n_cta = prompt_ctas(total) < most_cta ? prompt_ctas(total) : most_cta;
+    if (units <= most_cta && total <= 12 * n_cta) {   // 32 bits from here on
+      const int places = most_cta * 2 / 3 / (int)units, three = (n_kv + 2) / 3, k = places < three ? places : three;
+      if (k > 0 && 3 * ((n_kv + k - 1) / k) <= 2 * (((int)total + (int)n_cta - 1) / (int)n_cta)) {
+        parts = k;
+        n_cta = units * k;
+      }
+    }
+  }
+  __host__ __device__ static int64_t div(int64_t a, int64_t b) {   // of numbers that are not negative
+    return (uint64_t)(a | b) < (1ull << 31) ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+  }
+  __host__ __device__ int part_begin(int i) const { return (int)div((int64_t)n_kv * i, parts); }
+  __host__ __device__ int64_t share(int i) const { return div(total * i, n_cta); }   // where CTA i's costs begin
+  // The first CTA with tiles of a unit, and how many have some.
+  __host__ __device__ void find(int64_t unit, int& first, int& n) const {
+    if (parts) {
+      first = (int)unit * parts;
+      n = parts;
+    } else {   // the CTA whose costs hold x is the largest c with total c / n_cta not above it
+      first = (int)div((unit * cost + kUnitTiles + 1) * n_cta - 1, total);
+      n = (int)div((unit + 1) * cost * n_cta - 1, total) - first + 1;
+    }
+  }
+};
 cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap, const Params& p, int head_dim, cudaStream_t stream,
                           Part part = kAll);
 // The kernel for few rows, p.n_cta blocks.

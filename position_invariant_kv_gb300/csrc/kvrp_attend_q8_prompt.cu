@@ -186,6 +186,11 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
+// 16 bytes to shared memory, asynchronously (zeros for none), and until all of this thread's have landed.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Two f16 values to e4m3 (NaN stays NaN; nothing here is above 448).
 __device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t v) {
   uint16_t r;
@@ -282,34 +287,42 @@ struct Shared {
   int nan_at[kWarpsRows][kMostFeatures];   // then: the first token with one, by features, a softmax warp's unit
   uint32_t tmem;
 };
-// The same where all units cost the same (the shared tokens): by arithmetic, in one thread.
-template <int N>
+// The shared tokens' pass: by arithmetic, in one thread.
+template <int D>
 __device__ __forceinline__ bool find_even_share(const Params& p, Shared& sh) {
   if (threadIdx.x == 0) {
     Unit u;
     u.j0 = u.j1 = 0;
-    u.left = u.spent = 0;
     if (load_seq<kShared>(p, 0, u)) {
-      u.s = 0;
-      u.n_kv = tiles_of<N, kShared>(0, p.g, u.rows, u.len);
-      const int cost = u.n_kv + kUnitTiles;
-      const int64_t total = (int64_t)u.n_rt * p.Hkv * cost, n_cta = min((int64_t)p.n_cta, prompt_ctas(total));
-      if (blockIdx.x < n_cta) {
-        const int64_t a = total * blockIdx.x / n_cta, b = total * (blockIdx.x + 1) / n_cta, unit = a / cost;
-        u.rt = (int)(unit / p.Hkv);
-        u.h = (int)(unit - (int64_t)u.rt * p.Hkv);
-        u.left = b - a;
-        take(u, (int)(a - unit * cost));
+      const EvenUnits e((int64_t)u.rows * p.g, p.Hkv, u.len, D, p.n_cta);
+      if (blockIdx.x < e.n_cta) {
+        int unit;
+        u.s = 0;
+        u.n_kv = e.n_kv;
+        if (e.parts) {
+          unit = blockIdx.x / e.parts;
+          const int i = blockIdx.x - unit * e.parts;
+          u.j0 = e.part_begin(i);
+          u.j1 = e.part_begin(i + 1);
+          u.left = u.spent = 0;
+        } else {
+          const int64_t a = e.share(blockIdx.x);
+          unit = (int)e.div(a, e.cost);
+          u.left = e.share(blockIdx.x + 1) - a;
+          take(u, (int)(a - unit * e.cost));
+        }
+        u.rt = unit / p.Hkv;
+        u.h = unit - u.rt * p.Hkv;
       }
     }
     sh.first = u;
   }
   __syncthreads();
-  return sh.first.j1 > sh.first.j0 || sh.first.left > sh.first.spent;
+  return sh.first.j1 > sh.first.j0;   // a share that goes on behind its first unit has that one's last tile
 }
 template <int N, Part kPart>
 __device__ __forceinline__ bool find_share(const Params& p, Shared& sh) {
-  if constexpr (kPart == kShared) return find_even_share<N>(p, sh);
+  if constexpr (kPart == kShared) return find_even_share<N == prompt_tokens(128) ? 128 : 64>(p, sh);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.seqs.n_seqs;
   int64_t mine = 0;
   for (int s = warp; s < n; s += kWarpsAll) mine += seq_cost<N, kPart>(p, s, blockIdx.x == 0) * p.Hkv;
@@ -806,29 +819,32 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
       const int first_limit = kPart == kShared ? u.len : u.len - u.rows + over_group(p, u.rt * kPromptRows + t * kRows) + 1;
       const uint32_t out_row = live ? (uint32_t)(u.row0 + tok) * p.Hq + u.h * p.g + (col - tok * p.g) : kNoRow;
       // ---- q / 2^(e - 7) = high + low, both e4m3 -------------------------------------------------
-      // A warp its 32 rows, D / 16 lanes a row, so that a load takes whole rows (a row a thread took
+      // A warp its 32 rows, D / 16 lanes a row, so that a copy takes whole rows (a row a thread took
       // 4 us of load instructions).  The scores of the unit before have all been computed.
       float c = 0.f;   // scores times this are x, the exponent in base 2
       {
         constexpr int kLanes = D / 16, kStep = 32 / kLanes, kSteps = 32 / kStep;
         const int first = u.rt * kPromptRows + t * kRows + (warp & 3) * 32, x = lane % kLanes;
         const int cols = u.rows * p.g;
-        uint4 v[kSteps][2];
-#pragma unroll
+        // The rows' 16-byte pieces go to shared memory as they are, each lane's two to the places of its high and
+        // its low part: loops of few instructions, as all of them come from memory when a kernel begins (with eight
+        // rows' loads and conversions written out a unit took 2.5 us more to begin).
+#pragma unroll 2
         for (int i = 0; i < kSteps; ++i) {
-          const int rc = first + i * kStep + lane / kLanes;
-          v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
-          if (rc < cols) {
-            const int tk = over_group(p, rc);
-            const uint4* at = reinterpret_cast<const uint4*>(p.q + (u.row0 + tk) * p.q_stride + (u.h * p.g + rc - tk * p.g) * D) + 2 * x;
-            v[i][0] = at[0];
-            v[i][1] = at[1];
-          }
+          const int r = i * kStep + lane / kLanes, rc = first + r;
+          const int tk = over_group(p, min(rc, cols - 1));
+          const uint16_t* at = p.q + (u.row0 + tk) * p.q_stride + (u.h * p.g + min(rc, cols - 1) - tk * p.g) * D + 16 * x;
+          const uint32_t to = row_chunk(0, (warp & 3) * 32 + r, x), bytes = rc < cols ? 16 : 0;
+          copy16(to, at, bytes);
+          copy16(to + L::kQ, at + 8, bytes);
         }
-#pragma unroll
+        copies_wait_all();
+#pragma unroll 2
         for (int i = 0; i < kSteps; ++i) {
-          const uint4 v0 = v[i][0], v1 = v[i][1];
-          const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+          const uint32_t at = row_chunk(0, (warp & 3) * 32 + i * kStep + lane / kLanes, x);
+          uint32_t w[8];
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "r"(at + L::kQ) : "memory");
           uint32_t most = 0;   // the row's largest magnitude, as bf16 bits
 #pragma unroll
           for (int k = 0; k < 8; ++k) most = __vmaxu2(most, w[k] & 0x7fff7fffu);
@@ -853,7 +869,6 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
             hi[k] = (uint32_t)h8[0] | ((uint32_t)h8[1] << 16);
             lo[k] = (uint32_t)l8[0] | ((uint32_t)l8[1] << 16);
           }
-          const uint32_t at = row_chunk(0, (warp & 3) * 32 + i * kStep + lane / kLanes, x);
           asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
           asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::kQ), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
           const float mine = __shfl_sync(0xffffffffu, p.scale * __uint_as_float((uint32_t)(127 - 7 + e) << 23), (lane % kStep) * kLanes);

@@ -48,16 +48,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const Params& p = j.p;
   const int chunks = (p.Hq + kItems - 1) / kItems;
   const int row = blockIdx.x / chunks, head = blockIdx.x % chunks * kItems + threadIdx.x / kLanes, f = threadIdx.x % kLanes;
-  pdl_wait();
+  // What is looked up first was there before this call: the passes' blocks had all waited for it, or were let in by
+  // blocks that had, when they let this kernel's in.
   pdl_launch_dependents();
   const View view = load_view(p);
-  if (view.tokens < 0) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) flag(p.status, KVRP_DEV_BAD_LENGTH);
-    return;
-  }
   int s = row;   // the row's sequence: the last whose first row is not behind it
-  if (p.seqs.row_start) {
-    if (row < view.first || row >= view.end) return;
+  if (p.seqs.row_start && view.tokens >= 0) {
     int lo = 0, hi = p.seqs.n_seqs;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -66,33 +62,31 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     }
     s = lo;
   }
-  int row0, rows, len;
-  const bool ok = part_sequence<kRest>(p, s, row0, rows, len);
-  if (head >= p.Hq) return;
+  int row0 = 0, rows = 0, len = 0;
+  const bool ok = view.tokens >= 0 && row >= view.first && row < view.end && part_sequence<kRest>(p, s, row0, rows, len);
   const int64_t at = (int64_t)row * p.Hq + head;
-  if (ok && len == 0) {   // an idle place of the batch
+  const bool idle = ok && len == 0;
+  const int h = head / p.g, jq = head - h * p.g;
+  // the shared tokens' parts
+  int first = 0, n_shared = 0;
+  int64_t y = 0;
+  if (ok && !idle && view.tokens > 0) {
+    const int64_t col = (int64_t)(row - view.first) * p.g + jq;
+    const EvenUnits e((int64_t)(view.end - view.first) * p.g, p.Hkv, view.tokens, D, j.shared_ctas);
+    e.find(col / kPromptRows * p.Hkv + h, first, n_shared);
+    y = col % kPromptRows;
+  }
+  pdl_wait();
+  if (view.tokens < 0 && blockIdx.x == 0 && threadIdx.x == 0) flag(p.status, KVRP_DEV_BAD_LENGTH);
+  if (!ok || head >= p.Hq) return;   // bad sequences are flagged by the own tokens' pass
+  if (idle) {   // a place of the batch that is free
     const int end = p.seqs.row_start ? p.seqs.row_start[s + 1] : s + 1;
     if (row < row0 || row >= end) return;
     *reinterpret_cast<uint2*>(p.out + at * D + 4 * f) = make_uint2(0, 0);
     if (p.lse && f == 0) p.lse[at] = -INFINITY;
     return;
   }
-  if (!ok || rows > p.max_rows || row < row0 || row >= row0 + rows) return;   // flagged by the second pass
-
-  const int h = head / p.g, jq = head - h * p.g;
-  // the shared tokens' parts
-  int first = 0, n_shared = 0;
-  int64_t y = 0;
-  if (view.tokens > 0) {
-    const int64_t col = (int64_t)(row - view.first) * p.g + jq, cost = (view.tokens + N - 1) / N + kUnitTiles;
-    const int64_t tiles = ((int64_t)(view.end - view.first) * p.g + kPromptRows - 1) / kPromptRows;
-    const int64_t unit = col / kPromptRows * p.Hkv + h, total = tiles * p.Hkv * cost;
-    const int64_t n_cta = min((int64_t)j.shared_ctas, prompt_ctas(total));
-    // the CTA of cost x is the largest c with total c / n_cta not above it
-    first = (int)(((unit * cost + kUnitTiles + 1) * n_cta - 1) / total);
-    n_shared = (int)(((unit + 1) * cost * n_cta - 1) / total) - first + 1;
-    y = col % kPromptRows;
-  }
+  if (rows > p.max_rows || row < row0 || row >= row0 + rows) return;
   // the own tokens'
   int2 own = make_int2(0, 0);
   int64_t own_y = 0;
