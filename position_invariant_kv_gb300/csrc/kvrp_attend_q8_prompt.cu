@@ -531,8 +531,9 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
     fewer_registers<L::kRegsMisc>();
     if (warp == 12) {
       // ---- TMA: a lane a page ---------------------------------------------------------------
-      // Table entries and scales of kAhead tiles are read at a time, a lane a page, and those of the next kAhead
-      // meanwhile: two dependent trips to memory a tile were what every tile took (1.33 us, whatever its rows).
+      // The parts of kv_attend_shared_q8 read the table entries and scales of kAhead tiles at a time, a lane a page,
+      // and those of the next kAhead meanwhile: with two dependent trips to memory a tile, a tile of few rows took
+      // 1.33 us instead of 1.19.  A prompt's tiles take longer anyway (688 us this way instead of 684).
       constexpr int kAhead = 32 / L::kP;
       int n = 0, nk = 0, nv = 0;   // the tile, K and V tiles issued
       bool ok = true;
@@ -555,32 +556,56 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         const auto scale = [&](const float* scales, int e, float none) {
           return e < 0 ? 0.f : e < p.seqs.num_pages ? scales[(int64_t)e * p.Hkv + u.h] : none;
         };
-        int b_page = -1, next_page = entry(u.j0), at = kAhead - 1;
-        float b_k = 0.f, b_v = 0.f, next_k = scale(p.k_scale, next_page, 0.f), next_v = scale(p.v_scale, next_page, kZeroBlock);
+        int b_page = -1, next_page = -1, at = kAhead - 1;
+        float b_k = 0.f, b_v = 0.f, next_k = 0.f, next_v = 0.f;
+        if constexpr (kPart != kAll) {
+          next_page = entry(u.j0);
+          next_k = scale(p.k_scale, next_page, 0.f);
+          next_v = scale(p.v_scale, next_page, kZeroBlock);
+        }
         for (int j = u.j0; j < u.j1 && ok; ++j, ++n) {
           const int ks = n % L::kKst, vs = n % L::kVst, slot = n % kScaleSlots;
-          if (++at == kAhead) {
-            at = 0;
-            b_page = next_page;
-            b_k = next_k;
-            b_v = next_v;
-            next_page = entry(j + kAhead);
-          } else if (at == 1) {
-            next_k = scale(p.k_scale, next_page, 0.f);
-            next_v = scale(p.v_scale, next_page, kZeroBlock);
+          bool mine;   // this lane has a page of the tile; one past the pool: the box reads zeros
+          int page = p.seqs.num_pages;
+          float fk = 0.f, fv = 0.f;
+          if constexpr (kPart == kAll) {
+            const int pg = j * L::kP + lane;
+            mine = lane < L::kP && pg < pages;
+            fv = mine ? kZeroBlock : 0.f;
+            if (mine) {
+              const int e = table[pg];
+              if (e >= 0 && e < p.seqs.num_pages) {
+                page = e;
+                fk = p.k_scale[(int64_t)e * p.Hkv + u.h];
+                fv = p.v_scale[(int64_t)e * p.Hkv + u.h];
+              } else {
+                flag(p.status, KVRP_DEV_BAD_PAGE);
+              }
+            }
+          } else {
+            if (++at == kAhead) {
+              at = 0;
+              b_page = next_page;
+              b_k = next_k;
+              b_v = next_v;
+              next_page = entry(j + kAhead);
+            } else if (at == 1) {
+              next_k = scale(p.k_scale, next_page, 0.f);
+              next_v = scale(p.v_scale, next_page, kZeroBlock);
+            }
+            const int from = (at * L::kP + lane) & 31;
+            page = __shfl_sync(0xffffffffu, b_page, from);
+            fk = __shfl_sync(0xffffffffu, b_k, from);
+            fv = __shfl_sync(0xffffffffu, b_v, from);
+            mine = lane < L::kP && page >= 0;
+            if (!mine) fk = fv = 0.f;
           }
-          const int from = (at * L::kP + lane) & 31;
-          const int page = __shfl_sync(0xffffffffu, b_page, from);
-          const bool mine = lane < L::kP && page >= 0;   // a page past the pool: the box reads zeros
-          const float fk = __shfl_sync(0xffffffffu, b_k, from);
-          float fv = __shfl_sync(0xffffffffu, b_v, from);
-          if (!mine) fv = 0.f;
           ok = wait(kempty(ks), ((n / L::kKst) & 1) ^ 1);   // the first pass finds the stage free
           if (!ok) break;
           // Both issuers have done tile n - 4's scores, so both softmax groups have read tile n - 5's, and
           // V's warps are past tile n - 5: nobody needs slot n - 8 any more.
           if (lane < kMostPages) {
-            sh.ks[slot][lane] = mine ? fk : 0.f;
+            sh.ks[slot][lane] = fk;
             sh.vs[slot][lane] = fv;
           }
           // positive numbers are in the order of their bits
@@ -826,25 +851,8 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
         constexpr int kLanes = D / 16, kStep = 32 / kLanes, kSteps = 32 / kStep;
         const int first = u.rt * kPromptRows + t * kRows + (warp & 3) * 32, x = lane % kLanes;
         const int cols = u.rows * p.g;
-        // The rows' 16-byte pieces go to shared memory as they are, each lane's two to the places of its high and
-        // its low part: loops of few instructions, as all of them come from memory when a kernel begins (with eight
-        // rows' loads and conversions written out a unit took 2.5 us more to begin).
-#pragma unroll 2
-        for (int i = 0; i < kSteps; ++i) {
-          const int r = i * kStep + lane / kLanes, rc = first + r;
-          const int tk = over_group(p, min(rc, cols - 1));
-          const uint16_t* at = p.q + (u.row0 + tk) * p.q_stride + (u.h * p.g + min(rc, cols - 1) - tk * p.g) * D + 16 * x;
-          const uint32_t to = row_chunk(0, (warp & 3) * 32 + r, x), bytes = rc < cols ? 16 : 0;
-          copy16(to, at, bytes);
-          copy16(to + L::kQ, at + 8, bytes);
-        }
-        copies_wait_all();
-#pragma unroll 2
-        for (int i = 0; i < kSteps; ++i) {
-          const uint32_t at = row_chunk(0, (warp & 3) * 32 + i * kStep + lane / kLanes, x);
-          uint32_t w[8];
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "r"(at + L::kQ) : "memory");
+        // A row's 16 values as high and low parts: into their places; and what its scores are multiplied with.
+        const auto convert = [&](const uint32_t (&w)[8], uint32_t at) {
           uint32_t most = 0;   // the row's largest magnitude, as bf16 bits
 #pragma unroll
           for (int k = 0; k < 8; ++k) most = __vmaxu2(most, w[k] & 0x7fff7fffu);
@@ -871,8 +879,52 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
           }
           asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
           asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + L::kQ), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
-          const float mine = __shfl_sync(0xffffffffu, p.scale * __uint_as_float((uint32_t)(127 - 7 + e) << 23), (lane % kStep) * kLanes);
-          if (i == lane / kStep) c = mine;
+          return __shfl_sync(0xffffffffu, p.scale * __uint_as_float((uint32_t)(127 - 7 + e) << 23), (lane % kStep) * kLanes);
+        };
+        if constexpr (kPart == kAll) {
+          uint4 v[kSteps][2];
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const int rc = first + i * kStep + lane / kLanes;
+            v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+            if (rc < cols) {
+              const int tk = over_group(p, rc);
+              const uint4* at = reinterpret_cast<const uint4*>(p.q + (u.row0 + tk) * p.q_stride + (u.h * p.g + rc - tk * p.g) * D) + 2 * x;
+              v[i][0] = at[0];
+              v[i][1] = at[1];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const uint4 v0 = v[i][0], v1 = v[i][1];
+            const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            const float mine = convert(w, row_chunk(0, (warp & 3) * 32 + i * kStep + lane / kLanes, x));
+            if (i == lane / kStep) c = mine;
+          }
+        } else {
+          // The rows' 16-byte pieces go to shared memory as they are, each lane's two to the places of its high and
+          // its low part, and loops of few instructions convert them: where a CTA has one unit or two its instructions
+          // come from memory too (16 x 5 rows over 65536 shared tokens: 135 us, written out as above 142; prompts,
+          // whose CTAs go through many units, take 237 us instead of 213 this way).
+#pragma unroll 2
+          for (int i = 0; i < kSteps; ++i) {
+            const int r = i * kStep + lane / kLanes, rc = first + r;
+            const int tk = over_group(p, min(rc, cols - 1));
+            const uint16_t* at = p.q + (u.row0 + tk) * p.q_stride + (u.h * p.g + min(rc, cols - 1) - tk * p.g) * D + 16 * x;
+            const uint32_t to = row_chunk(0, (warp & 3) * 32 + r, x), bytes = rc < cols ? 16 : 0;
+            copy16(to, at, bytes);
+            copy16(to + L::kQ, at + 8, bytes);
+          }
+          copies_wait_all();
+#pragma unroll 2
+          for (int i = 0; i < kSteps; ++i) {
+            const uint32_t at = row_chunk(0, (warp & 3) * 32 + i * kStep + lane / kLanes, x);
+            uint32_t w[8];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "r"(at + L::kQ) : "memory");
+            const float mine = convert(w, at);
+            if (i == lane / kStep) c = mine;
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(qfull(t));
