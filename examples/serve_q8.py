@@ -6,11 +6,15 @@ Two chunks that were cached on their own are relocated behind each other into th
 bf16 cache (kv_relocate_batch), moved into the 8-bit cache (kv_pack_q8), and two sequences
 go on over them: a question's rows are normed, rotated and appended (kv_append_q8) and
 attend over chunks and question (kv_attend_q8); then tokens are decoded one at a time from
-a captured CUDA graph that follows the lengths on the device.  Every attention output is
-compared with the fp32 evaluation over the same 8-bit cache.
+a captured CUDA graph that follows the lengths on the device.  Last, a batch of users goes on
+behind the first sequence's chunks, which all of them share: a step's tables (kv_step_tables),
+appended rows, attention that reads the shared pages once (kv_attend_shared_q8) and drafts
+verified against the target's probabilities (kv_verify_drafts) are one graph, replayed while
+sequences grow by what was accepted.  Every attention output is compared with the fp32
+evaluation over the same 8-bit cache.
 
-The queries, keys and values of new rows are random: they stand in for a model's
-projections.  Needs a GB300.
+The queries, keys and values of new rows are random, and so are probabilities and drafts: they
+stand in for a model's.  Needs a GB300.
 """
 from __future__ import annotations
 
@@ -25,6 +29,7 @@ import position_invariant_kv_gb300 as kvrp
 
 HQ, HKV, D, THETA = 28, 4, 128, 1e6
 CHUNK, QUESTION, DECODE, SEQS = 500, 37, 20, 2
+USERS, DRAFTS, STEPS, VOCAB = 5, 3, 8, 3001
 ROW = HKV * D
 SAME = dict(n_q_heads=HQ, n_kv_heads=HKV, head_dim=D)
 
@@ -47,8 +52,11 @@ def main() -> None:
     torch.manual_seed(7)
     bf = dict(dtype=torch.bfloat16, device="cuda")
     pages_each = -(-(2 * CHUNK + QUESTION + DECODE) // 16)
-    pages = SEQS * pages_each + 3
-    tables = torch.randperm(pages, device="cuda")[: SEQS * pages_each].to(torch.int32).view(SEQS, pages_each).contiguous()
+    users_each = -(-(QUESTION + (STEPS + 1) * (DRAFTS + 1)) // 16) + 1     # own pages of a user behind the shared chunks
+    pages = SEQS * pages_each + USERS * users_each + 3
+    order = torch.randperm(pages, device="cuda").to(torch.int32)
+    tables = order[: SEQS * pages_each].view(SEQS, pages_each).contiguous()
+    free = order[SEQS * pages_each:]
     status = i32([0])
 
     # 1. the chunks of both sequences, relocated into the bf16 pages of the layer
@@ -116,6 +124,78 @@ def main() -> None:
         graph.replay()
         lens = [x + 1 for x in lens]
     check(f"{DECODE} decoded tokens from a graph", q, out, lens, [1] * SEQS)
+
+    # 5. users behind the chunks of sequence 0, whose full pages they share; free pages come from a ring
+    shared = 2 * CHUNK // 16 * 16
+    prefix = kvrp.Prefix(block_table=tables[0][: shared // 16].contiguous(), length=i32([2 * CHUNK]))
+    stride = shared // 16 + users_each
+    d_tables = torch.zeros(USERS, stride, dtype=torch.int32, device="cuda")
+    d_lens, d_starts = i32([0] * USERS), i32([0] * (USERS + 1))
+    kept, new, held = i32([shared] * USERS), i32([QUESTION - 2 * u for u in range(USERS)]), i32([0] * USERS)
+    ring = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    ring[: free.numel()] = free
+    ring_state = i32([0, free.numel()])
+
+    def user_step(n, most):
+        """Buffers of n rows, at most `most` a user, and the calls of a step over them."""
+        seqs = kvrp.Seqs(seq_lens=d_lens, block_tables=d_tables, num_pages=pages, n_rows=n, row_start=d_starts, max_rows=most)
+        workspace = torch.empty(kvrp.kv_attend_shared_q8_workspace_size(HQ, HKV, D, most, n), dtype=torch.uint8, device="cuda")
+        qkv, q, out = torch.empty(n, HQ + 2 * HKV, D, **bf), torch.empty(n, HQ, D, **bf), torch.empty(n, HQ, D, **bf)
+        positions = torch.zeros(n, dtype=torch.int32, device="cuda")
+
+        def run():
+            kvrp.kv_step_tables(kept, new, seqs, held_pages=held, free_pages=ring, free_state=ring_state, prefix=prefix,
+                                positions=positions, d_status=status)
+            kvrp.kv_append_q8(qkv[:, :HQ], qkv[:, HQ:HQ + HKV], qkv[:, HQ + HKV:], seqs, **SAME, rope_theta=THETA, q_out=q,
+                              q_norm=q_norm, k_norm=k_norm, q_stride=qkv.stride(0), k_stride=qkv.stride(0),
+                              v_stride=qkv.stride(0), positions=positions, d_status=status, **cache)
+            kvrp.kv_attend_shared_q8(q, seqs, prefix, **SAME, softmax_scale=D ** -0.5, out=out, workspace=workspace,
+                                     d_status=status, **cache)
+        return seqs, qkv, q, out, run
+
+    def check_users(what, q, out):
+        torch.cuda.synchronize()
+        starts, lens, worst = d_starts.tolist(), d_lens.tolist(), 0.0
+        for u in range(USERS):
+            a, b = starts[u], starts[u + 1]
+            ref = plain_attention(q[a:b], lens[u], b - a, d_tables[u][: -(-lens[u] // 16)], k_pool, k_scale, v_pool, v_scale)
+            worst = max(worst, ((out[a:b].float() - ref).norm() / ref.norm()).item())
+        assert int(status) == 0 and worst < 5e-3, (what, int(status), worst)
+        print(f"{what}: relative difference to the plain evaluation {worst:.1e}")
+
+    n = int(new.sum())
+    _, qkv, q, out, run = user_step(n, QUESTION)
+    qkv.normal_()
+    run()
+    check_users(f"{USERS} questions behind shared chunks", q, out)
+
+    # a token and its drafts for each user: tables, append, attention and verification in one graph
+    rows = DRAFTS + 1
+    kept.copy_(d_lens)
+    new.fill_(rows)
+    seqs, qkv, q, out, run = user_step(USERS * rows, rows)
+    target, draft = (torch.empty(USERS * rows, VOCAB, device="cuda") for _ in range(2))
+    tokens, out_tokens = (torch.zeros(USERS * rows, dtype=torch.int32, device="cuda") for _ in range(2))
+    u_accept, u_sample, accepted = torch.empty(USERS * rows, device="cuda"), torch.empty(USERS, device="cuda"), i32([0] * USERS)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+        kvrp.kv_verify_drafts(target, seqs, vocab=VOCAB, draft=draft, tokens=tokens, u_accept=u_accept, u_sample=u_sample,
+                              out_tokens=out_tokens, accepted=accepted, kept_lens=kept, d_status=status)
+    grown = kept.clone()
+    for _ in range(STEPS):
+        qkv.normal_()
+        logits = 2 * torch.randn_like(target)
+        target.copy_(torch.softmax(logits, -1))
+        draft.copy_(torch.softmax(logits + 0.5 * torch.randn_like(target), -1))
+        tokens[1:].copy_(torch.multinomial(draft, 1)[:-1, 0])      # drawn from row r, it is row r + 1's token
+        u_accept.uniform_()
+        u_sample.uniform_()
+        graph.replay()
+        grown += accepted + 1
+    check_users(f"{STEPS} steps of {DRAFTS} drafts", q, out)
+    assert torch.equal(grown, kept) and bool((out_tokens.view(USERS, rows)[:, 0] >= 0).all())
+    print(f"{STEPS} steps of {DRAFTS} drafts: {(kept - kept.min()).tolist()} tokens beyond the slowest user's")
 
 
 if __name__ == "__main__":

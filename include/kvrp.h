@@ -620,7 +620,10 @@ typedef struct kvrp_prefix {
  * the rows concerned stay as they were.  A prefix of no tokens, and batches of one
  * sequence, are fine.  Several prefixes: one call each, over the sequences of seqs'
  * arrays that share it (row_start may begin above 0).  Everything else, NaN, bad pages,
- * idle sequences and lse among it, is as in kv_attend_q8.
+ * idle sequences and lse among it, is as in kv_attend_q8.  The workspace holds partial
+ * results of both passes in fp32, 2 x (head_dim + 4) x 4 bytes for each (row, query
+ * head) beside a fixed part: for long prompts kv_attend_q8, whose work is the same there,
+ * needs less.
  */
 size_t kv_attend_shared_q8_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_rows,
                                           int32_t n_rows);
@@ -725,8 +728,9 @@ kvrp_status kv_verify_drafts(
  * kvrp_test_set_wait_limit -- for tests of the failure path only.  Sets the
  * limit, in SM clock cycles, of the relocation kernel's pipeline waits in the
  * plans built from now on by any thread, and of kv_attend_q8's kernel for many
- * rows in the calls from now on (0 restores the default of about one second).  With a limit of a few hundred cycles the waits give up almost at
- * once: the launch then ORs KVRP_DEV_TIMEOUT into *d_status, lets its copies
+ * rows (and kv_attend_shared_q8's) in the calls from now on (0 restores the default
+ * of about one second).  With a limit of a few hundred cycles the waits give up almost
+ * at once: the launch then ORs KVRP_DEV_TIMEOUT into *d_status, lets its copies
  * and tensor-core work drain, frees its TMEM and returns, leaving the output
  * incomplete.  It never hangs the GPU, whatever the limit.
  */
@@ -757,7 +761,8 @@ const char* kvrp_last_error(void);
  * attention call (kv_attend_*), append, pack, step tables or verification enqueued.  Relocation: the relocation
  * kernel, plus for a batch the small copy launches that carry its launch plan to
  * the device (31 KB of plan each).  Attention: the block and combine kernels (2;
- * the combine alone when no chunk has tokens).  Append, pack and draft verification: 1.
+ * the combine alone when no chunk has tokens); kv_attend_shared_q8 3, with many rows 4,
+ * one fewer where the prefix has no pages.  Append, pack and draft verification: 1.
  * Step tables: 1, or 2 for many rows.  0 when the
  * call returned an error or had nothing to move. */
 int32_t kvrp_last_launch_count(void);

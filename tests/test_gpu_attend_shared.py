@@ -298,3 +298,21 @@ def test_two_calls_at_once():
                 c.run()
     for c in cs:
         c.check()
+
+
+@pytest.mark.parametrize("case", [dict(prefix=3200, ctx=[300, 17], rows=[1, 1], hq=14, hkv=2, d=128),
+                                  dict(prefix=1600, ctx=[120], rows=[90], hq=8, hkv=2, d=64)])
+def test_short_wait_limit_reports_timeout_and_the_next_call_is_right(case):
+    """The passes' waits give up almost at once; the call returns, says so, and leaves nothing behind."""
+    c = Shared(**case)
+    try:
+        c.kvrp.kvrp_test_set_wait_limit(1)
+        c.run()
+    finally:
+        c.kvrp.kvrp_test_set_wait_limit(0)
+    torch.cuda.synchronize()                      # the launches return
+    assert int(c.status) & c.kvrp.KVRP_DEV_TIMEOUT
+    c.status.zero_()
+    c.run()
+    c.check()
+    assert int(c.status) == 0
