@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kThreadsAll, 1)
             copy16(to + L::kQ, at + 8, bytes);
           }
           copies_wait_all();
-#pragma unroll 2
+#pragma unroll 1
           for (int i = 0; i < kSteps; ++i) {
             const uint32_t at = row_chunk(0, (warp & 3) * 32 + i * kStep + lane / kLanes, x);
             uint32_t w[8];

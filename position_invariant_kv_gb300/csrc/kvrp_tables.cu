@@ -15,8 +15,8 @@
 // evenly however uneven the sequences are, each entry finding its sequence by bisection in shared
 // memory.  Small calls are one block, which fills and then moves the state on.  Large ones (prompts)
 // are two launches: blocks over the whole GPU, each scanning all sequences again (cheaper than a
-// third launch), fill tables, positions and slots; the second launch, one block, moves the state on,
-// which the first still reads.
+// third launch), fill tables, positions, slots and the ring's end; the second launch, one block, moves
+// lengths, pages held and the ring's state on, which the first still reads.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -53,6 +53,9 @@ struct Params {
 };
 
 // What a sequence of the block's 512 has to do.
+struct Counts {
+  int kept, fresh, held;
+};
 struct Plan {
   int length, need, held;
   int take0;          // pages that the sequences before it take
@@ -60,9 +63,10 @@ struct Plan {
 };
 struct Smem {
   int64_t rows[kWarps];
-  int takes[kWarps], entries[kWarps];
+  int takes[kWarps], entries[kWarps], gives[kWarps], taken[kWarps];
   int row_end[kThreads];    // of the batch's rows, at most n_rows
-  int entry_end[kThreads];  // of the block's new table entries, or of the pages given back
+  int entry_end[kThreads];  // of the block's new table entries,
+  int give_end[kThreads];   // of the pages given back
   Plan plan[kThreads];
   uint8_t served[kThreads];
 };
@@ -77,22 +81,20 @@ __device__ __forceinline__ T warp_scan(T v) {   // inclusive
   }
   return v;
 }
-// The first of n ascending ends that is above x (x is below the last).
-__device__ __forceinline__ int above(const int* end, int n, int x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (end[mid] > x) hi = mid;
-    else lo = mid + 1;
-  }
-  return lo;
+// The first of the block's ascending ends that is above x (x is below the last).
+__device__ __forceinline__ int above(const int* end, int x) {
+  int at = 0;
+#pragma unroll
+  for (int step = kThreads / 2; step > 0; step >>= 1)
+    if (end[at + step - 1] <= x) at += step;
+  return at;
 }
 __device__ __forceinline__ int ring_at(int head, int i, int size) {   // head, i < size
   const int64_t at = (int64_t)head + i;
   return (int)(at < size ? at : at - size);
 }
 
-// kFill: table entries, positions, slots.  kApply: row starts, lengths, pages held, the ring.
+// kFill: table entries, positions, slots, pages into the ring.  kApply: row starts, lengths, pages held, the ring's state.
 template <bool kFill, bool kApply>
 __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant__ Params p) {
   __shared__ Smem sh;
@@ -124,14 +126,13 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   int64_t rows0 = 0;           // of the sequences before the block's
   int64_t asked0 = 0;          // pages asked for by them
   int64_t took = 0, gave = 0;  // pages taken and given back by them
+  const auto counts = [&](int s) {
+    return s < p.n_seqs ? Counts{__ldcg(p.kept + s), __ldcg(p.fresh + s), __ldcg(p.held + s)} : Counts{0, 0, 0};
+  };
+  Counts next = counts(tid);
   for (int s0 = 0; s0 < p.n_seqs; s0 += kThreads) {
-    const int s = s0 + tid, n = min(kThreads, p.n_seqs - s0);
-    int kept = 0, fresh = 0, held = 0;
-    if (s < p.n_seqs) {
-      kept = __ldcg(p.kept + s);
-      fresh = __ldcg(p.fresh + s);
-      held = __ldcg(p.held + s);
-    }
+    const int s = s0 + tid, kept = next.kept, fresh = next.fresh, held = next.held;
+    next = counts(s + kThreads);   // those of the sequences after, meanwhile
     const int64_t rows = max(fresh, 0), length = (int64_t)kept + fresh;
     bool fine = usable && kept >= 0 && fresh >= 0 && held >= 0 && held <= p.stride && (held == 0 || held >= shared) &&
                 length <= q8::kMostTokens && length <= (int64_t)p.stride * kPage;
@@ -164,25 +165,35 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
       entry_total += sh.entries[w];
     }
     const bool served = fine && (takes == 0 || upto <= count);
+    const int gives = served && held > max(need, shared) ? held - max(need, shared) : 0, taken = served ? takes : 0;
+    const int give_sum = warp_scan(gives), taken_sum = warp_scan(taken);
+    if (lane == 31) sh.gives[warp] = give_sum, sh.taken[warp] = taken_sum;
     sh.row_end[tid] = (int)min(row_end, (int64_t)p.n_rows);
     sh.entry_end[tid] = entry_end;
     sh.plan[tid] = {(int)length, need, held, (int)min(upto - takes, (int64_t)size), from};
     sh.served[tid] = served;
     __syncthreads();
+    int give_end = give_sum, give_total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) give_end += sh.gives[w];
+      give_total += sh.gives[w];
+      took += sh.taken[w];
+    }
 
     if constexpr (kFill) {
-      for (int e = worker; e < entry_total; e += workers) {   // new table entries
-        const int x = above(sh.entry_end, n, e);
+      for (int64_t e = worker; e < entry_total; e += workers) {   // new table entries
+        const int x = above(sh.entry_end, (int)e);
         const Plan q = sh.plan[x];
         if (!sh.served[x]) continue;
-        const int at = q.need - (sh.entry_end[x] - e);
+        const int at = q.need - (sh.entry_end[x] - (int)e);
         const int page = page_of(at, q);
         if (page < 0 || page >= size) flag(p.status, KVRP_DEV_BAD_PAGE);
         p.table[(int64_t)(s0 + x) * p.stride + at] = page;
       }
       if (p.positions || p.slots) {
         for (int64_t r = block_row + worker; r < end_row; r += workers) {
-          const int x = above(sh.row_end, n, (int)r);
+          const int x = above(sh.row_end, (int)r);
           const Plan q = sh.plan[x];
           int at = 0;
           int64_t slot = -1;
@@ -196,32 +207,22 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
           if (p.slots) p.slots[r] = slot;
         }
       }
+      if (give_total > 0) {   // the ring's places behind the free pages: nobody reads them in this call
+        sh.give_end[tid] = give_end;
+        __syncthreads();
+        for (int64_t e = worker; e < give_total; e += workers) {
+          const int x = above(sh.give_end, (int)e);
+          const Plan q = sh.plan[x];
+          const int page = p.table[(int64_t)(s0 + x) * p.stride + q.held - (sh.give_end[x] - (int)e)];
+          if (page < 0 || page >= size) flag(p.status, KVRP_DEV_BAD_PAGE);
+          const int64_t place = gave + e;   // a ring that the pages would pass the end of loses them
+          if (place < size - count) p.ring[ring_at(head, count + (int)place, size)] = page;
+          else flag(p.status, KVRP_DEV_BAD_LENGTH);
+        }
+      }
     }
+    gave += give_total;
     if constexpr (kApply) {
-      const int gives = served && held > max(need, shared) ? held - max(need, shared) : 0, taken = served ? takes : 0;
-      const int give_sum = warp_scan(gives), taken_sum = warp_scan(taken);
-      __syncthreads();   // the entries' ends have been read
-      if (lane == 31) sh.entries[warp] = give_sum, sh.takes[warp] = taken_sum;
-      __syncthreads();
-      int give_end = give_sum, give_total = 0;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) give_end += sh.entries[w];
-        give_total += sh.entries[w];
-        took += sh.takes[w];
-      }
-      sh.entry_end[tid] = give_end;
-      __syncthreads();
-      for (int e = tid; e < give_total; e += kThreads) {   // pages given back
-        const int x = above(sh.entry_end, n, e);
-        const Plan q = sh.plan[x];
-        const int page = p.table[(int64_t)(s0 + x) * p.stride + q.held - (sh.entry_end[x] - e)];
-        if (page < 0 || page >= size) flag(p.status, KVRP_DEV_BAD_PAGE);
-        const int64_t place = gave + e;   // behind the free ones; a ring that they would pass the end of loses them
-        if (place < size - count) p.ring[ring_at(head, count + (int)place, size)] = page;
-        else flag(p.status, KVRP_DEV_BAD_LENGTH);
-      }
-      gave += give_total;
       if (s < p.n_seqs) {
         if (!fine) flag(p.status, KVRP_DEV_BAD_LENGTH);
         else if (!served) flag(p.status, KVRP_DEV_NO_PAGES);
