@@ -9,9 +9,9 @@ import pytest
 import torch
 
 from oracle.serve import attend_rows
-from serve_util import bf16_bits_to_f64, dev, f64, i32
+from serve_util import bf16_bits_to_f64, dev, f64, i32, round_to_bf16_bits
 from test_gpu_attend_q8 import Case
-from test_gpu_attend_q8_edges import send
+from test_gpu_attend_q8_edges import FLOOR, check, send
 
 pytestmark = pytest.mark.gpu
 
@@ -72,6 +72,8 @@ FEW = {
     "drafts_128": dict(prefix=1600, ctx=[14, 60, 0], rows=[2, 1, 0], hq=14, hkv=2, d=128),
     "any_scale": dict(prefix=128, ctx=[100, 33], rows=[1, 1], hq=8, hkv=2, d=128, one_each=True, pow2=False),
     "wide_value_scales": dict(prefix=400, ctx=[300, 10], rows=[1, 1], hq=8, hkv=2, d=128, one_each=True, v_spread=30),
+    "shares": dict(prefix=15008, ctx=[3, 40], rows=[1, 1], hq=21, hkv=3, d=128, one_each=True),
+    "shares_64": dict(prefix=9008, ctx=[5, 40], rows=[2, 1], hq=16, hkv=8, d=64),
     "idle": dict(prefix=80, ctx=[10, 20, 30], rows=[1] * 3, hq=8, hkv=2, d=128, one_each=True, idle=(1,)),
     "all_idle": dict(prefix=80, ctx=[10, 20], rows=[1, 1], hq=8, hkv=2, d=64, one_each=True, idle=(0, 1)),
 }
@@ -81,6 +83,7 @@ MANY = {
     "ragged": dict(prefix=96, ctx=[0, 130, 17, 50, 3], rows=[37, 1, 0, 64, 129], hq=14, hkv=2, d=128),
     "ragged_64": dict(prefix=512, ctx=[3, 100, 0], rows=[150, 2, 17], hq=8, hkv=4, d=64),
     "units": dict(prefix=16, ctx=[3, 9], rows=[300, 270], hq=16, hkv=16, d=64),
+    "more_units_than_sms": dict(prefix=160, ctx=[3, 9], rows=[300, 270], hq=64, hkv=64, d=64),
     "group_16": dict(prefix=64, ctx=[60, 0], rows=[21, 2], hq=32, hkv=2, d=128),
     "no_prefix": dict(prefix=0, ctx=[60, 0], rows=[21, 18], hq=8, hkv=2, d=128),
     "value_scales": dict(prefix=400, ctx=[40], rows=[30], hq=4, hkv=2, d=128, v_spread=30),
@@ -316,3 +319,62 @@ def test_short_wait_limit_reports_timeout_and_the_next_call_is_right(case):
     c.run()
     c.check()
     assert int(c.status) == 0
+
+
+SHAPES = {
+    "few_128": dict(prefix=320, ctx=[0, 14, 233], rows=[3, 4, 4], hq=4, hkv=2, d=128),
+    "few_64": dict(prefix=2000, ctx=[13, 70], rows=[2, 4], hq=16, hkv=4, d=64),
+    "many_128": dict(prefix=1600, ctx=[5, 90], rows=[41, 20], hq=7, hkv=1, d=128),
+    "many_64": dict(prefix=64, ctx=[0, 150], rows=[70, 30], hq=8, hkv=2, d=64),
+}
+each_shape = pytest.mark.parametrize("shape", SHAPES)
+
+
+@each_shape
+@pytest.mark.parametrize("size", [-42, -100])
+def test_tiny_queries(shape, size):
+    """Rows far below one, a row of zeros and one as it was (bars: test_gpu_attend_q8_edges.py)."""
+    c = Shared(**SHAPES[shape])
+    q = bf16_bits_to_f64(c.q) * np.exp2(size)
+    q[0, 0] = 0
+    q[-1, -1] /= np.exp2(size)
+    c.q = round_to_bf16_bits(q)
+    check(c)
+
+
+@each_shape
+def test_queries_of_uneven_elements(shape):
+    """Elements of a row up to 2^14 apart, the largest ones few."""
+    c = Shared(**SHAPES[shape])
+    rng = np.random.default_rng(3)
+    c.q = round_to_bf16_bits(bf16_bits_to_f64(c.q) * np.exp2(-rng.integers(0, 15, c.q.shape)))
+    check(c)
+
+
+@each_shape
+@pytest.mark.parametrize("where", ["shared", "own", "all"])
+def test_zero_values(shape, where):
+    """Blocks of zeros, scale 2^-126, in one part or both."""
+    c = Shared(**SHAPES[shape])
+    for s, n in enumerate(c.lens):
+        lo, hi = {"shared": (0, c.first), "own": (c.first, -(-n // 16)), "all": (0, -(-n // 16))}[where]
+        c.val[1][c.table[s][lo:hi]], c.scale[1][c.table[s][lo:hi]] = 0, FLOOR
+    check(c)
+    if where == "all":
+        assert bool((c.out == 0).all())
+
+
+@each_shape
+def test_queries_that_are_not_numbers(shape):
+    """A row of q with NaN or inf is NaN; the others are what they were."""
+    c = Shared(**SHAPES[shape])
+    c.run()
+    torch.cuda.synchronize()
+    want = c.out.clone()
+    c.dq = c.dq.clone()
+    c.dq[1, 2, 3], c.dq[-1, 0, 5] = float("nan"), float("inf")
+    c.run()
+    torch.cuda.synchronize()
+    bad = torch.zeros(c.out.shape[:2], dtype=torch.bool, device="cuda")
+    bad[1, 2] = bad[-1, 0] = True
+    assert bool(c.out[bad].isnan().all()) and torch.equal(c.out[~bad], want[~bad])
