@@ -761,7 +761,8 @@ const char* kvrp_last_error(void);
  * attention call (kv_attend_*), append, pack, step tables or verification enqueued.  Relocation: the relocation
  * kernel, plus for a batch the small copy launches that carry its launch plan to
  * the device (31 KB of plan each).  Attention: the block and combine kernels (2;
- * the combine alone when no chunk has tokens); kv_attend_shared_q8 3, with many rows 4,
+ * the combine alone when no chunk has tokens); kv_attend_shared_q8 3, with more than
+ * 4 x floor(16 / group) rows a sequence 4,
  * one fewer where the prefix has no pages.  Append, pack and draft verification: 1.
  * Step tables: 1, or 2 for many rows.  0 when the
  * call returned an error or had nothing to move. */

@@ -118,7 +118,7 @@ struct PlanSmem {
 constexpr int kLeast = 2;
 template <Part kPart>
 __device__ __forceinline__ bool find_share(const Params& p, Plan* out, PlanSmem& sh) {
-  const int n = p.seqs.n_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = kPart == kRest ? p.seqs.n_seqs * p.chunks : p.seqs.n_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool idle = false;
   auto cost = [&](const Seq& q) { return q.pages > 0 ? q.pages + p.unit_pages : 0; };   // of one head group
   int64_t later = 0;   // the sequences past the first kThreads
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
         const int q = i_q + lane, pg = i_first + (stream + q / PG * p.streams) * PG + q % PG;
         b_page = -1;      // none
         if (pg < ic.end) {
-          b_page = p.seqs.block_tables[(int64_t)ic.s * p.seqs.table_stride + (kPart == kRest ? table0 : 0) + pg];
+          b_page = p.seqs.block_tables[(int64_t)(kPart == kRest ? place_sequence(p, ic.s) : ic.s) * p.seqs.table_stride + (kPart == kRest ? table0 : 0) + pg];
           if (b_page < 0 || b_page >= p.seqs.num_pages) {
             b_page = p.seqs.num_pages;   // read as zeros
             flag(p.status, KVRP_DEV_BAD_PAGE);

@@ -51,6 +51,7 @@ struct Params {
   // kv_attend_shared_q8 only: the tokens that all sequences begin with, and its passes' results
   const int32_t *prefix_table, *prefix_length;
   int prefix_pages;
+  int all_rows, chunks; // few rows: a sequence's rows in up to `chunks` runs of max_rows, all_rows in all
   bool behind;          // few rows: launched behind the shared tokens' pass, on which nothing here depends
   float* dense;         // [n_rows][Hq][D + 4]: like `partial`, of a unit that one CTA held
   int2* found;          // [n_rows][n_grp], few rows: by a sequence's first row the CTA that begins a unit, and its
@@ -176,24 +177,41 @@ __device__ __forceinline__ View load_view(const Params& p) {
   v.tokens = ok ? length / kPage * kPage : -1;
   return v;
 }
-// sequence() for a part: rows, and the tokens that they see at most of it.
+// sequence() for the tokens behind the shared ones.  A sequence that is not behind them, or whose rows are not among
+// the batch's, is bad.
+__device__ __forceinline__ bool own_sequence(const Params& p, int s, int& row0, int& rows, int& len) {
+  const View v = load_view(p);
+  bool ok = sequence(p.seqs, s, row0, rows, len);
+  if (ok && rows > 0) {
+    ok = v.tokens >= 0 && len - rows >= v.tokens && row0 >= v.first && row0 + rows <= v.end && rows <= p.all_rows;
+    if (ok) len -= v.tokens;
+    else rows = 0;
+  }
+  return ok;
+}
+// The sequence whose run of rows number s is.
+__device__ __forceinline__ int place_sequence(const Params& p, int s) {
+  return p.chunks == 1 ? s : (int)((uint32_t)s / (uint32_t)p.chunks);
+}
+// sequence() for a part: rows, and the tokens that they see at most of it.  A run of a sequence's rows is a sequence
+// that ends with its last row.
 template <Part kPart>
 __device__ __forceinline__ bool part_sequence(const Params& p, int s, int& row0, int& rows, int& len) {
   if constexpr (kPart == kAll) return sequence(p.seqs, s, row0, rows, len);
-  const View v = load_view(p);
   if constexpr (kPart == kShared) {
+    const View v = load_view(p);
     row0 = v.first;
     rows = v.tokens > 0 ? v.end - v.first : 0;
     len = max(v.tokens, 0);
     return true;
   }
-  // A sequence that is not behind the shared tokens, or whose rows are not among the batch's, is bad.
-  bool ok = sequence(p.seqs, s, row0, rows, len);
-  if (ok && rows > 0) {
-    ok = v.tokens >= 0 && len - rows >= v.tokens && row0 >= v.first && row0 + rows <= v.end;
-    if (ok) len -= v.tokens;
-    else rows = 0;
-  }
+  if (p.chunks == 1) return own_sequence(p, s, row0, rows, len);
+  const int seq = place_sequence(p, s), before = (s - seq * p.chunks) * p.max_rows;
+  const bool ok = own_sequence(p, seq, row0, rows, len);
+  const int after = max(rows - before - p.max_rows, 0);
+  len -= rows > 0 ? after : 0;
+  row0 += before;
+  rows = max(rows - before - after, 0);
   return ok;
 }
 

@@ -9,8 +9,8 @@
 //     for prompts (kvrp_attend_q8_prompt.cu) with every row seeing every token.  K and V of the shared pages are
 //     read once for each 256 (row, query head) pairs of a KV head instead of once a sequence, and few rows
 //     a sequence become full tiles.
-//   - the sequences' own tokens: the kernel that kv_attend_q8 takes for as many rows, from the shared
-//     pages' end on.
+//   - the sequences' own tokens, from the shared pages' end on: kv_attend_q8's kernel for few rows (see
+//     Runs for more of them than it takes at once) or for many.
 //   - join_kernel merges both passes' partial results, in fp32, and rounds once.  A unit of the first pass
 //     that several CTAs shared is found by arithmetic (all its units cost the same); one of the second
 //     by a record that the CTA that begins it leaves.
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     s = lo;
   }
   int row0 = 0, rows = 0, len = 0;
-  const bool ok = view.tokens >= 0 && row >= view.first && row < view.end && part_sequence<kRest>(p, s, row0, rows, len);
+  const bool ok = view.tokens >= 0 && row >= view.first && row < view.end && own_sequence(p, s, row0, rows, len);
   const int64_t at = (int64_t)row * p.Hq + head;
   const bool idle = ok && len == 0;
   const int h = head / p.g, jq = head - h * p.g;
@@ -86,13 +86,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     if (p.lse && f == 0) p.lse[at] = -INFINITY;
     return;
   }
-  if (rows > p.max_rows || row < row0 || row >= row0 + rows) return;
+  if (row < row0 || row >= row0 + rows) return;
   // the own tokens'
   int2 own = make_int2(0, 0);
   int64_t own_y = 0;
   if (j.few) {
-    own = p.found[(int64_t)row0 * p.n_grp + h / p.hg];
-    own_y = (h % p.hg) * p.max_rows * p.g + (row - row0) * p.g + jq;
+    const int in_run = (row - row0) % p.max_rows;
+    own = p.found[(int64_t)(row - in_run) * p.n_grp + h / p.hg];
+    own_y = (h % p.hg) * p.max_rows * p.g + in_run * p.g + jq;
   }
   const int n = n_shared + max(own.y, 1);
   const auto entry = [&](int x) -> const float* {
@@ -146,6 +147,20 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   if (p.lse && f == 0) p.lse[at] = (m + lg2(l)) * kLn2;
 }
 
+// A sequence's rows go through the kernel for few rows in runs of as many as it takes, each reading the sequence's own
+// tokens again (from L2), if there are few runs; else through the kernel for many.
+// 28 / 4 heads x 128: 16 sequences of 5 rows over 16000 shared tokens and 60 to 600 own, three runs, 56.3 us against
+// 67.8 the other way; 32 of 8 rows over 300 to 3000 own, four runs, 100.2 against 99.2.
+constexpr int kMostRuns = 4;
+struct Runs {
+  int rows, count;   // rows of a run; runs of max_rows rows, 0: too many
+};
+Runs runs(int64_t max_rows, int g) {
+  const int rows = (int)std::min<int64_t>(max_rows, kMaxCols / g);
+  const int64_t count = (max_rows + rows - 1) / rows;
+  return {rows, count <= kMostRuns ? (int)count : 0};
+}
+
 // Where things are in the workspace, in bytes.
 struct Layout {
   size_t meta, found, shared, shared_dense, partial, dense, end;
@@ -153,7 +168,8 @@ struct Layout {
 Layout layout(int Hq, int Hkv, int D, int64_t max_rows, int64_t n_rows, int sms) {
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const int g = Hq / Hkv, hg = head_group(Hkv);
-  const bool few = max_rows * g <= kMaxCols;
+  const Runs r = runs(max_rows, g);
+  const bool few = r.count > 0;
   const size_t entry = (D + 4) * sizeof(float), rows = (size_t)n_rows * Hq * entry;
   Layout l;
   l.meta = 256;   // what aligning the caller's pointer takes
@@ -161,7 +177,7 @@ Layout layout(int Hq, int Hkv, int D, int64_t max_rows, int64_t n_rows, int sms)
   l.shared = l.found + (few ? up((size_t)n_rows * (Hkv / hg) * sizeof(int2)) : 0);
   l.shared_dense = l.shared + up((size_t)sms * 2 * kPromptRows * entry);
   l.partial = l.shared_dense + up(rows);
-  l.dense = l.partial + (few ? up((size_t)kMaxCtasPerSm * sms * 2 * hg * max_rows * g * entry)
+  l.dense = l.partial + (few ? up((size_t)kMaxCtasPerSm * sms * 2 * hg * r.rows * g * entry)
                              : up((size_t)sms * 2 * kPromptRows * entry));
   l.end = l.dense + up(rows);
   return l;
@@ -206,8 +222,11 @@ kvrp_status kv_attend_shared_q8(const void* q, int64_t q_stride, const kvrp_seqs
   st = current_device_sms(&sms, &smem_optin);
   if (st != KVRP_OK) return st;
   sms = attend_q8::sm_count();   // at most what the workspace is laid out for
-  const bool few = (int64_t)p.max_rows * p.g <= attend_q8::kMaxCols;
+  const attend_q8::Runs runs = attend_q8::runs(p.max_rows, p.g);
+  const bool few = runs.count > 0;
   const attend_q8::Layout at = attend_q8::layout(n_q_heads, n_kv_heads, head_dim, p.max_rows, seqs->n_rows, sms);
+  p.all_rows = p.max_rows;
+  p.chunks = 1;
   uint8_t* base = reinterpret_cast<uint8_t*>(reinterpret_cast<uintptr_t>(workspace) & ~uintptr_t(255));
   p.prefix_table = prefix->block_table;
   p.prefix_length = prefix->length;
@@ -233,7 +252,11 @@ kvrp_status kv_attend_shared_q8(const void* q, int64_t q_stride, const kvrp_seqs
   p.partial = reinterpret_cast<float*>(base + at.partial);
   p.dense = reinterpret_cast<float*>(base + at.dense);
   p.behind = few && launches > 0;
-  if (few) attend_q8::set_few(p, sms, head_dim);
+  if (few) {
+    p.max_rows = runs.rows;
+    p.chunks = runs.count;
+    attend_q8::set_few(p, sms, head_dim);
+  }
   if (e == cudaSuccess)
     e = few ? attend_q8::launch_few(p, head_dim, stream, attend_q8::kRest)
             : attend_q8::launch_prompt(kmap, vmap, p, head_dim, stream, attend_q8::kRest);
