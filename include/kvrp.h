@@ -610,7 +610,8 @@ typedef struct kvrp_prefix {
 /*
  * kv_attend_shared_q8 -- kv_attend_q8 for a batch whose sequences all begin with
  * the prefix's tokens: those are read once for the whole batch instead of once a
- * sequence.  The same result up to rounding, the same arguments, and
+ * sequence (or by each, where they are so few that this is faster).  The same result up
+ * to rounding, the same arguments, and
  *   prefix       the shared tokens, in pages of the same pools.  Table entries of
  *                the sequences for these pages are not read.
  *   workspace    kv_attend_shared_q8_workspace_size(...) bytes, max_rows and n_rows
@@ -737,6 +738,14 @@ kvrp_status kv_verify_drafts(
 void kvrp_test_set_wait_limit(uint32_t cycles);
 
 /*
+ * kvrp_test_set_each_limit -- for tests only.  Sets how many bytes of shared keys and
+ * values (counted once a sequence) kv_attend_shared_q8 lets each sequence read for
+ * itself, in the calls from now on by any thread: 0 none (nor any alone), so that the
+ * small cases of a test take the shared pass too; below 0 restores the library's own.
+ */
+void kvrp_test_set_each_limit(int64_t bytes);
+
+/*
  * kvrp_test_attend_split -- for tests of the host-side planning only; no CUDA
  * call.  The work split kv_attend_relocated gives n_cta blocks for chunks of
  * these token counts and ranks (host arrays of n_chunks): the stage sequence
@@ -761,9 +770,9 @@ const char* kvrp_last_error(void);
  * attention call (kv_attend_*), append, pack, step tables or verification enqueued.  Relocation: the relocation
  * kernel, plus for a batch the small copy launches that carry its launch plan to
  * the device (31 KB of plan each).  Attention: the block and combine kernels (2;
- * the combine alone when no chunk has tokens); kv_attend_shared_q8 3, with more than
- * 4 x floor(16 / group) rows a sequence 4,
- * one fewer where the prefix has no pages.  Append, pack and draft verification: 1.
+ * the combine alone when no chunk has tokens); kv_attend_shared_q8 2 where little is
+ * shared, else 3, with more than 4 x floor(16 / group) rows a sequence 4 (3 where the
+ * prefix has no pages).  Append, pack and draft verification: 1.
  * Step tables: 1, or 2 for many rows.  0 when the
  * call returned an error or had nothing to move. */
 int32_t kvrp_last_launch_count(void);

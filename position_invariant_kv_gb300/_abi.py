@@ -26,7 +26,7 @@ KVRP_BF16 = 1
 EXPORTED_SYMBOLS = (
     "kv_relocate_patch", "kv_relocate_patch_mrope", "kv_relocate_patch_mla", "kv_relocate_batch",
     "kv_relocate_batch_workspace_size", "kv_relocate_batch_noalloc", "kv_relocate_batch_mrope",
-    "kv_relocate_batch_mla", "kvrp_test_set_wait_limit", "kvrp_test_attend_split", "kv_patch_form_workspace_size",
+    "kv_relocate_batch_mla", "kvrp_test_set_wait_limit", "kvrp_test_set_each_limit", "kvrp_test_attend_split", "kv_patch_form_workspace_size",
     "kv_patch_form", "kv_patch_form_orbit", "kv_attend_relocated_workspace_size", "kv_attend_relocated",
     "kv_append", "kv_append_q8", "kv_pack_q8", "kv_attend_q8_workspace_size", "kv_attend_q8",
     "kv_attend_shared_q8_workspace_size", "kv_attend_shared_q8", "kv_step_tables", "kv_verify_drafts",
@@ -116,6 +116,8 @@ def _load_library():
         C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]
     L.kvrp_test_set_wait_limit.restype = None
     L.kvrp_test_set_wait_limit.argtypes = [C.c_uint32]
+    L.kvrp_test_set_each_limit.restype = None
+    L.kvrp_test_set_each_limit.argtypes = [C.c_int64]
     L.kvrp_test_attend_split.restype = C.c_int32
     L.kvrp_test_attend_split.argtypes = [C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int32, C.c_int32,
                                          C.c_int32, C.c_int32, C.c_int32, C.POINTER(C.c_int32)]
@@ -416,6 +418,11 @@ def kv_relocate_batch_mla(chunks, *, n_layers: int, kv_lora_dim: int, rope_dim: 
     _check(lib().kv_relocate_batch_mla(
         arr, n, int(n_layers), int(kv_lora_dim), int(rope_dim), float(rope_theta), _ptr(workspace),
         int(workspace_bytes), _ptr(d_status), _stream(stream)))
+
+
+def kvrp_test_set_each_limit(limit: int) -> None:
+    """Testing hook: bytes of shared keys and values that kv_attend_shared_q8's sequences may read each (-1: its own limit)."""
+    lib().kvrp_test_set_each_limit(int(limit))
 
 
 def kvrp_test_set_wait_limit(cycles: int) -> None:

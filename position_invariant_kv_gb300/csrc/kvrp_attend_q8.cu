@@ -118,7 +118,7 @@ struct PlanSmem {
 constexpr int kLeast = 2;
 template <Part kPart>
 __device__ __forceinline__ bool find_share(const Params& p, Plan* out, PlanSmem& sh) {
-  const int n = kPart == kRest ? p.seqs.n_seqs * p.chunks : p.seqs.n_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = kPart == kAll ? p.seqs.n_seqs : p.seqs.n_seqs * p.chunks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   bool idle = false;
   auto cost = [&](const Seq& q) { return q.pages > 0 ? q.pages + p.unit_pages : 0; };   // of one head group
   int64_t later = 0;   // the sequences past the first kThreads
@@ -229,7 +229,7 @@ struct Decode {
   static constexpr int kSmem = kRing + kMergeSlots * kMerge * 4;
 };
 
-template <int D, int NT, Part kPart>   // head_dim; tiles of 8 (row, head) columns; kAll or kRest
+template <int D, int NT, Part kPart>   // head_dim; tiles of 8 (row, head) columns; kAll, kRest or kEach
 __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kernel(const __grid_constant__ Params p) {
   using C = Decode<D, NT>;
   constexpr int KT = D / 16;                 // 16-deep steps over the features; 16-feature tiles of O^T
@@ -250,10 +250,10 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
   if (!behind) pdl_wait();
   pdl_launch_dependents();
   Plan plan;
-  __shared__ int table0;   // the first page of a sequence that its rows attend over
-  if (kPart == kRest && tid == 0) table0 = max(load_view(p).tokens, 0) / kPage;
+  __shared__ int table0;   // the shared tokens' pages
+  if (kPart != kAll && tid == 0) table0 = max(load_view(p).tokens, 0) / kPage;
   if (!find_share<kPart>(p, &plan, plan_smem)) {
-    if constexpr (kPart == kAll) {
+    if constexpr (kPart != kRest) {
       if (tid == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
       if (plan.idle) write_idle(p, D);
     }
@@ -301,7 +301,10 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
         const int q = i_q + lane, pg = i_first + (stream + q / PG * p.streams) * PG + q % PG;
         b_page = -1;      // none
         if (pg < ic.end) {
-          b_page = p.seqs.block_tables[(int64_t)(kPart == kRest ? place_sequence(p, ic.s) : ic.s) * p.seqs.table_stride + (kPart == kRest ? table0 : 0) + pg];
+          const int32_t* table = p.seqs.block_tables + (int64_t)(kPart == kAll ? ic.s : place_sequence(p, ic.s)) * p.seqs.table_stride;
+          if (kPart == kRest) table += table0;
+          if (kPart == kEach && pg < table0) table = p.prefix_table;
+          b_page = table[pg];
           if (b_page < 0 || b_page >= p.seqs.num_pages) {
             b_page = p.seqs.num_pages;   // read as zeros
             flag(p.status, KVRP_DEV_BAD_PAGE);
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
         for (int b = 0; b < 2; ++b) {
           const int c = nt * 8 + 2 * tig + b;
           if (c >= cols) continue;
-          if (kPart == kAll && begins && ends) {
+          if (kPart != kRest && begins && ends) {
             const float2 r = result_factors(m[nt][b], om[nt][b], l[nt][b]);
             const int64_t row = (int64_t)(cq.row0 + c / p.g) * p.Hq + head * p.g + c % p.g;
             uint32_t w[FPL / 2];
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, (Decode<D, NT>::kCtas)) decode_kerne
     }
     if (!next_segment<kPart>(p, cc, cq)) break;
   }
-  if constexpr (kPart == kAll) {
+  if constexpr (kPart != kRest) {
     if (tid == 0) p.meta[blockIdx.x] = meta;
     if (plan.idle) write_idle(p, D);
   }
@@ -879,6 +882,9 @@ cudaError_t launch_few(const Params& p, int head_dim, cudaStream_t stream, Part 
   if (part == kRest)
     kernel = head_dim == 64 ? (two ? decode_kernel<64, 2, kRest> : decode_kernel<64, 1, kRest>)
                             : (two ? decode_kernel<128, 2, kRest> : decode_kernel<128, 1, kRest>);
+  if (part == kEach)
+    kernel = head_dim == 64 ? (two ? decode_kernel<64, 2, kEach> : decode_kernel<64, 1, kEach>)
+                            : (two ? decode_kernel<128, 2, kEach> : decode_kernel<128, 1, kEach>);
   const int smem = head_dim == 64 ? (two ? Decode<64, 2>::kSmem : Decode<64, 1>::kSmem)
                                   : (two ? Decode<128, 2>::kSmem : Decode<128, 1>::kSmem);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -894,6 +900,19 @@ cudaError_t launch_few(const Params& p, int head_dim, cudaStream_t stream, Part 
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+cudaError_t launch_combine(const Params& p, int head_dim, int sms, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(5 * sms);
+  cfg.blockDim = dim3(kCombineThreads);
+  return cudaLaunchKernelEx(&cfg, head_dim == 64 ? combine_kernel<64> : combine_kernel<128>, p);
 }
 
 }  // namespace attend_q8
@@ -992,17 +1011,7 @@ kvrp_status kv_attend_q8(const void* q, int64_t q_stride, const kvrp_seqs* seqs,
     return KVRP_OK;
   }
   cudaError_t e = attend_q8::launch_few(p, head_dim, stream, attend_q8::kAll);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(5 * sms);
-  cfg.blockDim = dim3(attend_q8::kCombineThreads);
-  if (e == cudaSuccess)
-    e = cudaLaunchKernelEx(&cfg, head_dim == 64 ? attend_q8::combine_kernel<64> : attend_q8::combine_kernel<128>, p);
+  if (e == cudaSuccess) e = attend_q8::launch_combine(p, head_dim, sms, stream);
   if (e != cudaSuccess) return fail(KVRP_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
   g_last_launches = 2;
   return KVRP_OK;

@@ -59,8 +59,9 @@ struct Params {
 };
 
 // Which tokens a kernel's rows attend over: all of their sequence's (kv_attend_q8); the shared ones, for all rows
-// of the batch as if they were one sequence's, each row seeing all; or those behind the shared ones.
-enum Part { kAll, kShared, kRest };
+// of the batch as if they were one sequence's, each row seeing all; those behind the shared ones; or both, read by
+// each sequence for itself.
+enum Part { kAll, kShared, kRest, kEach };
 
 // The kernel for many rows: its columns (rows a partial result holds) and its launch,
 // p.n_cta blocks.
@@ -123,6 +124,8 @@ cudaError_t launch_prompt(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
 // The kernel for few rows, p.n_cta blocks.
 cudaError_t launch_few(const Params& p, int head_dim, cudaStream_t stream, Part part);
 void set_few(Params& p, int sms, int head_dim);   // p's fields for it
+// Merges what that kernel (kAll, kEach) left in parts.
+cudaError_t launch_combine(const Params& p, int head_dim, int sms, cudaStream_t stream);
 // The host checks of both calls, and what they fill in of the parameters.
 kvrp_status check_call(const char* fn, const void* q, int64_t& q_stride, const kvrp_seqs* seqs, int32_t n_q_heads,
                        int32_t n_kv_heads, int32_t head_dim, float softmax_scale, const void* k_pool, const void* v_pool,
@@ -177,15 +180,16 @@ __device__ __forceinline__ View load_view(const Params& p) {
   v.tokens = ok ? length / kPage * kPage : -1;
   return v;
 }
-// sequence() for the tokens behind the shared ones.  A sequence that is not behind them, or whose rows are not among
-// the batch's, is bad.
+// sequence() for the tokens behind the shared ones (kRest) or for all (kEach).  A sequence that is not behind them, or
+// whose rows are not among the batch's, is bad.
+template <Part kPart>
 __device__ __forceinline__ bool own_sequence(const Params& p, int s, int& row0, int& rows, int& len) {
   const View v = load_view(p);
   bool ok = sequence(p.seqs, s, row0, rows, len);
   if (ok && rows > 0) {
     ok = v.tokens >= 0 && len - rows >= v.tokens && row0 >= v.first && row0 + rows <= v.end && rows <= p.all_rows;
-    if (ok) len -= v.tokens;
-    else rows = 0;
+    if (!ok) rows = 0;
+    else if (kPart == kRest) len -= v.tokens;
   }
   return ok;
 }
@@ -205,9 +209,9 @@ __device__ __forceinline__ bool part_sequence(const Params& p, int s, int& row0,
     len = max(v.tokens, 0);
     return true;
   }
-  if (p.chunks == 1) return own_sequence(p, s, row0, rows, len);
+  if (p.chunks == 1) return own_sequence<kPart>(p, s, row0, rows, len);
   const int seq = place_sequence(p, s), before = (s - seq * p.chunks) * p.max_rows;
-  const bool ok = own_sequence(p, seq, row0, rows, len);
+  const bool ok = own_sequence<kPart>(p, seq, row0, rows, len);
   const int after = max(rows - before - p.max_rows, 0);
   len -= rows > 0 ? after : 0;
   row0 += before;

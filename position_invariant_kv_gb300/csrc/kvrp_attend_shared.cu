@@ -12,14 +12,25 @@
 //   - the sequences' own tokens, from the shared pages' end on: kv_attend_q8's kernel for few rows (see
 //     Runs for more of them than it takes at once) or for many.
 //   - join_kernel merges both passes' partial results, in fp32, and rounds once.  A unit of the first pass
-//     that several CTAs shared is found by arithmetic (all its units cost the same); one of the second
-//     by a record that the CTA that begins it leaves.
+//     that several CTAs shared is found by arithmetic (EvenUnits); one of the second by a record that the
+//     CTA that begins it leaves.
+// The second pass depends on nothing in the first: its blocks take the SMs that the first one's leave, one
+// after another, and wait for it at their end alone; the join looks up what it needs before it waits.
+//
+// Measured, 28 / 4 heads x 128: 64 sequences, 16384 shared tokens, 30 to 1500 own: 46 us (kv_attend_q8, which
+// reads the shared tokens for each sequence, takes 203); 96 sequences, 100000 and 100 to 3000: 173 us, 804 TFLOP/s;
+// 16 of 5 rows, 65536 and 40 to 2000: 120 us; 3 over 1008: 17.5 us.  32 / 32 heads, 24 sequences, 4144 and 20 to 700:
+// 40 us.  The 46 us: 4 until the first pass knows its share, 5 until its queries are laid out, 14 for 11 token
+// tiles a CTA, 3 for its results, 12 for the own tokens behind them (26 MB: latency), 6 for the join (20 MB of partial
+// results from L2).  A token tile takes 1.2 us whatever the rows: 1850 of its 2300 cycles are the softmax warps', a
+// thread a row, and the products and conversions beside them take as long in turn.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include "kvrp.h"
@@ -63,7 +74,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     s = lo;
   }
   int row0 = 0, rows = 0, len = 0;
-  const bool ok = view.tokens >= 0 && row >= view.first && row < view.end && own_sequence(p, s, row0, rows, len);
+  const bool ok = view.tokens >= 0 && row >= view.first && row < view.end && own_sequence<kRest>(p, s, row0, rows, len);
   const int64_t at = (int64_t)row * p.Hq + head;
   const bool idle = ok && len == 0;
   const int h = head / p.g, jq = head - h * p.g;
@@ -161,6 +172,15 @@ Runs runs(int64_t max_rows, int g) {
   return {rows, count <= kMostRuns ? (int)count : 0};
 }
 
+// Up to this many bytes of shared keys and values, counted for each run of each sequence, and for up to two runs
+// in all, every sequence reads them for itself (again from L2): one pass and kv_attend_q8's combine instead of
+// three launches.  28 / 4 heads x 128, read by each and once: 8 sequences over 4000 shared tokens (31 MB) 18.9 and 21.0 us,
+// over 12000 (94 MB) 26.0 and 26.5, 16 over 8000 (125 MB) 28.6 and 24.2; 2 over 64000 (125 MB) 33.7 and 46.1, 1 over 160000
+// 50.6 and 84.8.
+constexpr int64_t kEachBytes = 96 << 20;
+constexpr int kEachRuns = 2;
+std::atomic<int64_t> each_bytes{kEachBytes};   // tests set it
+
 // Where things are in the workspace, in bytes.
 struct Layout {
   size_t meta, found, shared, shared_dense, partial, dense, end;
@@ -173,7 +193,7 @@ Layout layout(int Hq, int Hkv, int D, int64_t max_rows, int64_t n_rows, int sms)
   const size_t entry = (D + 4) * sizeof(float), rows = (size_t)n_rows * Hq * entry;
   Layout l;
   l.meta = 256;   // what aligning the caller's pointer takes
-  l.found = l.meta + (few ? 0 : meta_bytes(sms));
+  l.found = l.meta + meta_bytes(few ? kMaxCtasPerSm * sms : sms);
   l.shared = l.found + (few ? up((size_t)n_rows * (Hkv / hg) * sizeof(int2)) : 0);
   l.shared_dense = l.shared + up((size_t)sms * 2 * kPromptRows * entry);
   l.partial = l.shared_dense + up(rows);
@@ -191,6 +211,8 @@ Layout layout(int Hq, int Hkv, int D, int64_t max_rows, int64_t n_rows, int sms)
 using namespace kvrp;
 
 extern "C" {
+
+void kvrp_test_set_each_limit(int64_t bytes) { attend_q8::each_bytes = bytes < 0 ? attend_q8::kEachBytes : bytes; }
 
 size_t kv_attend_shared_q8_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_rows,
                                           int32_t n_rows) {
@@ -234,6 +256,23 @@ kvrp_status kv_attend_shared_q8(const void* q, int64_t q_stride, const kvrp_seqs
   p.n_cta = sms;
   p.cols = attend_q8::kPromptRows;
 
+  p.meta = reinterpret_cast<int4*>(base + at.meta);
+  p.found = reinterpret_cast<int2*>(base + at.found);
+  p.partial = reinterpret_cast<float*>(base + at.partial);
+  p.dense = reinterpret_cast<float*>(base + at.dense);
+  const int64_t all_runs = (int64_t)seqs->n_seqs * runs.count, limit = attend_q8::each_bytes;
+  const double each = (double)all_runs * prefix->n_pages * 2 * q8::kPage * n_kv_heads * head_dim;   // past 64 bits at the ends
+  if (few && (each <= (double)limit || (all_runs <= attend_q8::kEachRuns && limit > 0))) {
+    p.max_rows = runs.rows;
+    p.chunks = runs.count;
+    attend_q8::set_few(p, sms, head_dim);
+    cudaError_t e = attend_q8::launch_few(p, head_dim, stream, attend_q8::kEach);
+    if (e == cudaSuccess) e = attend_q8::launch_combine(p, head_dim, sms, stream);
+    if (e != cudaSuccess) return fail(KVRP_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    g_last_launches = 2;
+    return KVRP_OK;
+  }
+
   CUtensorMap kmap, vmap;
   st = encode_q8_pool(&kmap, k_pool, seqs->num_pages, n_kv_heads * head_dim, head_dim);
   if (st == KVRP_OK) st = encode_q8_pool(&vmap, v_pool, seqs->num_pages, n_kv_heads * head_dim, head_dim);
@@ -247,10 +286,6 @@ kvrp_status kv_attend_shared_q8(const void* q, int64_t q_stride, const kvrp_seqs
     e = attend_q8::launch_prompt(kmap, vmap, shared, head_dim, stream, attend_q8::kShared);
     ++launches;
   }
-  p.meta = reinterpret_cast<int4*>(base + at.meta);
-  p.found = reinterpret_cast<int2*>(base + at.found);
-  p.partial = reinterpret_cast<float*>(base + at.partial);
-  p.dense = reinterpret_cast<float*>(base + at.dense);
   p.behind = few && launches > 0;
   if (few) {
     p.max_rows = runs.rows;

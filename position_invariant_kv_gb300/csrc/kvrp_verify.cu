@@ -16,6 +16,10 @@
 //     the part of the warp that holds it again (from L2), a vector a thread, and scans that.
 //   - A row begins wherever its stride puts it: vectors are cut at 16-byte boundaries, the ends
 //     are read by elements, and where p's and q's rows begin differently q is.
+//
+// Measured: 256 sequences x 262144 values (fp32, 424 MB) 77 us, 5.5 TB/s, 81% of a copy; 64 x 130003 (56 MB)
+// 15.8 us, where finding the rows before and the token after streaming them takes 5; 37 x 50021 bf16 9.6 us; one
+// sequence x 32000 5.1 us, a launch and five dependent trips to memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

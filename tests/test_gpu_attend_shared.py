@@ -24,6 +24,15 @@ def gpu():
     build()
 
 
+@pytest.fixture(params=["shared", "each"], autouse=True)
+def way(request):
+    """The shared tokens read once for the batch, or by each sequence (with few rows), whatever their number."""
+    import position_invariant_kv_gb300 as kvrp
+    kvrp.kvrp_test_set_each_limit(0 if request.param == "shared" else 1 << 50)
+    yield request.param
+    kvrp.kvrp_test_set_each_limit(-1)
+
+
 class Shared(Case):
     """Case with the first `prefix` tokens of all sequences on the same pages, `ctx` own tokens behind
     them; the sequences' own table entries for these pages are -1."""
@@ -97,12 +106,13 @@ MANY = {
 
 
 @pytest.mark.parametrize("name", [f"few-{n}" for n in FEW] + [f"many-{n}" for n in MANY])
-def test_parity(name):
+def test_parity(name, way):
     kind, name = name.split("-")
     c = Shared(**(FEW if kind == "few" else MANY)[name])
     c.run()
     at_once = 16 // (c.hq // c.hkv)          # rows of a run; up to four runs take the kernel for few rows
-    assert c.kvrp.kvrp_last_launch_count() == (3 if (c.max_rows or sum(c.rows)) <= 4 * at_once else 4)
+    few = (c.max_rows or sum(c.rows)) <= 4 * at_once
+    assert c.kvrp.kvrp_last_launch_count() == ((2 if way == "each" else 3) if few else 4)
     c.check()
     assert int(c.status) == 0
     first = c.out.clone(), c.lse.clone()
@@ -310,9 +320,11 @@ def test_two_calls_at_once():
 
 @pytest.mark.parametrize("case", [dict(prefix=3200, ctx=[300, 17], rows=[1, 1], hq=14, hkv=2, d=128),
                                   dict(prefix=1600, ctx=[120], rows=[90], hq=8, hkv=2, d=64)])
-def test_short_wait_limit_reports_timeout_and_the_next_call_is_right(case):
+def test_short_wait_limit_reports_timeout_and_the_next_call_is_right(case, way):
     """The passes' waits give up almost at once; the call returns, says so, and leaves nothing behind."""
     c = Shared(**case)
+    if way == "each" and max(c.rows) == 1:
+        pytest.skip("no pass with waits")
     try:
         c.kvrp.kvrp_test_set_wait_limit(1)
         c.run()
@@ -383,3 +395,14 @@ def test_queries_that_are_not_numbers(shape):
     bad = torch.zeros(c.out.shape[:2], dtype=torch.bool, device="cuda")
     bad[1, 2] = bad[-1, 0] = True
     assert bool(c.out[bad].isnan().all()) and torch.equal(c.out[~bad], want[~bad])
+
+
+def test_the_librarys_own_limit():
+    """Little that is shared is read by each sequence, much once."""
+    import position_invariant_kv_gb300 as kvrp
+    kvrp.kvrp_test_set_each_limit(-1)
+    for prefix, n, launches in ((160, 3, 2), (3008, 34, 3)):      # 0.5 MB, 105 MB
+        c = Shared(prefix=prefix, ctx=[i for i in range(n)], rows=[1] * n, hq=4, hkv=4, d=128, one_each=True)
+        c.run()
+        assert kvrp.kvrp_last_launch_count() == launches
+        c.check(seqs=[0, n - 1])

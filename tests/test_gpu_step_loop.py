@@ -27,10 +27,20 @@ def e4m3(x):
     return torch.from_numpy(x.astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8)
 
 
-@pytest.mark.parametrize("hq,hkv,d,rows", [(8, 2, 128, 4), (14, 2, 64, 4), (4, 4, 128, 1)])
-def test_a_decode_loop(hq, hkv, d, rows):
-    """rows 4 x group 4: the kernel for few rows; x group 7: the one for many."""
+@pytest.mark.parametrize("each", [0, -1])
+@pytest.mark.parametrize("hq,hkv,d,rows", [(8, 2, 128, 4), (14, 2, 64, 4), (4, 4, 128, 1), (32, 2, 64, 5)])
+def test_a_decode_loop(hq, hkv, d, rows, each):
+    """4 rows x group 4: the kernel for few rows; x group 7: in runs; 5 rows x group 16: the kernel for many.
+    each 0: the shared pages are read once for the batch; -1: few as they are here, by each sequence."""
     import position_invariant_kv_gb300 as kvrp
+    kvrp.kvrp_test_set_each_limit(each)
+    try:
+        decode_loop(kvrp, hq, hkv, d, rows)
+    finally:
+        kvrp.kvrp_test_set_each_limit(-1)
+
+
+def decode_loop(kvrp, hq, hkv, d, rows):
     rng = np.random.default_rng(rows * d + hq)
     n, vocab, shared, steps = 6, 501, 5, 7
     pages, stride = shared + 40, shared + 9
