@@ -65,7 +65,7 @@ namespace attend_q8 {
 
 
 // ---- shares ---------------------------------------------------------------------------
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = kFewHeads, kThreads = 32 * kWarps;
 
 struct Seq {
   int row0, rows, len, pages;   // pages 0: no work

@@ -27,6 +27,7 @@ constexpr float kLeastFactor = 1.17549435e-38f;   // 2^-126: what a score is mul
 constexpr float kZeroBlock = 0x1p-126f;    // a zero block's scale, which a page outside the pool reads as
 constexpr int kMaxCtasPerSm = 2, kMaxCtas = 1024;   // bounds of the grid
 constexpr int kMaxCols = 16;        // rows x group of the decode kernel
+constexpr int kFewHeads = 8;        // KV heads that a CTA of it takes together, at most: its warps
 
 struct Params {
   const uint16_t* q;

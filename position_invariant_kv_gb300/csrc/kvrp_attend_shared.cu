@@ -4,7 +4,8 @@
 //   out = (e^a O_a + e^b O_b) / (e^a + e^b):  O_a, a the attention and log-sum-exp over the shared tokens,
 //   O_b, b over a sequence's own tokens behind them (causal).
 //
-// Three passes, none of which reads anything twice:
+// Where little is shared each sequence reads it (kEachBytes): the kernel for few rows over the prefix's pages and the
+// sequence's own, one after the other.  Else three passes, none of which reads much twice:
 //   - the shared tokens, for all rows of the batch as if they were one sequence's: the tensor-core kernel
 //     for prompts (kvrp_attend_q8_prompt.cu) with every row seeing every token.  K and V of the shared pages are
 //     read once for each 256 (row, query head) pairs of a KV head instead of once a sequence, and few rows
@@ -17,13 +18,13 @@
 // The second pass depends on nothing in the first: its blocks take the SMs that the first one's leave, one
 // after another, and wait for it at their end alone; the join looks up what it needs before it waits.
 //
-// Measured, 28 / 4 heads x 128: 64 sequences, 16384 shared tokens, 30 to 1500 own: 46 us (kv_attend_q8, which
-// reads the shared tokens for each sequence, takes 203); 96 sequences, 100000 and 100 to 3000: 173 us, 804 TFLOP/s;
-// 16 of 5 rows, 65536 and 40 to 2000: 120 us; 3 over 1008: 17.5 us.  32 / 32 heads, 24 sequences, 4144 and 20 to 700:
-// 40 us.  The 46 us: 4 until the first pass knows its share, 5 until its queries are laid out, 14 for 11 token
-// tiles a CTA, 3 for its results, 12 for the own tokens behind them (26 MB: latency), 6 for the join (20 MB of partial
-// results from L2).  A token tile takes 1.2 us whatever the rows: 1850 of its 2300 cycles are the softmax warps', a
-// thread a row, and the products and conversions beside them take as long in turn.
+// Measured, 28 / 4 heads x 128, beside kv_attend_q8, which reads the shared tokens for each sequence: 64 sequences,
+// 16384 shared tokens, 30 to 1500 own 46 us (134.6); 96, 100000 and 100 to 3000: 173 us, 802 TFLOP/s (1090); 16 of 5 rows,
+// 65536 and 40 to 2000: 120 us (423).  32 / 32 heads, 24 sequences, 4144 and 20 to 700: 40 us (105).  32 / 8 heads x 64,
+// 32 of 4 rows, 9008 and 10 to 900: 41.5 us (77.7).  The 46 us: 4 until the first pass knows its share, 5 until its
+// queries are laid out, 14 for 11 token tiles a CTA, 3 for its results, 12 for the own tokens behind them (26 MB:
+// latency), 6 for the join (20 MB of partial results from L2).  A token tile takes 1.2 us whatever the rows: 1850 of its
+// 2300 cycles are the softmax warps', a thread a row, and the products and conversions beside them take as long in turn.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -164,21 +165,24 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // 67.8 the other way; 32 of 8 rows over 300 to 3000 own, four runs, 100.2 against 99.2.
 constexpr int kMostRuns = 4;
 struct Runs {
-  int rows, count;   // rows of a run; runs of max_rows rows, 0: too many
+  int rows;        // of a run
+  int64_t count;   // runs of max_rows rows
+  bool few;
 };
 Runs runs(int64_t max_rows, int g) {
   const int rows = (int)std::min<int64_t>(max_rows, kMaxCols / g);
   const int64_t count = (max_rows + rows - 1) / rows;
-  return {rows, count <= kMostRuns ? (int)count : 0};
+  return {rows, count, count <= kMostRuns};
 }
 
 // Up to this many bytes of shared keys and values, counted for each run of each sequence, and for up to two runs
 // in all, every sequence reads them for itself (again from L2): one pass and kv_attend_q8's combine instead of
 // three launches.  28 / 4 heads x 128, read by each and once: 8 sequences over 4000 shared tokens (31 MB) 18.9 and 21.0 us,
 // over 12000 (94 MB) 26.0 and 26.5, 16 over 8000 (125 MB) 28.6 and 24.2; 2 over 64000 (125 MB) 33.7 and 46.1, 1 over 160000
-// 50.6 and 84.8.
+// 50.6 and 84.8.  More runs a sequence than above do so too, if all that its table can hold is counted: 2 sequences of 6
+// rows over 16, 64 / 4 heads, 42.8 us the other way.
 constexpr int64_t kEachBytes = 96 << 20;
-constexpr int kEachRuns = 2;
+constexpr int kEachRuns = 2, kMostEachRuns = 16;
 std::atomic<int64_t> each_bytes{kEachBytes};   // tests set it
 
 // Where things are in the workspace, in bytes.
@@ -189,16 +193,17 @@ Layout layout(int Hq, int Hkv, int D, int64_t max_rows, int64_t n_rows, int sms)
   const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const int g = Hq / Hkv, hg = head_group(Hkv);
   const Runs r = runs(max_rows, g);
-  const bool few = r.count > 0;
+  const bool few = r.few;
   const size_t entry = (D + 4) * sizeof(float), rows = (size_t)n_rows * Hq * entry;
   Layout l;
   l.meta = 256;   // what aligning the caller's pointer takes
-  l.found = l.meta + meta_bytes(few ? kMaxCtasPerSm * sms : sms);
+  l.found = l.meta + meta_bytes(kMaxCtasPerSm * sms);
   l.shared = l.found + (few ? up((size_t)n_rows * (Hkv / hg) * sizeof(int2)) : 0);
   l.shared_dense = l.shared + up((size_t)sms * 2 * kPromptRows * entry);
   l.partial = l.shared_dense + up(rows);
   l.dense = l.partial + (few ? up((size_t)kMaxCtasPerSm * sms * 2 * hg * r.rows * g * entry)
-                             : up((size_t)sms * 2 * kPromptRows * entry));
+                             : up((size_t)sms * 2 * kPromptRows * entry));   // which holds the other's at most too
+  static_assert(kPromptRows >= kMaxCtasPerSm * kFewHeads * kMaxCols, "the parts of the kernel for few rows");
   l.end = l.dense + up(rows);
   return l;
 }
@@ -245,7 +250,7 @@ kvrp_status kv_attend_shared_q8(const void* q, int64_t q_stride, const kvrp_seqs
   if (st != KVRP_OK) return st;
   sms = attend_q8::sm_count();   // at most what the workspace is laid out for
   const attend_q8::Runs runs = attend_q8::runs(p.max_rows, p.g);
-  const bool few = runs.count > 0;
+  const bool few = runs.few;
   const attend_q8::Layout at = attend_q8::layout(n_q_heads, n_kv_heads, head_dim, p.max_rows, seqs->n_rows, sms);
   p.all_rows = p.max_rows;
   p.chunks = 1;
@@ -261,10 +266,12 @@ kvrp_status kv_attend_shared_q8(const void* q, int64_t q_stride, const kvrp_seqs
   p.partial = reinterpret_cast<float*>(base + at.partial);
   p.dense = reinterpret_cast<float*>(base + at.dense);
   const int64_t all_runs = (int64_t)seqs->n_seqs * runs.count, limit = attend_q8::each_bytes;
-  const double each = (double)all_runs * prefix->n_pages * 2 * q8::kPage * n_kv_heads * head_dim;   // past 64 bits at the ends
-  if (few && (each <= (double)limit || (all_runs <= attend_q8::kEachRuns && limit > 0))) {
+  const double pages = few ? prefix->n_pages : std::max(prefix->n_pages, seqs->table_stride);
+  const double each = (double)all_runs * pages * 2 * q8::kPage * n_kv_heads * head_dim;   // past 64 bits at the ends
+  if (runs.count <= attend_q8::kMostEachRuns &&
+      (each <= (double)limit || (few && all_runs <= attend_q8::kEachRuns && limit > 0))) {
     p.max_rows = runs.rows;
-    p.chunks = runs.count;
+    p.chunks = (int)runs.count;
     attend_q8::set_few(p, sms, head_dim);
     cudaError_t e = attend_q8::launch_few(p, head_dim, stream, attend_q8::kEach);
     if (e == cudaSuccess) e = attend_q8::launch_combine(p, head_dim, sms, stream);
@@ -289,7 +296,7 @@ kvrp_status kv_attend_shared_q8(const void* q, int64_t q_stride, const kvrp_seqs
   p.behind = few && launches > 0;
   if (few) {
     p.max_rows = runs.rows;
-    p.chunks = runs.count;
+    p.chunks = (int)runs.count;
     attend_q8::set_few(p, sms, head_dim);
   }
   if (e == cudaSuccess)

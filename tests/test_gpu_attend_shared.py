@@ -110,9 +110,8 @@ def test_parity(name, way):
     kind, name = name.split("-")
     c = Shared(**(FEW if kind == "few" else MANY)[name])
     c.run()
-    at_once = 16 // (c.hq // c.hkv)          # rows of a run; up to four runs take the kernel for few rows
-    few = (c.max_rows or sum(c.rows)) <= 4 * at_once
-    assert c.kvrp.kvrp_last_launch_count() == ((2 if way == "each" else 3) if few else 4)
+    runs = -(-(c.max_rows or sum(c.rows)) // (16 // (c.hq // c.hkv)))   # of the rows that the kernel for few takes
+    assert c.kvrp.kvrp_last_launch_count() == (2 if way == "each" and runs <= 16 else 3 if runs <= 4 else 4)
     c.check()
     assert int(c.status) == 0
     first = c.out.clone(), c.lse.clone()
@@ -325,6 +324,8 @@ def test_short_wait_limit_reports_timeout_and_the_next_call_is_right(case, way):
     c = Shared(**case)
     if way == "each" and max(c.rows) == 1:
         pytest.skip("no pass with waits")
+    if way == "each":
+        c.kvrp.kvrp_test_set_each_limit(0)
     try:
         c.kvrp.kvrp_test_set_wait_limit(1)
         c.run()
@@ -406,3 +407,22 @@ def test_the_librarys_own_limit():
         c.run()
         assert kvrp.kvrp_last_launch_count() == launches
         c.check(seqs=[0, n - 1])
+
+
+def test_a_pool_past_32_bits():
+    """Pages whose bytes lie past 4 GB of their pools."""
+    c = Shared(prefix=48, ctx=[5, 20, 0], rows=[1] * 3, hq=32, hkv=32, d=128, one_each=True)
+    pages = 70000
+    at, pools, scales = pages - c.pages, [], []
+    for pool, scale in zip(c.pool, c.dsc):
+        pools.append(torch.empty((pages, *pool.shape[1:]), dtype=torch.uint8, device="cuda"))
+        scales.append(torch.empty((pages, scale.shape[1]), device="cuda"))
+        pools[-1][at:], scales[-1][at:] = pool, scale
+    assert pools[0][at:].data_ptr() - pools[0].data_ptr() > 2 ** 32
+    table = np.where(c.table >= 0, c.table + at, -1)
+    table[:, :c.first] = -1
+    c.run(seqs=c.kvrp.Seqs(seq_lens=i32(c.lens), block_tables=i32(table), num_pages=pages),
+          prefix=c.kvrp.Prefix(i32(c.prefix_pages + at), i32([48])), k_pool=pools[0], v_pool=pools[1], k_scale=scales[0],
+          v_scale=scales[1])
+    c.check()
+    assert int(c.status) == 0

@@ -364,3 +364,10 @@ def test_verify_graph_and_streams():
                 g.replay()
         for x in xs:
             x.check()
+
+
+def test_verify_rows_past_32_bits():
+    """Rows 2^30 elements and one apart: element, and byte, offsets past 2^31."""
+    x = Verify([4, 1], 1003, bf16=True, seed=6, pad=2 ** 30 - 1002)
+    x.call()
+    x.check()
