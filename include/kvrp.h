@@ -642,7 +642,8 @@ kvrp_status kv_attend_shared_q8(
  * NULL here) from each sequence's tokens and rows, so that a captured step goes
  * on by itself while lengths, accepted drafts and sequences come and go.
  *   kept_lens    int32 [n_seqs]: tokens of the cache that stay (kv_verify_drafts'
- *                kept_lens; 0 for a place that falls free).  May be seqs->seq_lens.
+ *                kept_lens; 0 for a place that falls free).  May be seqs->seq_lens (a
+ *                sequence that cannot be served then loses its length).
  *   new_rows     int32 [n_seqs]: rows to append behind them.
  *   prefix       optional: the first pages of every sequence, owned by none.  Its
  *                length may change only while no sequence holds pages.
@@ -661,7 +662,8 @@ kvrp_status kv_attend_shared_q8(
  * entries past those needed keep what they held.
  *   row_start    the running sum of new_rows (at most n_rows).
  *   seq_lens     kept + new; 0 (an idle place, whose rows the other calls leave out)
- *                for a sequence that cannot be served.  It keeps its pages and table;
+ *                for a sequence that cannot be served.  It keeps its pages and table
+ *                (and, kv_verify_drafts' kept_lens being an array of its own, its place);
  *                its rows get position 0 and slot -1, as do the rows behind the last
  *                sequence.
  * *d_status: KVRP_DEV_NO_PAGES, if a sequence and those before it ask for more
@@ -709,8 +711,9 @@ kvrp_status kv_step_tables(
  *   kept_lens     optional device int32 [n_seqs]: seq_lens without the rows turned down
  *                 (the cache then holds all tokens but the drawn one).  May be
  *                 seqs->seq_lens.
- * An idle sequence (length 0) gets -1 in its rows, and 0; one without rows 0, and its
- * length.  A sequence with a bad length is flagged (KVRP_DEV_BAD_LENGTH) and its
+ * An idle sequence (length 0) gets -1 in its rows and 0 accepted, and its kept_lens stays
+ * as it was: one that kv_step_tables had no pages for goes on where it stood once there
+ * are some.  One without rows gets 0, and its length.  A sequence with a bad length is flagged (KVRP_DEV_BAD_LENGTH) and its
  * outputs stay as they were.  KVRP_DEV_BAD_TOKEN: a drafted token outside [0, vocab)
  * (it is turned down), or a row without weight (the token is -1).  block_tables and
  * num_pages of `seqs` are not used beyond its checks.  vocab up to 2^22.  Pointers 4-byte

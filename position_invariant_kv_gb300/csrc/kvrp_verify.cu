@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     for (int r = row0 + tid; r < end; r += kThreads) p.out[r] = -1;   // an idle place's rows
     if (tid == 0) {
       if (p.accepted) p.accepted[s] = 0;
-      if (p.kept) p.kept[s] = len;
+      if (p.kept && len > 0) p.kept[s] = len;
     }
     return;
   }

@@ -230,7 +230,7 @@ class Verify:
         self.seqs = self.kvrp.Seqs(seq_lens=self.d_lens, block_tables=torch.zeros((len(self.rows), 400), dtype=torch.int32, device="cuda"),
                                    num_pages=1, n_rows=self.n, row_start=i32(starts))
         self.out, self.accepted = i32([-9] * self.n), i32([-9] * len(self.rows))
-        self.kept = self.d_lens if in_place else i32([-9] * len(self.rows))
+        self.kept, self.in_place = self.d_lens if in_place else i32([-9] * len(self.rows)), in_place
         self.status = i32([0])
         self.args = dict(vocab=self.vocab, tokens=i32(self.tokens), u_accept=torch.tensor(self.u, device="cuda"),
                          u_sample=torch.tensor(self.v, device="cuda"), out_tokens=self.out, accepted=self.accepted,
@@ -254,7 +254,7 @@ class Verify:
             else:
                 out += [-1] * r
                 accepted.append(0)
-                kept.append(length)
+                kept.append(length if length or self.in_place else -9)   # an idle place's stays
             at += r
         return out, accepted, kept, odd
 
@@ -371,3 +371,22 @@ def test_verify_rows_past_32_bits():
     x = Verify([4, 1], 1003, bf16=True, seed=6, pad=2 ** 30 - 1002)
     x.call()
     x.check()
+
+
+def test_a_sequence_without_pages_goes_on_when_there_are_some():
+    """Tables and verification in turn: one that could not be served keeps its tokens, then gets its page."""
+    t = Tables(kept=[15, 31], new=[2, 2], held=[1, 2], table=[[0, -1, -1], [1, 2, -1]], ring=[3, -1, -1, -1, -1], state=[0, 1])
+    t.call(held_out=t.held, free_state_out=t.state)
+    assert t.check(held=t.held, state=t.state)["status"] == step.NO_PAGES
+    out, accepted, kept = i32([-9] * 4), i32([-9] * 2), t.kept
+    target = torch.full((4, 8), 0.125, device="cuda")
+    t.kvrp.kv_verify_drafts(target, t.seqs, vocab=8, tokens=i32([1, 2, 3, 4]), u_accept=torch.zeros(4, device="cuda"),
+                            u_sample=torch.zeros(2, device="cuda"), out_tokens=out, accepted=accepted, kept_lens=kept,
+                            d_status=t.status)
+    assert kept.tolist() == [17, 31] and accepted.tolist() == [1, 0] and out.tolist() == [2, 0, -1, -1]
+    t.ring[1], t.state[1] = 4, 1                  # a page has become free
+    t.host.update(kept=[17, 31], table=t.table.cpu().numpy(), ring=t.ring.tolist(), state=t.state.tolist(), held=t.held.tolist())
+    t.status.zero_()
+    t.call(held_out=t.held, free_state_out=t.state)
+    want = t.check(held=t.held, state=t.state)
+    assert want["status"] == 0 and want["seq_lens"] == [19, 33] and t.table[1].tolist() == [1, 2, 4]
