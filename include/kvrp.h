@@ -672,7 +672,7 @@ kvrp_status kv_attend_shared_q8(
  * has no pages for, fewer kept tokens than the prefix, rows past n_rows, or more
  * tokens than its table has entries for, for all sequences where free_state or the
  * prefix's length is out of range, and where more pages come back than the ring
- * holds (they are lost); KVRP_DEV_BAD_PAGE, where a page written or given back is
+ * has places for (those past its end are lost and not counted); KVRP_DEV_BAD_PAGE, where a page written or given back is
  * outside [0, num_pages) (it goes where it belongs all the same; a row on it gets
  * slot -1).  n_seqs x table_stride must stay below 2^31 (UNSUPPORTED).
  * Asynchronous on `stream`; may be captured into a graph.

@@ -60,9 +60,9 @@ def step_tables(kept, new, held, table, ring, state, n_rows, prefix_table=(), pr
             status |= 0 if 0 <= table[s, e] < size else BAD_PAGE
             if count + given < size:
                 ring[(head + count + given) % size] = int(table[s, e])
+                given += 1
             else:
-                status |= BAD_LENGTH
-            given += 1
+                status |= BAD_LENGTH   # lost: no place, and not counted
         for i in range(m):
             page = int(table[s, (k + i) // PAGE])
             positions[start + i] = k + i
@@ -72,7 +72,7 @@ def step_tables(kept, new, held, table, ring, state, n_rows, prefix_table=(), pr
                 status |= BAD_PAGE
         left[s] = need
         lens.append(length)
-    state = [(head + taken) % size, min(size, count - taken + given)] if usable else [head, count]
+    state = [(head + taken) % size, count - taken + given] if usable else [head, count]
     return {"table": table, "ring": ring, "state": state, "held": left, "row_start": starts, "seq_lens": lens,
             "positions": positions, "slots": slots, "status": status}
 

@@ -247,7 +247,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     p.row_start[0] = 0;
     if (usable) {
       p.state_out[0] = ring_at(head, (int)took, size);
-      p.state_out[1] = (int)min((int64_t)size, count - took + gave);
+      // Pages that the ring had no place for are lost: counted, they would stand for places whose pages have just been taken.
+      p.state_out[1] = (int)(count - took + min(gave, (int64_t)size - count));
     } else {
       const int a = __ldcg(p.state), b = __ldcg(p.state + 1);
       p.state_out[0] = a;

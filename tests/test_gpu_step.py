@@ -158,6 +158,26 @@ def test_tables_more_back_than_the_ring_holds():
     assert t.check()["status"] == step.BAD_LENGTH
 
 
+@pytest.mark.parametrize("behind", [0, 9000])   # rows behind the last sequence: one launch, two
+def test_tables_take_and_lose_pages_in_one_call(behind):
+    """Pages that are lost are not counted: no page of a served table is among the free ones afterwards."""
+    size, n = 40, 6
+    table = np.full((n, 12), -1)
+    for s, pages in ((1, range(0, 12)), (3, range(12, 24)), (5, range(24, 27))):
+        table[s, :len(pages)] = list(pages)
+    ring = [(x + 27) % size for x in range(size)]       # free: 27 to 39, and of the ended ones' pages what the books say wrongly
+    t = Tables(kept=[0, 0, 0, 0, 0, 48], new=[33, 0, 17, 0, 3, 2], held=[0, 12, 0, 12, 0, 3], table=table, ring=ring, state=[5, 30],
+               n_rows=55 + behind)
+    t.call()
+    want = t.check()
+    assert t.kvrp.kvrp_last_launch_count() == (2 if behind else 1)
+    head, count = want["state"]
+    assert count == 30 - 7 + 10 and want["status"] & step.BAD_LENGTH
+    free = {t.ring.tolist()[(head + i) % size] for i in range(count)}
+    served = t.table.cpu().numpy()
+    assert not free & {int(served[s, i]) for s in (0, 2, 4) for i in range(want["held"][s])}
+
+
 def test_tables_rows_behind_the_last_sequence():
     t = Tables(kept=[5, 40], new=[3, 2], held=[1, 3], table=[[2, 0, 0], [1, 0, 3]], ring=[9, 9, 9, 9], state=[0, 0], n_rows=600)
     t.call()

@@ -31,6 +31,14 @@ def test_tables_prefix_and_shortage():
     assert got["slots"][21:38] == [-1] * 17 and got["slots"][38] == -1
 
 
+def test_tables_pages_that_the_ring_has_no_place_for_are_not_counted():
+    # one sequence takes page 6, the other gives 0, 1, 2 back to a ring with two places: 2 is lost, and 6 is not free again
+    got = step.step_tables(kept=[0, 0], new=[1, 0], held=[0, 3], table=[[-1] * 3, [0, 1, 2]], ring=[8, 9, 7, 6], state=[3, 2],
+                           n_rows=1)
+    assert got["table"][0].tolist() == [6, -1, -1] and got["ring"] == [8, 0, 1, 6]
+    assert got["state"] == [0, 3] and got["status"] & step.BAD_LENGTH   # free: 8, 0, 1
+
+
 def test_drawn_token_is_exact_at_the_border():
     p = np.array([[0.25, 0.5, 0.25]], np.float32)
     draw = lambda u: step.verify_sequence(p, None, [0], [0.0], u)[1]  # noqa: E731
