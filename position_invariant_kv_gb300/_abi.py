@@ -226,6 +226,27 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+# Torch's types and Tensor.data_ptr, once a tensor has come along: the package works without torch too.
+_int32 = _int64 = _float32 = _bfloat16 = _data_ptr = None
+
+
+def _need_types(**arrays) -> None:
+    """Refuses tensors of other types; name=(array, its types' names).  An address has no type."""
+    global _int32, _int64, _float32, _bfloat16, _data_ptr
+    for name, (x, types) in arrays.items():
+        if x is None or isinstance(x, int):
+            continue
+        if str(x.dtype).rsplit(".", 1)[-1] not in types:
+            raise ValueError(f"{name}: a tensor of {' or '.join(types)} is needed, not of {x.dtype}")
+        if _data_ptr is None:
+            import torch
+            _int32, _int64, _float32, _bfloat16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
+            _data_ptr = torch.Tensor.data_ptr
+
+
+_I32, _I64, _F32 = ("int32", "uint32"), ("int64", "uint64"), ("float32",)
+
+
 def _find_current_stream():
     """torch's current stream as an address.  The raw getter costs 0.2 us a call where
     building a Stream object costs 3 us, as much as the rest of a call's marshalling."""
@@ -668,18 +689,54 @@ def kv_attend_shared_q8(q, seqs: Seqs, prefix: Prefix, *, n_q_heads: int, n_kv_h
 def kv_step_tables(kept_lens, new_rows, seqs: Seqs, *, held_pages, free_pages, free_state, held_out=None, free_state_out=None,
                    prefix: Optional[Prefix] = None, positions=None, slots=None, d_status=None, stream=None) -> None:
     """Row starts, lengths, block tables (written into the arrays of seqs), positions and slots of a step, from each
-    sequence's kept tokens and new rows.  held_out and free_state_out default to held_pages and free_state."""
+    sequence's kept tokens and new rows.  held_out and free_state_out default to held_pages and free_state.
+    Tensors are int32, slots int64."""
+    held_out = held_pages if held_out is None else held_out
+    free_state_out = free_state if free_state_out is None else free_state_out
+    ptr = _ptr   # the usual types at one comparison each: a call's marshalling takes as long as its kernel
+    try:
+        if (kept_lens.dtype is _int32 and new_rows.dtype is _int32 and held_pages.dtype is _int32 and held_out.dtype is _int32
+                and free_pages.dtype is _int32 and free_state.dtype is _int32 and free_state_out.dtype is _int32
+                and (positions is None or positions.dtype is _int32) and (slots is None or slots.dtype is _int64)):
+            ptr = _data_ptr
+    except AttributeError:   # an address
+        pass
+    if ptr is _ptr:
+        _need_types(kept_lens=(kept_lens, _I32), new_rows=(new_rows, _I32), held_pages=(held_pages, _I32),
+                    held_out=(held_out, _I32), free_pages=(free_pages, _I32), free_state=(free_state, _I32),
+                    free_state_out=(free_state_out, _I32), positions=(positions, _I32), slots=(slots, _I64))
     _check(lib().kv_step_tables(
-        _ptr(kept_lens), _ptr(new_rows), seqs.ref, prefix.ref if prefix is not None else None, _ptr(held_pages),
-        _ptr(held_pages if held_out is None else held_out), _ptr(free_pages), _ptr(free_state),
-        _ptr(free_state if free_state_out is None else free_state_out), _ptr(positions), _ptr(slots), _ptr(d_status),
-        _stream(stream)))
+        ptr(kept_lens), ptr(new_rows), seqs.ref, prefix.ref if prefix is not None else None, ptr(held_pages), ptr(held_out),
+        ptr(free_pages), ptr(free_state), ptr(free_state_out), _ptr(positions), _ptr(slots), _ptr(d_status), _stream(stream)))
+
+
+_PROBS = {"float32": KVRP_F32, "bfloat16": KVRP_BF16}
 
 
 def kv_verify_drafts(target, seqs: Seqs, *, vocab: int, tokens, u_accept, u_sample, out_tokens, draft=None,
-                     prob_type: int = KVRP_F32, accepted=None, kept_lens=None, target_stride: int = 0, draft_stride: int = 0,
-                     d_status=None, stream=None) -> None:
-    """Which drafted tokens stay against the target's probabilities, and the token after the last one that does."""
+                     prob_type: Optional[int] = None, accepted=None, kept_lens=None, target_stride: int = 0,
+                     draft_stride: int = 0, d_status=None, stream=None) -> None:
+    """Which drafted tokens stay against the target's probabilities, and the token after the last one that does.
+    Tensors: target and draft float32 or bfloat16, both the same, tokens and counts int32, random numbers float32.
+    prob_type is read off the tensors, and is needed only beside addresses (default KVRP_F32)."""
+    ptr = _ptr
+    try:
+        kind = target.dtype
+        if (tokens.dtype is _int32 and u_accept.dtype is _float32 and u_sample.dtype is _float32 and out_tokens.dtype is _int32
+                and (accepted is None or accepted.dtype is _int32) and (kept_lens is None or kept_lens.dtype is _int32)
+                and (draft is None or draft.dtype is kind) and (kind is _float32 or kind is _bfloat16)):
+            ptr, kind = _data_ptr, KVRP_F32 if kind is _float32 else KVRP_BF16
+    except AttributeError:   # an address
+        pass
+    if ptr is _ptr:
+        _need_types(target=(target, _PROBS), draft=(draft, _PROBS), tokens=(tokens, _I32), u_accept=(u_accept, _F32),
+                    u_sample=(u_sample, _F32), out_tokens=(out_tokens, _I32), accepted=(accepted, _I32), kept_lens=(kept_lens, _I32))
+        kinds = {_PROBS[str(x.dtype).rsplit(".", 1)[-1]] for x in (target, draft) if x is not None and not isinstance(x, int)}
+        if len(kinds) > 1:
+            raise ValueError("target and draft: tensors of one type are needed")
+        kind = kinds.pop() if kinds else KVRP_F32 if prob_type is None else prob_type
+    if prob_type is not None and prob_type != kind:
+        raise ValueError("prob_type is not that of target or draft")
     _check(lib().kv_verify_drafts(
-        _ptr(target), target_stride, _ptr(draft), draft_stride, prob_type, vocab, seqs.ref, _ptr(tokens), _ptr(u_accept),
-        _ptr(u_sample), _ptr(out_tokens), _ptr(accepted), _ptr(kept_lens), _ptr(d_status), _stream(stream)))
+        ptr(target), target_stride, _ptr(draft), draft_stride, kind, vocab, seqs.ref, ptr(tokens), ptr(u_accept), ptr(u_sample),
+        ptr(out_tokens), _ptr(accepted), _ptr(kept_lens), _ptr(d_status), _stream(stream)))

@@ -349,6 +349,18 @@ def test_verify_odd_values(draft):
     x.check()
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_reads_the_type_off_the_tensors(bf16, draft):
+    x = Verify([3, 2, 4], 777, bf16=bf16, draft=draft, seed=12)
+    x.call()
+    x.check()
+    del x.args["prob_type"]
+    x.out.fill_(-9)
+    x.kvrp.kv_verify_drafts(x.target, x.seqs, draft=x.draft, **x.args)
+    x.check()
+
+
 def test_verify_bad_lengths_keep_their_outputs():
     x = Verify([3, 4, 2, 2], 500, seed=3)
     x.lens = [9, 3, -1, 8]            # fewer tokens than rows; a negative length
