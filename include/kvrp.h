@@ -749,6 +749,20 @@ void kvrp_test_set_wait_limit(uint32_t cycles);
 void kvrp_test_set_each_limit(int64_t bytes);
 
 /*
+ * kvrp_test_even_units -- for tests of the host-side planning only; no CUDA call.  How
+ * kv_attend_shared_q8's pass over `tokens` shared tokens divides itself among at most
+ * most_cta blocks, for `pairs` (row, query head) pairs of each of `heads` KV heads:
+ *   out[0..4]  token tiles of a unit, parts of a unit (0: shares), units, a unit's cost, blocks;
+ * then for each of the n_units numbers in `units` the first block with tiles of that unit
+ * and how many have some; then for each of the n_blocks numbers in `blocks` where that block's
+ * share begins and ends, in the costs of all units, or, where units are cut into parts, the first
+ * tile of its part and the one behind the last.  out holds 5 + 2 n_units + 2 n_blocks numbers.
+ * Returns 0, or -1 on invalid arguments (numbers out of range among them).
+ */
+int32_t kvrp_test_even_units(int64_t pairs, int32_t heads, int32_t tokens, int32_t head_dim, int32_t most_cta,
+                             const int64_t* units, int32_t n_units, const int32_t* blocks, int32_t n_blocks, int64_t* out);
+
+/*
  * kvrp_test_attend_split -- for tests of the host-side planning only; no CUDA
  * call.  The work split kv_attend_relocated gives n_cta blocks for chunks of
  * these token counts and ranks (host arrays of n_chunks): the stage sequence

@@ -26,7 +26,8 @@ KVRP_BF16 = 1
 EXPORTED_SYMBOLS = (
     "kv_relocate_patch", "kv_relocate_patch_mrope", "kv_relocate_patch_mla", "kv_relocate_batch",
     "kv_relocate_batch_workspace_size", "kv_relocate_batch_noalloc", "kv_relocate_batch_mrope",
-    "kv_relocate_batch_mla", "kvrp_test_set_wait_limit", "kvrp_test_set_each_limit", "kvrp_test_attend_split", "kv_patch_form_workspace_size",
+    "kv_relocate_batch_mla", "kvrp_test_set_wait_limit", "kvrp_test_set_each_limit", "kvrp_test_attend_split",
+    "kvrp_test_even_units", "kv_patch_form_workspace_size",
     "kv_patch_form", "kv_patch_form_orbit", "kv_attend_relocated_workspace_size", "kv_attend_relocated",
     "kv_append", "kv_append_q8", "kv_pack_q8", "kv_attend_q8_workspace_size", "kv_attend_q8",
     "kv_attend_shared_q8_workspace_size", "kv_attend_shared_q8", "kv_step_tables", "kv_verify_drafts",
@@ -121,6 +122,9 @@ def _load_library():
     L.kvrp_test_attend_split.restype = C.c_int32
     L.kvrp_test_attend_split.argtypes = [C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int32, C.c_int32,
                                          C.c_int32, C.c_int32, C.c_int32, C.POINTER(C.c_int32)]
+    L.kvrp_test_even_units.restype = C.c_int32
+    L.kvrp_test_even_units.argtypes = [C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.POINTER(C.c_int64), C.c_int32,
+                                       C.POINTER(C.c_int32), C.c_int32, C.POINTER(C.c_int64)]
     L.kv_relocate_batch_noalloc.restype = st
     L.kv_relocate_batch_noalloc.argtypes = [
         C.POINTER(kvrp_chunk), C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_double, C.c_void_p,
@@ -465,6 +469,19 @@ def kvrp_test_attend_split(tokens, ranks, *, n_q_heads: int, n_kv_heads: int, he
     if cnt < 0:
         raise ValueError("kvrp_test_attend_split: invalid arguments")
     return [out[i] for i in range(cnt + 1)] if cnt > 0 else []
+
+
+def kvrp_test_even_units(pairs: int, heads: int, tokens: int, *, head_dim: int, most_cta: int, units=(), blocks=()):
+    """Testing hook: how kv_attend_shared_q8's pass over the shared tokens divides itself.  Returns
+    ((token tiles of a unit, parts, units, a unit's cost, blocks), [(first block, blocks) of each unit asked for],
+    [(begin, end) of each block asked for]); ValueError on invalid input."""
+    u, b = (C.c_int64 * max(1, len(units)))(*units), (C.c_int32 * max(1, len(blocks)))(*blocks)
+    out = (C.c_int64 * (5 + 2 * len(units) + 2 * len(blocks)))()
+    if lib().kvrp_test_even_units(int(pairs), int(heads), int(tokens), int(head_dim), int(most_cta), u, len(units), b, len(blocks), out):
+        raise ValueError("kvrp_test_even_units: invalid arguments")
+    x = list(out)
+    pairs_of = lambda y: list(zip(y[::2], y[1::2]))  # noqa: E731
+    return tuple(x[:5]), pairs_of(x[5:5 + 2 * len(units)]), pairs_of(x[5 + 2 * len(units):])
 
 
 def kv_relocate_batch_noalloc(chunks, *, n_layers: int, n_kv_heads: int, head_dim: int,

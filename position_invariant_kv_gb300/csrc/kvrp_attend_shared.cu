@@ -219,6 +219,31 @@ extern "C" {
 
 void kvrp_test_set_each_limit(int64_t bytes) { attend_q8::each_bytes = bytes < 0 ? attend_q8::kEachBytes : bytes; }
 
+int32_t kvrp_test_even_units(int64_t pairs, int32_t heads, int32_t tokens, int32_t head_dim, int32_t most_cta,
+                             const int64_t* units, int32_t n_units, const int32_t* blocks, int32_t n_blocks, int64_t* out) {
+  if (pairs < 0 || pairs >= 1 << 28 || heads <= 0 || heads > 4096 || tokens < 0 || tokens > q8::kMostTokens ||
+      (head_dim != 64 && head_dim != 128) || most_cta <= 0 || most_cta > attend_q8::kMaxCtas || !out || n_units < 0 ||
+      n_blocks < 0 || (n_units && !units) || (n_blocks && !blocks))
+    return -1;
+  const attend_q8::EvenUnits e(pairs, heads, tokens, head_dim, most_cta);
+  const int64_t head[] = {e.n_kv, e.parts, e.units, e.cost, e.n_cta};
+  out = std::copy(head, head + 5, out);
+  for (int i = 0; i < n_units; ++i, out += 2) {
+    if (units[i] < 0 || units[i] >= e.units) return -1;
+    int first = 0, n = 0;
+    e.find(units[i], first, n);
+    out[0] = first;
+    out[1] = n;
+  }
+  for (int i = 0; i < n_blocks; ++i, out += 2) {
+    if (blocks[i] < 0 || blocks[i] >= e.n_cta) return -1;
+    const int in_unit = e.parts ? blocks[i] % e.parts : 0;
+    out[0] = e.parts ? e.part_begin(in_unit) : e.share(blocks[i]);
+    out[1] = e.parts ? e.part_begin(in_unit + 1) : e.share(blocks[i] + 1);
+  }
+  return 0;
+}
+
 size_t kv_attend_shared_q8_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_rows,
                                           int32_t n_rows) {
   if (check_heads("kv_attend_shared_q8_workspace_size", n_q_heads, n_kv_heads, head_dim) != KVRP_OK || max_rows <= 0 ||
