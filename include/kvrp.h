@@ -624,7 +624,11 @@ typedef struct kvrp_prefix {
  * idle sequences and lse among it, is as in kv_attend_q8.  The workspace holds partial
  * results of both passes in fp32, 2 x (head_dim + 4) x 4 bytes for each (row, query
  * head) beside a fixed part: for long prompts kv_attend_q8, whose work is the same there,
- * needs less.
+ * needs less and is faster (28 / 4 heads x 128, 8 sequences of 200 rows over 16384 shared
+ * tokens: 359 us, this call 416).  So it is where sequences have more than 2 x floor(16 / group)
+ * rows each and long contexts of their own, which this call reads up to four times (32
+ * sequences of 8 rows, 1024 shared tokens, 16384 own: 268 us, this call 401).  Rows that two
+ * sequences of a row_start out of order both claim hold no meaning.
  */
 size_t kv_attend_shared_q8_workspace_size(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t max_rows,
                                           int32_t n_rows);
@@ -705,7 +709,7 @@ kvrp_status kv_step_tables(
  *                 is draft[r][i] = 1 at the drafted token and 0 elsewhere.
  *   tokens        device int32 [n_rows]; u_accept, u_sample   device fp32 [n_rows],
  *                 [n_seqs], in [0, 1).
- *   out_tokens    device int32 [n_rows]: from each sequence's first row on the drafts that
+ *   out_tokens    device int32 [n_rows], apart from all other arrays: from each sequence's first row on the drafts that
  *                 stay, the drawn token, then -1.
  *   accepted      optional device int32 [n_seqs]: how many drafts stay.
  *   kept_lens     optional device int32 [n_seqs]: seq_lens without the rows turned down

@@ -19,12 +19,15 @@
 // after another, and wait for it at their end alone; the join looks up what it needs before it waits.
 //
 // Measured, 28 / 4 heads x 128, beside kv_attend_q8, which reads the shared tokens for each sequence: 64 sequences,
-// 16384 shared tokens, 30 to 1500 own 46 us (134.6); 96, 100000 and 100 to 3000: 173 us, 802 TFLOP/s (1090); 16 of 5 rows,
-// 65536 and 40 to 2000: 120 us (423).  32 / 32 heads, 24 sequences, 4144 and 20 to 700: 40 us (105).  32 / 8 heads x 64,
-// 32 of 4 rows, 9008 and 10 to 900: 41.5 us (77.7).  The 46 us: 4 until the first pass knows its share, 5 until its
-// queries are laid out, 14 for 11 token tiles a CTA, 3 for its results, 12 for the own tokens behind them (26 MB:
-// latency), 6 for the join (20 MB of partial results from L2).  A token tile takes 1.2 us whatever the rows: 1850 of its
-// 2300 cycles are the softmax warps', a thread a row, and the products and conversions beside them take as long in turn.
+// 16384 shared tokens, 30 to 1500 own 49.8 us (135.7); 96, 100000 and 100 to 3000: 173 us, 800 TFLOP/s (1092); 16 of 5
+// rows, 65536 and 40 to 2000: 120 us (425).  32 / 32 heads, 24 sequences, 4144 and 20 to 700: 44.8 us (107).  32 / 8 heads
+// x 64, 32 of 4 rows, 9008 and 10 to 900: 42.7 us (78.2).  Of the 49.8 us, by time stamps: 4 until the first pass knows its
+// share, 5 until its queries are laid out, 14 for 11 token tiles a CTA, 3 for its results, 12 for the own tokens behind them
+// (26 MB: latency), 6 for the join (20 MB of partial results from L2); the rest lies between the launches.  A token tile
+// takes 1.2 us whatever the rows: 1850 of its 2300 cycles are the softmax warps', a thread a row, and the products and
+// conversions beside them take as long in turn.
+// Many rows a sequence: 8 sequences of 200 (900) rows over 16384 shared tokens 416 us (1735), where kv_attend_q8 takes 359
+// (1394): its work is the same, and it writes no partial results of two passes.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -162,7 +165,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // A sequence's rows go through the kernel for few rows in runs of as many as it takes, each reading the sequence's own
 // tokens again (from L2), if there are few runs; else through the kernel for many.
 // 28 / 4 heads x 128: 16 sequences of 5 rows over 16000 shared tokens and 60 to 600 own, three runs, 56.3 us against
-// 67.8 the other way; 32 of 8 rows over 300 to 3000 own, four runs, 100.2 against 99.2.
+// 67.8 the other way; 32 of 8 rows over 300 to 3000 own, four runs, 100.2 against 99.2.  The rule does not know how long the
+// own contexts are, which each run reads again, from memory where they do not fit L2: behind 1024 shared tokens, 16384 own
+// each, 16 sequences of 4 rows, two runs, take 111 us (kv_attend_q8 139), of 6, three, 157 (139), of 8, four, 205 (139); 32 of
+// 4 rows 205 (267), of 8 401 (268).
 constexpr int kMostRuns = 4;
 struct Runs {
   int rows;        // of a run
@@ -177,10 +183,10 @@ Runs runs(int64_t max_rows, int g) {
 
 // Up to this many bytes of shared keys and values, counted for each run of each sequence, and for up to two runs
 // in all, every sequence reads them for itself (again from L2): one pass and kv_attend_q8's combine instead of
-// three launches.  28 / 4 heads x 128, read by each and once: 8 sequences over 4000 shared tokens (31 MB) 18.9 and 21.0 us,
-// over 12000 (94 MB) 26.0 and 26.5, 16 over 8000 (125 MB) 28.6 and 24.2; 2 over 64000 (125 MB) 33.7 and 46.1, 1 over 160000
-// 50.6 and 84.8.  More runs a sequence than above do so too, if all that its table can hold is counted: 2 sequences of 6
-// rows over 16, 64 / 4 heads, 42.8 us the other way.
+// three launches.  28 / 4 heads x 128, read by each and once: 8 sequences over 4000 shared tokens (31 MB) 19.1 and 20.5 us,
+// over 12000 (94 MB) 26.2 and 25.9, 16 over 8000 (125 MB) 29.9 and 23.5, 8 over 16000 30.3 and 26.6; 2 over 64000 (125 MB)
+// 36.6 and 45.6, 1 over 160000 50.8 and 84.7, 4 over 160000 91.2 and 84.5.  More runs a sequence than above do so too, if all
+// that its table can hold is counted: 2 sequences of 6 rows over 16, 64 / 4 heads, 42.8 us the other way.
 constexpr int64_t kEachBytes = 96 << 20;
 constexpr int kEachRuns = 2, kMostEachRuns = 16;
 std::atomic<int64_t> each_bytes{kEachBytes};   // tests set it

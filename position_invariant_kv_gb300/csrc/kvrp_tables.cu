@@ -19,8 +19,10 @@
 // lengths, pages held and the ring's state on, which the first still reads.
 //
 // Measured: 64 sequences of 5 rows 5.2 us, of which a launch is half and the rest three dependent trips to
-// memory; 48 places, prompts of 37 to 6000 rows (47000) behind 1024 shared pages 7.9 us; 3000 sequences, half of them
-// beginning behind 1024 shared pages, a third ending, 42 us: six rounds of 512 in each of two launches.
+// memory; 48 places, prompts of 37 to 6000 rows (47000) behind 1024 shared pages 8.2 us; 3000 sequences, half of them
+// beginning behind 1024 shared pages, a third ending, 41 us: six rounds of 512 in each of two launches.  What comes back
+// is not counted when the launches are chosen: in a step of few rows one block moves it all, a third of 500 sequences
+// of 250 pages 46 us, of 3000 sequences 249 us (20 where none ends).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

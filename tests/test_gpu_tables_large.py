@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 LARGE = {
     "prefix": dict(n=1300, shared=110, rows=4, ctx=60), "rows": dict(n=2000, rows=16, ctx=60),
     "prefix_short": dict(n=1300, shared=110, rows=40, ctx=60, short=True), "rows_short": dict(n=1100, rows=50, ctx=40, short=True),
-    "exact": dict(n=1025, shared=130, rows=20, spare=0), "round": dict(n=1024, rows=30, ctx=300),
+    "exact": dict(n=1025, shared=130, rows=20, spare=0), "whole": dict(n=1024, rows=30, ctx=300),
 }
 
 
