@@ -1,5 +1,5 @@
 """kv_step_tables in two launches over more sequences than a block takes at a time (512): what is carried from one
-round to the next, by the blocks that fill the tables and again by the one that moves the state on.
+512 to the next, by the blocks that fill the tables and again by the one that moves the state on.
 
 Compared for equality with the oracle, as in test_gpu_step.py."""
 import numpy as np
